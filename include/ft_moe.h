@@ -275,6 +275,86 @@ ft_status ft_moe_forward_w4a4(const ft_moe_config *cfg, const ft_moe_banks *rout
 ft_status ft_moe_quantize_nvfp4(const void *src, int32_t src_dtype, int32_t rows, int32_t K, uint8_t *codes,
                                 uint8_t *scales, float *glob, void *stream);
 
+/* ---- expert products and their gradients ------------------------------------- */
+
+/* The parts of an expert layer with bf16 (unquantized) or 8-bit weights, for training it and for
+ * serving it: the two products of every expert over its own rows, their gradients, and the
+ * SwiGLU step between them. Rows are sorted by expert: expert e owns the rows
+ * [offs[e], offs[e + 1]) of x, y, dx and dy (int32 [E + 1] on the device, as ft_moe_align writes
+ * its expert_off with block = 1; a larger block makes its padding rows part of the batch). Sizes
+ * may be any, zero included. offs = NULL means one expert (E = 1) that owns all P rows: the plain
+ * product. Rows of no expert are neither read into a result nor written.
+ *   forward  y[p, n]     = sum_k x[p, k]  * w[e, n, k]
+ *   dgrad    dx[p, k]    = sum_n dy[p, n] * w[e, n, k]
+ *   wgrad    dw[e, n, k] = sum_p dy[p, n] * x[p, k]     (zero for an expert without rows)
+ * Sums are fp32, rounded once when stored. Every output depends on its own expert's rows alone:
+ * a value that is not finite stays inside the rows (or weights) that it belongs to. Results do
+ * not change from run to run.
+ *   x, dy, y, dx  device rows, ld_* elements apart (a multiple of 8), 16-byte aligned; inputs are
+ *                 bf16, outputs bf16 or fp32 (*_dtype)
+ *   w             device bf16 [E, N, K], contiguous, 16-byte aligned
+ *   dw            device bf16 or fp32 [E, N, K], contiguous; accumulate = 1 (fp32 only) adds to it
+ *   workspace     device, >= ft_moe_group_workspace_size bytes, 256-byte aligned; its first bytes
+ *                 hold the status word (ft_moe_read_status): FT_ERR_INVALID_ROUTING when offs
+ *                 decreases or leaves [0, P] (its rows are then clamped and the results undefined)
+ * N and K are multiples of 8, at most 65536; E <= 1024; P <= 2^25. P = 0 computes nothing (wgrad
+ * then clears dw, or leaves it when accumulating). Errors: FT_ERR_INVALID_ARG,
+ * FT_ERR_UNSUPPORTED (sizes outside these limits), FT_ERR_WORKSPACE, FT_ERR_CUDA. */
+ft_status ft_moe_group_workspace_size(int32_t E, int32_t P, int32_t N, int32_t K, size_t *bytes);
+ft_status ft_moe_group_gemm(const void *x, int64_t ld_x, const void *w, const int32_t *offs, int32_t E, int32_t P,
+                            int32_t N, int32_t K, void *y, int64_t ld_y, int32_t y_dtype, void *workspace,
+                            size_t workspace_bytes, void *stream);
+ft_status ft_moe_group_gemm_dgrad(const void *dy, int64_t ld_dy, const void *w, const int32_t *offs, int32_t E, int32_t P,
+                                  int32_t N, int32_t K, void *dx, int64_t ld_dx, int32_t dx_dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+ft_status ft_moe_group_gemm_wgrad(const void *dy, int64_t ld_dy, const void *x, int64_t ld_x, const int32_t *offs, int32_t E,
+                                  int32_t P, int32_t N, int32_t K, void *dw, int32_t dw_dtype, int32_t accumulate,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* The forward product with both operands in e4m3 (8-bit floating point), scaled in blocks of 128
+ * along K (x) and of 128 x 128 (w, the weight format of FT_FORMAT_FP8_BLOCK banks):
+ *   y[p, n] = sum_b x_scale[b, p] * w_scale[e, n / 128, b] * sum_{k in block b} x[p, k] * w[e, n, k]
+ * The inner sums run on the 8-bit tensor cores, the outer ones in fp32. Nothing is rounded to 16
+ * bits on the way. Rows, offs, workspace and errors as above.
+ *   x        device e4m3 codes, rows ld_x apart (a multiple of 16), 16-byte aligned
+ *   x_scale  device f32 [ceil(K / 128)][ld_xs], one scale per block and row, ld_xs >= P
+ *   w        device e4m3 codes [E, N, K], contiguous, 16-byte aligned
+ *   w_scale  device f32 [E, ceil(N / 128), ceil(K / 128)]
+ *   y        device bf16 or fp32 rows, ld_y >= N apart, 16-byte aligned
+ * K is a multiple of 16; N is any size. */
+ft_status ft_moe_group_gemm_fp8(const void *x, int64_t ld_x, const float *x_scale, int64_t ld_xs, const void *w,
+                                const float *w_scale, const int32_t *offs, int32_t E, int32_t P, int32_t N, int32_t K, void *y,
+                                int64_t ld_y, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* e4m3 codes and block scales of activation rows, as ft_moe_group_gemm_fp8 reads them: per 128
+ * values of a row scale = max(amax / 448, 2^-126) and code = e4m3(v * (1 / scale)), every step one
+ * correctly rounded fp32 operation, codes to nearest with ties to even. A block that holds an
+ * infinity or a NaN dequantizes to values that are all not finite.
+ *   src     device bf16 or fp32 rows, ld_src elements apart, 16-byte aligned rows
+ *   codes   device u8 rows, ld_codes apart (a multiple of 16), 16-byte aligned (out)
+ *   scales  device f32 [ceil(K / 128)][ld_scales], ld_scales >= rows (out)
+ * K is a multiple of 16. rows = 0 is a no-op. Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED,
+ * FT_ERR_CUDA. */
+ft_status ft_moe_quantize_fp8(const void *src, int32_t src_dtype, int64_t ld_src, int32_t rows, int32_t K, uint8_t *codes,
+                              int64_t ld_codes, float *scales, int64_t ld_scales, void *stream);
+
+/* SwiGLU between the two products, on bf16 rows gu = [gate (I), up (I)]:
+ *   h = w * silu(gate) * up        silu(g) = g * s,  s = 1 / (1 + e^-g)
+ * with one fp32 weight w per row (the routing weight) or w = NULL for 1, fp32 inside, bf16 out;
+ * the _quantize_fp8 form stores the fp32 h in 8 bits with ft_moe_quantize_fp8's rule instead (I a
+ * multiple of 16, 16-byte aligned rows). The backward form gives, from dh,
+ *   d gate = w * dh * up * s * (1 + gate * (1 - s)),  d up = w * dh * gate * s   (bf16, dgu)
+ *   d w    = sum_i dh * silu(gate) * up                                          (fp32, dw or NULL)
+ * The forward and backward forms take any I and any 2-byte aligned rows (16-byte aligned ones
+ * with I a multiple of 8 are faster). rows = 0 is a no-op. Outputs may not overlap inputs. Errors as
+ * above. */
+ft_status ft_moe_swiglu(const void *gu, int64_t ld_gu, const float *w, int32_t rows, int32_t I, void *h, int64_t ld_h,
+                        void *stream);
+ft_status ft_moe_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float *w, int32_t rows, int32_t I, uint8_t *codes,
+                                     int64_t ld_codes, float *scales, int64_t ld_scales, void *stream);
+ft_status ft_moe_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, const void *dh, int64_t ld_dh, int32_t rows,
+                                 int32_t I, void *dgu, int64_t ld_dgu, float *dw, void *stream);
+
 /* ---- test and debug exports ------------------------------------------------ */
 
 /* Expert-sorted, tile-padded slot order (the moe_align step named in "feat(qwen3_5_moe):
@@ -355,8 +435,8 @@ enum { FT_STAGE_ALIGN = 0, FT_STAGE_GATE_UP, FT_STAGE_SHARED_GATE_UP, FT_STAGE_D
  * itself after one forward call; events = NULL disarms it explicitly. */
 ft_status ft_moe_set_stage_events(void *const *events);
 
-/* Fault injection for tests of the error path, armed for the next ft_moe_forward call
- * on this thread that launches kernels (then disarmed). wait_limit_ns replaces the
+/* Fault injection for tests of the error path, armed for the next ft_moe_forward (or
+ * ft_moe_group_gemm*) call on this thread that launches kernels (then disarmed). wait_limit_ns replaces the
  * pipelined kernels' limit on every barrier wait (0 = the default, about two seconds;
  * otherwise 1 ms to 2 s); skip_producer = 1 makes the tensor-core (prefill) kernels issue
  * no copies, so that their consumers' bounded waits run out: each CTA then records

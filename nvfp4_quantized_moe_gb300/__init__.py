@@ -20,7 +20,9 @@ __all__ = [
     "FT_GU", "FT_GU_SCALE", "FT_GU_GLOBAL", "FT_DN", "FT_DN_SCALE", "FT_DN_GLOBAL",
     "FT_DTYPE_BF16", "FT_DTYPE_F32", "STATUS", "ft_moe_set_stage_events", "ft_moe_launch_count",
     "FT_NSTAGES", "STAGES", "ft_moe_debug_inject_stall", "ft_moe_workspace_size_w4a4", "ft_moe_forward_w4a4",
-    "ft_moe_quantize_nvfp4",
+    "ft_moe_quantize_nvfp4", "ft_moe_group_workspace_size", "ft_moe_group_gemm", "ft_moe_group_gemm_dgrad",
+    "ft_moe_group_gemm_wgrad", "ft_moe_group_gemm_fp8", "ft_moe_quantize_fp8", "ft_moe_swiglu",
+    "ft_moe_swiglu_quantize_fp8", "ft_moe_swiglu_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libftmoe.so")
@@ -37,7 +39,10 @@ BANK_NAMES = ("gate_up", "gate_up_scale", "gate_up_global", "down", "down_scale"
 EXPORTS = ("ft_moe_layout", "ft_moe_pack", "ft_moe_route", "ft_moe_route_gemm", "ft_moe_workspace_size",
            "ft_moe_forward", "ft_moe_align_workspace_size", "ft_moe_align", "ft_moe_dequant", "ft_moe_read_status",
            "ft_last_error", "ft_moe_set_stage_events", "ft_moe_launch_count", "ft_moe_align_static",
-           "ft_moe_debug_inject_stall", "ft_moe_workspace_size_w4a4", "ft_moe_forward_w4a4", "ft_moe_quantize_nvfp4")
+           "ft_moe_debug_inject_stall", "ft_moe_workspace_size_w4a4", "ft_moe_forward_w4a4", "ft_moe_quantize_nvfp4",
+           "ft_moe_group_workspace_size", "ft_moe_group_gemm", "ft_moe_group_gemm_dgrad", "ft_moe_group_gemm_wgrad",
+           "ft_moe_group_gemm_fp8", "ft_moe_quantize_fp8", "ft_moe_swiglu", "ft_moe_swiglu_quantize_fp8",
+           "ft_moe_swiglu_backward")
 FT_NSTAGES = 6
 STAGES = ("align", "gate_up", "shared_gate_up", "down", "shared_down", "combine")
 
@@ -89,7 +94,7 @@ def load():
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"libftmoe.so not built at {LIB_PATH}: run nvfp4_quantized_moe_gb300/build.py")
         L = ctypes.CDLL(LIB_PATH)
-        P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         sigs = {
             "ft_moe_layout": [P, I32, P],
             "ft_moe_pack": [P, I32, P, P, P],
@@ -106,6 +111,15 @@ def load():
             "ft_moe_workspace_size_w4a4": [P, I32, P],
             "ft_moe_forward_w4a4": [P, P, P, P, I32, P, P, P, I32, P, SZ, P],
             "ft_moe_quantize_nvfp4": [P, I32, I32, I32, P, P, P, P],
+            "ft_moe_group_workspace_size": [I32, I32, I32, I32, P],
+            "ft_moe_group_gemm": [P, I64, P, P, I32, I32, I32, I32, P, I64, I32, P, SZ, P],
+            "ft_moe_group_gemm_dgrad": [P, I64, P, P, I32, I32, I32, I32, P, I64, I32, P, SZ, P],
+            "ft_moe_group_gemm_wgrad": [P, I64, P, I64, P, I32, I32, I32, I32, P, I32, I32, P, SZ, P],
+            "ft_moe_group_gemm_fp8": [P, I64, P, I64, P, P, P, I32, I32, I32, I32, P, I64, I32, P, SZ, P],
+            "ft_moe_quantize_fp8": [P, I32, I64, I32, I32, P, I64, P, I64, P],
+            "ft_moe_swiglu": [P, I64, P, I32, I32, P, I64, P],
+            "ft_moe_swiglu_quantize_fp8": [P, I64, P, I32, I32, P, I64, P, I64, P],
+            "ft_moe_swiglu_backward": [P, I64, P, P, I64, I32, I32, P, I64, P, P],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -242,6 +256,136 @@ def ft_moe_quantize_nvfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.
     rows, K = src.shape
     _check(load().ft_moe_quantize_nvfp4(_ptr(src), dt, rows, K, _ptr(codes), _ptr(scales), _ptr(glob),
                                         _stream(stream, src)))
+
+
+def _rows(name, t, dtypes, cols=None, rows=None):
+    """Row stride of a 2-D tensor whose rows are contiguous; its type and shape are checked."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: expected shape ({'rows' if rows is None else rows}, "
+                         f"{'columns' if cols is None else cols}), got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _whole(name, t, dtypes, shape):
+    """A contiguous tensor of the given types and shape (or None, where it may be left out)."""
+    if t is None:
+        return
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {' or '.join(map(str, dtypes))} of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_OUT, _E4M3 = (torch.bfloat16, torch.float32), (torch.uint8, torch.float8_e4m3fn)
+_OUT_CODE = {torch.bfloat16: FT_DTYPE_BF16, torch.float32: FT_DTYPE_F32}
+
+
+def _group(w_shape, offs, workspace):
+    E, N, K = w_shape
+    if offs is None and E != 1:
+        raise ValueError("offs may be None for one expert only")
+    _whole("offs", offs, (torch.int32,), (E + 1,))
+    return E, N, K, workspace.numel() * workspace.element_size()
+
+
+def ft_moe_group_workspace_size(E: int, P: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load().ft_moe_group_workspace_size(E, P, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def ft_moe_group_gemm(x: torch.Tensor, w: torch.Tensor, offs, y: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """y[p] = w[e] . x[p] for the rows p of every expert e (w bf16 [E, N, K]; y bf16 or fp32)."""
+    E, N, K, nbytes = _group(w.shape, offs, workspace)
+    _whole("w", w, _BF16, (E, N, K))
+    ldx = _rows("x", x, _BF16, K)
+    ldy = _rows("y", y, _OUT, N, x.shape[0])
+    _check(load().ft_moe_group_gemm(_ptr(x), ldx, _ptr(w), _ptr(offs), E, x.shape[0], N, K, _ptr(y), ldy,
+                                    _OUT_CODE[y.dtype], _ptr(workspace), nbytes, _stream(stream, x)))
+
+
+def ft_moe_group_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offs, dx: torch.Tensor, workspace: torch.Tensor,
+                            stream=None):
+    """dx[p] = w[e]^T . dy[p]: the gradient of ft_moe_group_gemm's rows (dx bf16 or fp32)."""
+    E, N, K, nbytes = _group(w.shape, offs, workspace)
+    _whole("w", w, _BF16, (E, N, K))
+    lddy = _rows("dy", dy, _BF16, N)
+    lddx = _rows("dx", dx, _OUT, K, dy.shape[0])
+    _check(load().ft_moe_group_gemm_dgrad(_ptr(dy), lddy, _ptr(w), _ptr(offs), E, dy.shape[0], N, K, _ptr(dx), lddx,
+                                          _OUT_CODE[dx.dtype], _ptr(workspace), nbytes, _stream(stream, dy)))
+
+
+def ft_moe_group_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offs, dw: torch.Tensor, workspace: torch.Tensor,
+                            accumulate: bool = False, stream=None):
+    """dw[e] = sum of dy[p] x[p]^T over expert e's rows (dw bf16 or fp32 [E, N, K]); accumulate adds to an fp32 dw."""
+    E, N, K, nbytes = _group(dw.shape, offs, workspace)
+    _whole("dw", dw, _OUT, (E, N, K))
+    lddy = _rows("dy", dy, _BF16, N)
+    ldx = _rows("x", x, _BF16, K, dy.shape[0])
+    _check(load().ft_moe_group_gemm_wgrad(_ptr(dy), lddy, _ptr(x), ldx, _ptr(offs), E, dy.shape[0], N, K, _ptr(dw),
+                                          _OUT_CODE[dw.dtype], int(bool(accumulate)), _ptr(workspace), nbytes,
+                                          _stream(stream, dy)))
+
+
+def ft_moe_group_gemm_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, offs,
+                          y: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """ft_moe_group_gemm on e4m3 codes (uint8 or float8_e4m3fn) with fp32 scales: x_scale [ceil(K/128), P],
+    w_scale [E, ceil(N/128), ceil(K/128)]."""
+    E, N, K, nbytes = _group(w.shape, offs, workspace)
+    _whole("w", w, _E4M3, (E, N, K))
+    _whole("w_scale", w_scale, _F32, (E, -(-N // 128), -(-K // 128)))
+    ldx = _rows("x", x, _E4M3, K)
+    ldxs = _rows("x_scale", x_scale, _F32, x.shape[0], -(-K // 128))
+    ldy = _rows("y", y, _OUT, N, x.shape[0])
+    _check(load().ft_moe_group_gemm_fp8(_ptr(x), ldx, _ptr(x_scale), ldxs, _ptr(w), _ptr(w_scale), _ptr(offs), E,
+                                        x.shape[0], N, K, _ptr(y), ldy, _OUT_CODE[y.dtype], _ptr(workspace), nbytes,
+                                        _stream(stream, x)))
+
+
+def ft_moe_quantize_fp8(src: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """e4m3 codes [rows, K] and scales [ceil(K/128), rows] of bf16 or fp32 rows."""
+    lds = _rows("src", src, _OUT)
+    rows, K = src.shape
+    ldc = _rows("codes", codes, _E4M3, K, rows)
+    ldsc = _rows("scales", scales, _F32, rows, -(-K // 128))
+    _check(load().ft_moe_quantize_fp8(_ptr(src), _OUT_CODE[src.dtype], lds, rows, K, _ptr(codes), ldc, _ptr(scales),
+                                      ldsc, _stream(stream, src)))
+
+
+def ft_moe_swiglu(gu: torch.Tensor, w, h: torch.Tensor, stream=None):
+    """h = w * silu(gate) * up of rows gu = [gate, up] (w: one fp32 weight per row, or None)."""
+    ldh = _rows("h", h, _BF16)
+    rows, I = h.shape
+    ldgu = _rows("gu", gu, _BF16, 2 * I, rows)
+    _whole("w", w, _F32, (rows,))
+    _check(load().ft_moe_swiglu(_ptr(gu), ldgu, _ptr(w), rows, I, _ptr(h), ldh, _stream(stream, gu)))
+
+
+def ft_moe_swiglu_quantize_fp8(gu: torch.Tensor, w, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """ft_moe_swiglu stored as e4m3 codes [rows, I] and scales [ceil(I/128), rows]."""
+    ldc = _rows("codes", codes, _E4M3)
+    rows, I = codes.shape
+    ldgu = _rows("gu", gu, _BF16, 2 * I, rows)
+    ldsc = _rows("scales", scales, _F32, rows, -(-I // 128))
+    _whole("w", w, _F32, (rows,))
+    _check(load().ft_moe_swiglu_quantize_fp8(_ptr(gu), ldgu, _ptr(w), rows, I, _ptr(codes), ldc, _ptr(scales), ldsc,
+                                             _stream(stream, gu)))
+
+
+def ft_moe_swiglu_backward(gu: torch.Tensor, w, dh: torch.Tensor, dgu: torch.Tensor, dw=None, stream=None):
+    """Gradients of ft_moe_swiglu: dgu = [d gate, d up] and, where dw is given, the row weights'."""
+    lddh = _rows("dh", dh, _BF16)
+    rows, I = dh.shape
+    ldgu = _rows("gu", gu, _BF16, 2 * I, rows)
+    lddgu = _rows("dgu", dgu, _BF16, 2 * I, rows)
+    _whole("w", w, _F32, (rows,))
+    _whole("dw", dw, _F32, (rows,))
+    _check(load().ft_moe_swiglu_backward(_ptr(gu), ldgu, _ptr(w), _ptr(dh), lddh, rows, I, _ptr(dgu), lddgu, _ptr(dw),
+                                         _stream(stream, gu)))
 
 
 def ft_moe_align_workspace_size(T: int, k: int, E: int) -> int:

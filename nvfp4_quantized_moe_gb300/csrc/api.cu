@@ -30,6 +30,9 @@ void injected_stall(uint64_t *wait_ns, int *skip_producer)
     *skip_producer = g_stall_active ? g_stall_skip : 0;
 }
 
+StallScope::StallScope() { g_stall_active = g_stall_armed; }
+StallScope::~StallScope() { g_stall_armed = g_stall_active = false; }
+
 // Record the stage boundary event i, if timing is armed.
 static cudaError_t stage_mark(int i, cudaStream_t s)
 {

@@ -1,0 +1,263 @@
+// Row kernels around the grouped products: 8-bit quantization of activation rows, and the SwiGLU
+// step between an expert's two products (forward, forward stored in 8 bits, backward). All are
+// bound by memory: each value is read once and written once, sums and maxima stay in fp32.
+//
+//   quantize   scale = max(amax / 448, 2^-126) over 128 values of a row, code = e4m3(v * (1 / scale)),
+//              each step one correctly rounded fp32 operation, codes to nearest even
+//   SwiGLU     h = w * g * s * u with s = 1 / (1 + e^-g) and the row's weight w (or 1)
+//   backward   dg = w dh u s (1 + g (1 - s)),  du = w dh g s,  dw = sum dh g s u
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ftmoe_device.cuh"
+#include "ftmoe_internal.h"
+
+namespace ftmoe {
+
+namespace {
+
+__device__ __forceinline__ void unpack8(uint4 q, float (&v)[8])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8])
+{
+    return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+
+// 8 values of a row starting at `col` (aligned to 8 elements).
+template <bool F32>
+__device__ __forceinline__ void load8(const void *row, int col, float (&v)[8])
+{
+    if constexpr (F32) {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + col);
+        const float4 a = __ldg(p), b = __ldg(p + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        unpack8(ldg_nc_v4(static_cast<const uint16_t *>(row) + col), v);
+    }
+}
+
+// Four e4m3 codes, nearest even, saturating at 448; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// The 16 lanes of a half warp hold 8 values each of one 128-value block: returns its scale.
+// Magnitudes are compared as integers, so that a NaN (whose bits exceed infinity's) is the
+// maximum and reaches the scale: a block that holds a value that is not finite has no finite value.
+__device__ __forceinline__ float block_scale(const float (&v)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const float s = __fdiv_rn(__uint_as_float(m), 448.0f);
+    return s < 0x1p-126f ? 0x1p-126f : s;
+}
+
+__device__ __forceinline__ uint2 block_codes(const float (&v)[8], float scale)
+{
+    const float r = __frcp_rn(scale);
+    return make_uint2(e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
+}
+
+// s = 1 / (1 + e^-g): the fast exponential and division, a few 1e-7 relative, far below the
+// rounding of the stored results; e^-g = inf gives 0.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+constexpr int kActThreads = 256;
+constexpr int kRowsPerCta = kActThreads / 16;  // quantizing kernels: 16 lanes per row and block
+
+}  // namespace
+
+// blockIdx.x: 16 rows (so that the scales of a block are written side by side); blockIdx.y:
+// blocks of 128 columns.
+template <bool F32>
+__global__ void __launch_bounds__(kActThreads)
+    quantize_fp8_kernel(const void *__restrict__ src, int64_t ld, int rows, int K, uint8_t *__restrict__ codes,
+                        int64_t ld_codes, float *__restrict__ scales, int64_t ld_scales)
+{
+    pdl_enter();
+    const int row = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4), l = threadIdx.x & 15;
+    const int col = blockIdx.y * 128 + 8 * l;
+    const bool in = row < rows && col < K;
+    float v[8] = {};
+    if (in) load8<F32>(static_cast<const char *>(src) + (int64_t)row * ld * (F32 ? 4 : 2), col, v);
+    const float s = block_scale(v);
+    if (in) *reinterpret_cast<uint2 *>(codes + row * ld_codes + col) = block_codes(v, s);
+    if (row < rows && l == 0) scales[blockIdx.y * ld_scales + row] = s;
+}
+
+__global__ void __launch_bounds__(kActThreads)
+    swiglu_quantize_fp8_kernel(const uint16_t *__restrict__ gu, int64_t ld, const float *__restrict__ w, int rows, int I,
+                               uint8_t *__restrict__ codes, int64_t ld_codes, float *__restrict__ scales,
+                               int64_t ld_scales)
+{
+    pdl_enter();
+    const int row = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4), l = threadIdx.x & 15;
+    const int col = blockIdx.y * 128 + 8 * l;
+    const bool in = row < rows && col < I;
+    float h[8] = {};
+    if (in) {
+        float g[8], u[8];
+        load8<false>(gu + row * ld, col, g);
+        load8<false>(gu + row * ld + I, col, u);
+        const float f = w ? __ldg(w + row) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = f * (g[i] * sigmoid(g[i]) * u[i]);
+    }
+    const float s = block_scale(h);
+    if (in) *reinterpret_cast<uint2 *>(codes + row * ld_codes + col) = block_codes(h, s);
+    if (row < rows && l == 0) scales[blockIdx.y * ld_scales + row] = s;
+}
+
+// One warp per row. VEC: 8 columns per lane and step (everything 16-byte aligned), else one.
+template <bool VEC>
+__global__ void __launch_bounds__(kActThreads)
+    swiglu_kernel(const uint16_t *__restrict__ gu, int64_t ld, const float *__restrict__ w, int rows, int I,
+                  uint16_t *__restrict__ h, int64_t ld_h)
+{
+    pdl_enter();
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (kActThreads / 32);
+    for (int row = blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5); row < rows; row += warps) {
+        const uint16_t *gr = gu + row * ld, *ur = gr + I;
+        uint16_t *o = h + row * ld_h;
+        const float f = w ? __ldg(w + row) : 1.0f;
+        if constexpr (VEC) {
+            for (int c = 8 * lane; c < I; c += 256) {
+                float g[8], u[8];
+                load8<false>(gr, c, g);
+                load8<false>(ur, c, u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = f * (g[i] * sigmoid(g[i]) * u[i]);
+                *reinterpret_cast<uint4 *>(o + c) = pack8(g);
+            }
+        } else {
+            for (int c = lane; c < I; c += 32) {
+                const float g = __uint_as_float((uint32_t)__ldg(gr + c) << 16), u = __uint_as_float((uint32_t)__ldg(ur + c) << 16);
+                o[c] = __bfloat16_as_ushort(__float2bfloat16_rn(f * (g * sigmoid(g) * u)));
+            }
+        }
+    }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(kActThreads)
+    swiglu_backward_kernel(const uint16_t *__restrict__ gu, int64_t ld, const float *__restrict__ w,
+                           const uint16_t *__restrict__ dh, int64_t ld_dh, int rows, int I, uint16_t *__restrict__ dgu,
+                           int64_t ld_dgu, float *__restrict__ dw)
+{
+    pdl_enter();
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (kActThreads / 32);
+    for (int row = blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5); row < rows; row += warps) {
+        const uint16_t *gr = gu + row * ld, *ur = gr + I, *dr = dh + row * ld_dh;
+        uint16_t *og = dgu + row * ld_dgu, *ou = og + I;
+        const float f = w ? __ldg(w + row) : 1.0f;
+        float sum = 0.f;
+        auto one = [&](float g, float u, float d, float &dg, float &du) {
+            const float s = sigmoid(g), gs = g * s, fd = f * d;
+            dg = fd * u * (s * (1.0f + g * (1.0f - s)));
+            du = fd * gs;
+            sum = fmaf(d, gs * u, sum);
+        };
+        if constexpr (VEC) {
+            for (int c = 8 * lane; c < I; c += 256) {
+                float g[8], u[8], d[8];
+                load8<false>(gr, c, g);
+                load8<false>(ur, c, u);
+                load8<false>(dr, c, d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) one(g[i], u[i], d[i], g[i], u[i]);
+                *reinterpret_cast<uint4 *>(og + c) = pack8(g);
+                *reinterpret_cast<uint4 *>(ou + c) = pack8(u);
+            }
+        } else {
+            for (int c = lane; c < I; c += 32) {
+                float dg, du;
+                one(__uint_as_float((uint32_t)__ldg(gr + c) << 16), __uint_as_float((uint32_t)__ldg(ur + c) << 16),
+                    __uint_as_float((uint32_t)__ldg(dr + c) << 16), dg, du);
+                og[c] = __bfloat16_as_ushort(__float2bfloat16_rn(dg));
+                ou[c] = __bfloat16_as_ushort(__float2bfloat16_rn(du));
+            }
+        }
+        if (dw) {  // the same order of additions on every run
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            if (lane == 0) dw[row] = sum;
+        }
+    }
+}
+
+static bool vec_ok(const void *p, int64_t ld, int I)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && I % 8 == 0;
+}
+
+static int row_grid(int rows)
+{
+    const int per = kActThreads / 32, cap = sm_count() * 8;
+    const int g = (rows + per - 1) / per;
+    return g < cap ? g : cap;
+}
+
+cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows, int K, uint8_t *codes, int64_t ld_codes,
+                                float *scales, int64_t ld_scales, cudaStream_t s)
+{
+    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (K + 127) / 128);
+    if (f32) FT_LAUNCH(quantize_fp8_kernel<true>, grid, dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales, ld_scales);
+    else FT_LAUNCH(quantize_fp8_kernel<false>, grid, dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales, ld_scales);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float *w, int rows, int I, uint8_t *codes,
+                                       int64_t ld_codes, float *scales, int64_t ld_scales, cudaStream_t s)
+{
+    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (I + 127) / 128);
+    FT_LAUNCH(swiglu_quantize_fp8_kernel, grid, dim3(kActThreads), 0, s, static_cast<const uint16_t *>(gu), ld_gu, w, rows, I,
+              codes, ld_codes, scales, ld_scales);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu(const void *gu, int64_t ld_gu, const float *w, int rows, int I, void *h, int64_t ld_h,
+                          cudaStream_t s)
+{
+    auto kern = vec_ok(gu, ld_gu, I) && vec_ok(h, ld_h, I) ? swiglu_kernel<true> : swiglu_kernel<false>;
+    FT_LAUNCH(kern, dim3(row_grid(rows)), dim3(kActThreads), 0, s, static_cast<const uint16_t *>(gu), ld_gu, w, rows, I,
+              static_cast<uint16_t *>(h), ld_h);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, const void *dh, int64_t ld_dh, int rows,
+                                   int I, void *dgu, int64_t ld_dgu, float *dw, cudaStream_t s)
+{
+    auto kern = vec_ok(gu, ld_gu, I) && vec_ok(dh, ld_dh, I) && vec_ok(dgu, ld_dgu, I) ? swiglu_backward_kernel<true>
+                                                                                     : swiglu_backward_kernel<false>;
+    FT_LAUNCH(kern, dim3(row_grid(rows)), dim3(kActThreads), 0, s, static_cast<const uint16_t *>(gu), ld_gu, w,
+              static_cast<const uint16_t *>(dh), ld_dh, rows, I, static_cast<uint16_t *>(dgu), ld_dgu, dw);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace ftmoe

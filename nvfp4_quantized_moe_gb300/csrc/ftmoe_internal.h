@@ -156,6 +156,57 @@ cudaError_t launch_quant_nvfp4(const void *src, bool f32_src, int K, const int *
 bool make_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
 
+// The same for a stack of `mats` matrices mat_bytes apart (boxes lie inside one matrix; what a box
+// reaches beyond its matrix reads as zero).
+bool make_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
+                        uint64_t mats, uint64_t row_bytes, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_rows,
+                        CUtensorMapSwizzle swz);
+
+// A grouped bf16 product (group_gemm.cu). Forward uses x and w, dgrad dy and w, wgrad dy and x;
+// `out` is y, dx or dw. Pointers, strides and sizes are the entry points', already checked.
+enum { kGroupForward, kGroupDgrad, kGroupWgrad };
+struct GroupGemm {
+    int form;
+    const int *offs;             // [E + 1], or null (E = 1: all P rows)
+    int E, P, N, K;
+    const void *x, *w, *dy;
+    int64_t ld_x, ld_dy, ld_out; // elements
+    void *out;
+    int out_f32, accumulate;
+    int *status;
+};
+cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s);
+// A grouped e4m3 product with block scales (group_gemm_fp8.cu).
+struct GroupGemm8 {
+    const int *offs;
+    int E, P, N, K;
+    const void *x, *w;
+    const float *xs, *ws;
+    int64_t ld_x, ld_xs, ld_out;
+    void *out;
+    int out_f32;
+    int *status;
+};
+cudaError_t launch_group_gemm_fp8(const GroupGemm8 &g, cudaStream_t s);
+// expert_act.cu. Strides in elements; scales are [ceil(columns / 128)][ld_scales].
+cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows, int K, uint8_t *codes, int64_t ld_codes,
+                                float *scales, int64_t ld_scales, cudaStream_t s);
+cudaError_t launch_swiglu(const void *gu, int64_t ld_gu, const float *w, int rows, int I, void *h, int64_t ld_h,
+                          cudaStream_t s);
+cudaError_t launch_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float *w, int rows, int I, uint8_t *codes,
+                                       int64_t ld_codes, float *scales, int64_t ld_scales, cudaStream_t s);
+cudaError_t launch_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, const void *dh, int64_t ld_dh, int rows,
+                                   int I, void *dgu, int64_t ld_dgu, float *dw, cudaStream_t s);
+
+// While one exists, the fault injection armed on this thread applies to the launches made; its
+// end disarms it.
+struct StallScope {
+    StallScope();
+    ~StallScope();
+    StallScope(const StallScope &) = delete;
+    StallScope &operator=(const StallScope &) = delete;
+};
+
 int sm_count();
 
 // Launch with programmatic stream serialization: the kernel may be scheduled before its
@@ -175,6 +226,26 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+// The same in clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s,
+                           const Args &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 // launch_pdl inside a function returning cudaError_t: return the launch error, if any.
 #define FT_LAUNCH(...)                                                                                         \
