@@ -258,134 +258,159 @@ def ft_moe_quantize_nvfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.
                                         _stream(stream, src)))
 
 
-def _rows(name, t, dtypes, cols=None, rows=None):
-    """Row stride of a 2-D tensor whose rows are contiguous; its type and shape are checked."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: expected shape ({'rows' if rows is None else rows}, "
-                         f"{'columns' if cols is None else cols}), got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _whole(name, t, dtypes, shape):
-    """A contiguous tensor of the given types and shape (or None, where it may be left out)."""
-    if t is None:
-        return
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {' or '.join(map(str, dtypes))} of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-
-
-_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+# The expert products and row kernels are short calls: what follows checks what the C call cannot
+# see (types, shapes, layouts) and passes plain integers.
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _OUT, _E4M3 = (torch.bfloat16, torch.float32), (torch.uint8, torch.float8_e4m3fn)
 _OUT_CODE = {torch.bfloat16: FT_DTYPE_BF16, torch.float32: FT_DTYPE_F32}
 
 
-def _group(w_shape, offs, workspace):
-    E, N, K = w_shape
+def _refuse(name, t, dtypes, shape):
+    raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} of shape {tuple(shape)} with contiguous "
+                     f"elements, got {t.dtype} {tuple(t.shape)} (strides {t.stride()})")
+
+
+def _rows(name, t, dtypes, rows, cols):
+    """Row stride of a [rows, cols] tensor whose rows are contiguous."""
+    if t.dtype not in dtypes or t.shape != (rows, cols):
+        _refuse(name, t, dtypes, (rows, cols))
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        _refuse(name, t, dtypes, (rows, cols))
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _whole(name, t, dtypes, shape):
+    """Address of a contiguous tensor of the given shape (None, where it may be left out, stays None)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, dtypes, shape)
+    return t.data_ptr()
+
+
+def _dims(name, t, n):
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _stream_of(stream, t):
+    """The stream to launch on, as an integer: the one given, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
+
+
+def _offsets(offs, E):
     if offs is None and E != 1:
         raise ValueError("offs may be None for one expert only")
-    _whole("offs", offs, (torch.int32,), (E + 1,))
-    return E, N, K, workspace.numel() * workspace.element_size()
+    return _whole("offs", offs, _I32, (E + 1,))
 
 
 def ft_moe_group_workspace_size(E: int, P: int, N: int, K: int) -> int:
     n = ctypes.c_size_t()
-    _check(load().ft_moe_group_workspace_size(E, P, N, K, ctypes.byref(n)))
+    status = (_lib or load()).ft_moe_group_workspace_size(E, P, N, K, ctypes.byref(n))
+    if status:
+        _check(status)
     return n.value
 
 
 def ft_moe_group_gemm(x: torch.Tensor, w: torch.Tensor, offs, y: torch.Tensor, workspace: torch.Tensor, stream=None):
     """y[p] = w[e] . x[p] for the rows p of every expert e (w bf16 [E, N, K]; y bf16 or fp32)."""
-    E, N, K, nbytes = _group(w.shape, offs, workspace)
-    _whole("w", w, _BF16, (E, N, K))
-    ldx = _rows("x", x, _BF16, K)
-    ldy = _rows("y", y, _OUT, N, x.shape[0])
-    _check(load().ft_moe_group_gemm(_ptr(x), ldx, _ptr(w), _ptr(offs), E, x.shape[0], N, K, _ptr(y), ldy,
-                                    _OUT_CODE[y.dtype], _ptr(workspace), nbytes, _stream(stream, x)))
+    E, N, K = _dims("w", w, 3)
+    P = _dims("x", x, 2)[0]
+    status = (_lib or load()).ft_moe_group_gemm(
+        x.data_ptr(), _rows("x", x, _BF16, P, K), _whole("w", w, _BF16, (E, N, K)), _offsets(offs, E), E, P, N, K,
+        y.data_ptr(), _rows("y", y, _OUT, P, N), _OUT_CODE[y.dtype], workspace.data_ptr(), workspace.nbytes,
+        _stream_of(stream, x))
+    if status:
+        _check(status)
 
 
 def ft_moe_group_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offs, dx: torch.Tensor, workspace: torch.Tensor,
                             stream=None):
     """dx[p] = w[e]^T . dy[p]: the gradient of ft_moe_group_gemm's rows (dx bf16 or fp32)."""
-    E, N, K, nbytes = _group(w.shape, offs, workspace)
-    _whole("w", w, _BF16, (E, N, K))
-    lddy = _rows("dy", dy, _BF16, N)
-    lddx = _rows("dx", dx, _OUT, K, dy.shape[0])
-    _check(load().ft_moe_group_gemm_dgrad(_ptr(dy), lddy, _ptr(w), _ptr(offs), E, dy.shape[0], N, K, _ptr(dx), lddx,
-                                          _OUT_CODE[dx.dtype], _ptr(workspace), nbytes, _stream(stream, dy)))
+    E, N, K = _dims("w", w, 3)
+    P = _dims("dy", dy, 2)[0]
+    status = (_lib or load()).ft_moe_group_gemm_dgrad(
+        dy.data_ptr(), _rows("dy", dy, _BF16, P, N), _whole("w", w, _BF16, (E, N, K)), _offsets(offs, E), E, P, N, K,
+        dx.data_ptr(), _rows("dx", dx, _OUT, P, K), _OUT_CODE[dx.dtype], workspace.data_ptr(), workspace.nbytes,
+        _stream_of(stream, dy))
+    if status:
+        _check(status)
 
 
 def ft_moe_group_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offs, dw: torch.Tensor, workspace: torch.Tensor,
                             accumulate: bool = False, stream=None):
     """dw[e] = sum of dy[p] x[p]^T over expert e's rows (dw bf16 or fp32 [E, N, K]); accumulate adds to an fp32 dw."""
-    E, N, K, nbytes = _group(dw.shape, offs, workspace)
-    _whole("dw", dw, _OUT, (E, N, K))
-    lddy = _rows("dy", dy, _BF16, N)
-    ldx = _rows("x", x, _BF16, K, dy.shape[0])
-    _check(load().ft_moe_group_gemm_wgrad(_ptr(dy), lddy, _ptr(x), ldx, _ptr(offs), E, dy.shape[0], N, K, _ptr(dw),
-                                          _OUT_CODE[dw.dtype], int(bool(accumulate)), _ptr(workspace), nbytes,
-                                          _stream(stream, dy)))
+    E, N, K = _dims("dw", dw, 3)
+    P = _dims("dy", dy, 2)[0]
+    status = (_lib or load()).ft_moe_group_gemm_wgrad(
+        dy.data_ptr(), _rows("dy", dy, _BF16, P, N), x.data_ptr(), _rows("x", x, _BF16, P, K), _offsets(offs, E), E, P,
+        N, K, _whole("dw", dw, _OUT, (E, N, K)), _OUT_CODE[dw.dtype], 1 if accumulate else 0, workspace.data_ptr(),
+        workspace.nbytes, _stream_of(stream, dy))
+    if status:
+        _check(status)
 
 
 def ft_moe_group_gemm_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, offs,
                           y: torch.Tensor, workspace: torch.Tensor, stream=None):
     """ft_moe_group_gemm on e4m3 codes (uint8 or float8_e4m3fn) with fp32 scales: x_scale [ceil(K/128), P],
     w_scale [E, ceil(N/128), ceil(K/128)]."""
-    E, N, K, nbytes = _group(w.shape, offs, workspace)
-    _whole("w", w, _E4M3, (E, N, K))
-    _whole("w_scale", w_scale, _F32, (E, -(-N // 128), -(-K // 128)))
-    ldx = _rows("x", x, _E4M3, K)
-    ldxs = _rows("x_scale", x_scale, _F32, x.shape[0], -(-K // 128))
-    ldy = _rows("y", y, _OUT, N, x.shape[0])
-    _check(load().ft_moe_group_gemm_fp8(_ptr(x), ldx, _ptr(x_scale), ldxs, _ptr(w), _ptr(w_scale), _ptr(offs), E,
-                                        x.shape[0], N, K, _ptr(y), ldy, _OUT_CODE[y.dtype], _ptr(workspace), nbytes,
-                                        _stream(stream, x)))
+    E, N, K = _dims("w", w, 3)
+    P = _dims("x", x, 2)[0]
+    nb = (K + 127) // 128
+    status = (_lib or load()).ft_moe_group_gemm_fp8(
+        x.data_ptr(), _rows("x", x, _E4M3, P, K), x_scale.data_ptr(), _rows("x_scale", x_scale, _F32, nb, P),
+        _whole("w", w, _E4M3, (E, N, K)), _whole("w_scale", w_scale, _F32, (E, (N + 127) // 128, nb)),
+        _offsets(offs, E), E, P, N, K, y.data_ptr(), _rows("y", y, _OUT, P, N), _OUT_CODE[y.dtype],
+        workspace.data_ptr(), workspace.nbytes, _stream_of(stream, x))
+    if status:
+        _check(status)
 
 
 def ft_moe_quantize_fp8(src: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
     """e4m3 codes [rows, K] and scales [ceil(K/128), rows] of bf16 or fp32 rows."""
-    lds = _rows("src", src, _OUT)
-    rows, K = src.shape
-    ldc = _rows("codes", codes, _E4M3, K, rows)
-    ldsc = _rows("scales", scales, _F32, rows, -(-K // 128))
-    _check(load().ft_moe_quantize_fp8(_ptr(src), _OUT_CODE[src.dtype], lds, rows, K, _ptr(codes), ldc, _ptr(scales),
-                                      ldsc, _stream(stream, src)))
+    rows, K = _dims("src", src, 2)
+    status = (_lib or load()).ft_moe_quantize_fp8(
+        src.data_ptr(), _OUT_CODE.get(src.dtype, 0), _rows("src", src, _OUT, rows, K), rows, K, codes.data_ptr(),
+        _rows("codes", codes, _E4M3, rows, K), scales.data_ptr(),
+        _rows("scales", scales, _F32, (K + 127) // 128, rows), _stream_of(stream, src))
+    if status:
+        _check(status)
 
 
 def ft_moe_swiglu(gu: torch.Tensor, w, h: torch.Tensor, stream=None):
     """h = w * silu(gate) * up of rows gu = [gate, up] (w: one fp32 weight per row, or None)."""
-    ldh = _rows("h", h, _BF16)
-    rows, I = h.shape
-    ldgu = _rows("gu", gu, _BF16, 2 * I, rows)
-    _whole("w", w, _F32, (rows,))
-    _check(load().ft_moe_swiglu(_ptr(gu), ldgu, _ptr(w), rows, I, _ptr(h), ldh, _stream(stream, gu)))
+    rows, I = _dims("h", h, 2)
+    status = (_lib or load()).ft_moe_swiglu(
+        gu.data_ptr(), _rows("gu", gu, _BF16, rows, 2 * I), _whole("w", w, _F32, (rows,)), rows, I, h.data_ptr(),
+        _rows("h", h, _BF16, rows, I), _stream_of(stream, gu))
+    if status:
+        _check(status)
 
 
 def ft_moe_swiglu_quantize_fp8(gu: torch.Tensor, w, codes: torch.Tensor, scales: torch.Tensor, stream=None):
     """ft_moe_swiglu stored as e4m3 codes [rows, I] and scales [ceil(I/128), rows]."""
-    ldc = _rows("codes", codes, _E4M3)
-    rows, I = codes.shape
-    ldgu = _rows("gu", gu, _BF16, 2 * I, rows)
-    ldsc = _rows("scales", scales, _F32, rows, -(-I // 128))
-    _whole("w", w, _F32, (rows,))
-    _check(load().ft_moe_swiglu_quantize_fp8(_ptr(gu), ldgu, _ptr(w), rows, I, _ptr(codes), ldc, _ptr(scales), ldsc,
-                                             _stream(stream, gu)))
+    rows, I = _dims("codes", codes, 2)
+    status = (_lib or load()).ft_moe_swiglu_quantize_fp8(
+        gu.data_ptr(), _rows("gu", gu, _BF16, rows, 2 * I), _whole("w", w, _F32, (rows,)), rows, I, codes.data_ptr(),
+        _rows("codes", codes, _E4M3, rows, I), scales.data_ptr(),
+        _rows("scales", scales, _F32, (I + 127) // 128, rows), _stream_of(stream, gu))
+    if status:
+        _check(status)
 
 
 def ft_moe_swiglu_backward(gu: torch.Tensor, w, dh: torch.Tensor, dgu: torch.Tensor, dw=None, stream=None):
     """Gradients of ft_moe_swiglu: dgu = [d gate, d up] and, where dw is given, the row weights'."""
-    lddh = _rows("dh", dh, _BF16)
-    rows, I = dh.shape
-    ldgu = _rows("gu", gu, _BF16, 2 * I, rows)
-    lddgu = _rows("dgu", dgu, _BF16, 2 * I, rows)
-    _whole("w", w, _F32, (rows,))
-    _whole("dw", dw, _F32, (rows,))
-    _check(load().ft_moe_swiglu_backward(_ptr(gu), ldgu, _ptr(w), _ptr(dh), lddh, rows, I, _ptr(dgu), lddgu, _ptr(dw),
-                                         _stream(stream, gu)))
+    rows, I = _dims("dh", dh, 2)
+    status = (_lib or load()).ft_moe_swiglu_backward(
+        gu.data_ptr(), _rows("gu", gu, _BF16, rows, 2 * I), _whole("w", w, _F32, (rows,)), dh.data_ptr(),
+        _rows("dh", dh, _BF16, rows, I), rows, I, dgu.data_ptr(), _rows("dgu", dgu, _BF16, rows, 2 * I),
+        _whole("dw", dw, _F32, (rows,)), _stream_of(stream, gu))
+    if status:
+        _check(status)
 
 
 def ft_moe_align_workspace_size(T: int, k: int, E: int) -> int:

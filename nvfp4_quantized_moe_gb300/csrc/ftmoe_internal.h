@@ -247,6 +247,32 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
+// Clusters of `cluster` CTAs of a kernel that can run at once: the grid of a persistent kernel. A
+// die's SMs need not divide into whole clusters, and a cluster beyond this number would start
+// only when another one ends. Looked up once per kernel and device (the answer is the device's).
+template <typename... KArgs>
+int resident_clusters(void (*kern)(KArgs...), int cluster, int threads, size_t smem)
+{
+    static int cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count() / cluster;
+    if (cache[dev] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(cluster * sm_count());
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = sm_count() / cluster;
+        cache[dev] = n < sm_count() / cluster ? n : sm_count() / cluster;
+    }
+    return cache[dev];
+}
 // launch_pdl inside a function returning cudaError_t: return the launch error, if any.
 #define FT_LAUNCH(...)                                                                                         \
     do {                                                                                                       \

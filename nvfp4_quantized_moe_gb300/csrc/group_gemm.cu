@@ -3,14 +3,14 @@
 //
 //   forward  y[p, n]     = sum_k x[p, k]  w[e, n, k]      M axis n, N axis p, contraction k
 //   dgrad    dx[p, k]    = sum_n dy[p, n] w[e, n, k]      M axis k, N axis p, contraction n
-//   wgrad    dw[e, n, k] = sum_p dy[p, n] x[p, k]         M axis k, N axis n, contraction p
+//   wgrad    dw[e, n, k] = sum_p dy[p, n] x[p, k]         M axis n, N axis k, contraction p
 //
 // Operands go from global memory through TMA (128-byte swizzle) into a ring of shared-memory
 // stages of 64 contraction steps and from there into tcgen05.mma (kind::f16, bf16 operands,
-// fp32 accumulators in tensor memory). An operand whose contraction axis is not the contiguous
-// one (w in dgrad, both in wgrad) is read by the tensor cores as it lies (the descriptor's
-// transposed form), so nothing is transposed in memory. Sums are fp32 and rounded once, at the
-// store.
+// fp32 accumulators in tensor memory, two of them so that one is stored while the next fills).
+// An operand whose contraction axis is not the contiguous one (w in dgrad, both in wgrad) is read
+// by the tensor cores as it lies (the descriptor's transposed form), so nothing is transposed in
+// memory. Sums are fp32 and rounded once, at the store.
 #include <cuda_bf16.h>
 
 #include "group_gemm.cuh"
@@ -21,18 +21,28 @@ namespace {
 
 using namespace grp;
 
-constexpr int kThreadsG = 256;  // warps: 0 TMA, 1 MMA, 2 tail rows (wgrad), 3 idle, 4..7 epilogue
+constexpr int kThreadsG = 384;  // warps: 0 TMA, 1 MMA, 2 tail rows (wgrad), 3 idle, 4..11 epilogue
 constexpr int kStep = 64;       // contraction steps per stage
-constexpr int kMaxStages = 12;
+// Long sums into fp32 outputs are cut into parts of this many stages, added in registers: the
+// tensor cores truncate where an fp32 addition rounds, so that the error of one long
+// accumulation grows with its length (5e-6 relative over 8192 steps, against 2e-7 for sums in
+// parts of 512). A bf16 output rounds 300 times coarser and keeps one accumulation.
+constexpr int kPartStages = 8;
 
-template <int CG, int BN>
+// Tile variants. CG: CTAs per tile of the M axis (a pair shares its B operand and halves what
+// each SM must load per multiplication); BN: largest extent along the N axis.
+template <int CG, int BN, bool WG>
 struct Ring {
     static constexpr int b_bytes = BN / CG * kChunkBytes;
     static constexpr int stage = kABytes + b_bytes;
-    static constexpr int stages = (200 * 1024) / stage < kMaxStages ? (200 * 1024) / stage : kMaxStages;
     // rows of one TMA box of a row-major B operand: short boxes, so that a short tile loads no
     // more rows than it has (to within a box)
     static constexpr int box_rows = BN <= 32 ? 16 : 32;
+    // wgrad's output tiles on their way to TMA: two of 32 rows x 128 bytes per epilogue warp;
+    // the smallest tiles: the partial sums of a split contraction
+    static constexpr int extra = WG ? 8 * 2 * 4096 : BN <= 32 ? BN * kTileM * 4 : 0;
+    static constexpr int fit = (216 * 1024 - extra) / stage;
+    static constexpr int stages = fit < 10 ? fit : 10;
 };
 
 struct GroupParams {
@@ -41,10 +51,10 @@ struct GroupParams {
     int M;                // size of the M axis
     int N;                // wgrad: size of the N axis
     int R;                // forward, dgrad: contraction length
-    void *out;            // forward, dgrad: [P][ld]; wgrad: [E][N][M]
+    void *out;            // forward, dgrad: [P][ld]
     int64_t ld;
-    int f32;              // out is fp32 (else bf16)
-    int accumulate;       // wgrad, fp32: add to what out holds
+    int accumulate;       // wgrad, fp32: add to what dw holds
+    int split;            // CTAs (one cluster) that share a unit's contraction
     int *status;
     uint64_t wait_ns;
     int skip_producer;
@@ -72,10 +82,41 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
     }
 }
 
+// W consecutive 32-bit columns of this thread's TMEM lane.
+template <int W>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[W])
+{
+    if constexpr (W == 32) tc::ld32(addr, v);
+    else tc::ld16(addr, v);
+}
+
+// TMA store of a 128-byte x 32-row tile (128-byte swizzle) of a stack of matrices, or its addition.
+__device__ __forceinline__ void store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2, bool add)
+{
+    if (add)
+        asm volatile(
+            "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                reinterpret_cast<uint64_t>(map)),
+            "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
 // One unit of work: a 128 x CG by (up to) BN tile of the output.
 struct Unit {
     int e, m0;        // expert, first M index of this CTA
-    int col0, cols;   // N axis: first index and count (rows p, or columns n of wgrad)
+    int col0, cols;   // N axis: first index and count (rows p, or columns k of wgrad)
     int half;         // N indices this CTA loads (all, or its half of a pair's)
     int r0, R;        // contraction range
 };
@@ -83,42 +124,50 @@ struct Unit {
 }  // namespace
 
 // WG: the wgrad form (both operands transposed, ragged contraction); A_MN: A transposed.
-template <int CG, int BN, bool A_MN, bool WG>
+template <int CG, int BN, bool A_MN, bool WG, bool F32>
 __global__ void __launch_bounds__(kThreadsG, 1)
     group_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ GroupParams p)
+                      const __grid_constant__ CUtensorMap map_c, const __grid_constant__ GroupParams p)
 {
     static_assert(!WG || A_MN, "wgrad reads both operands transposed");
-    using T = Ring<CG, BN>;
+    using T = Ring<CG, BN, WG>;
     constexpr int S = T::stages;
-    constexpr int kGran = WG ? 64 : 16;  // N indices per CTA come in multiples of this
+    constexpr int kGran = WG ? 64 : 16;        // N indices per CTA come in multiples of this
+    constexpr bool kSplit = CG == 1 && BN <= 32;
+    constexpr int HC = BN / 2;                 // columns of one half's epilogue warps
+    constexpr int W = HC < 32 ? HC : 32;       // columns per tensor-memory load
     pdl_enter();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * T::stage);
-    uint64_t *empty = full + S, *tail = empty + S, *acc_full = tail + S, *acc_empty = acc_full + 2;
+    unsigned char *extra = smem + S * T::stage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(extra + T::extra);
+    uint64_t *empty = full + S, *tail = empty + S, *peer_tail = tail + S, *acc_full = peer_tail + S,
+             *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = kSplit ? p.split : 1;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const bool leader = rank == 0;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(full + i, CG);   // each CTA's producer (or tail warp)
-            mbar_init(empty + i, 1);   // the MMA commit
-            mbar_init(tail + i, 1);
+            mbar_init(full + i, 1);       // the leader's producer (or tail warp), for both CTAs of a pair
+            mbar_init(empty + i, 1);      // the MMA commit
+            mbar_init(tail + i, 1);       // wgrad: this CTA's copies of a stage that has tail rows
+            mbar_init(peer_tail + i, 1);  // wgrad, leader: the other CTA's tail rows are zeroed
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4 * CG);  // every epilogue warp
+            mbar_init(acc_empty + i, 8 * CG);  // every epilogue warp
         }
         *abort_flag = 0;
         fence_mbar_init();
         tc::prefetch_map(&map_a);
         tc::prefetch_map(&map_b);
+        if (WG) tc::prefetch_map(&map_c);
     }
     if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
     const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles, sh_flag);
@@ -132,7 +181,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const int m_tiles = (p.M + kTileM * CG - 1) / (kTileM * CG);
     const int n_tiles = (p.N + BN - 1) / BN;  // wgrad
     const int units = WG ? p.E * n_tiles * m_tiles : sh_tiles[p.E] * m_tiles;
-    const int u0 = blockIdx.x / CG, du = gridDim.x / CG;
+    const int u0 = blockIdx.x / (CG * split), du = gridDim.x / (CG * split);
+    const int part = kSplit ? (int)(blockIdx.x % split) : 0;
     auto unit_of = [&](int u) {
         Unit r;
         const int t = u / m_tiles;
@@ -154,6 +204,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         r.half = ((r.cols + CG - 1) / CG + kGran - 1) / kGran * kGran;
         return r;
     };
+    // this CTA's stages [first, last) of a contraction of R steps
+    auto first_stage = [&](int R) { return kSplit ? (R + kStep - 1) / kStep * part / split : 0; };
+    auto last_stage = [&](int R) {
+        const int nb = (R + kStep - 1) / kStep;
+        return kSplit ? nb * (part + 1) / split : nb;
+    };
     bool dead = false;
 
     if (warp == 0) {
@@ -163,11 +219,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             uint32_t ph = 1;
             for (int u = u0; u < units && !dead; u += du) {
                 const Unit x = unit_of(u);
-                const int nb = (x.R + kStep - 1) / kStep;
+                const int nb = last_stage(x.R);
                 const int boxes = WG ? x.half / 64 : (x.half + T::box_rows - 1) / T::box_rows;
                 const uint32_t bytes = kABytes + boxes * (WG ? 64 * kChunkBytes : T::box_rows * kChunkBytes);
-                for (int b = 0; b < nb; ++b, ++it) {
-                    if (!mbar_wait_timed(empty + s, ph, abort_flag, wl)) { dead = true; break; }
+                for (int b = first_stage(x.R); b < nb; ++b, ++it) {
+                    if (!wait_cluster(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
                     const int k0 = b * kStep;
                     uint32_t bar;
@@ -175,9 +231,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                         bar = smem_u32(tail + s);
                         mbar_arrive_expect_tx(tail + s, bytes);
                     } else {
+                        // the leader expects both CTAs' bytes (equally many); the other's may land first
                         bar = CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
-                        if (CG == 2) arrive_expect_tx_cluster(bar, bytes);
-                        else mbar_arrive_expect_tx(full + s, bytes);
+                        if (leader) mbar_arrive_expect_tx(full + s, CG * bytes);
                     }
                     if (WG) {
                         load_2d<CG>(sa, &map_a, x.m0, x.r0 + k0, bar);
@@ -208,34 +264,36 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0 && leader) {
-            int s = 0, uc = 0;
+            int s = 0, ac = 0;
             uint32_t ph = 0;
             for (int u = u0; u < units && !dead; u += du) {
                 const Unit x = unit_of(u);
-                if (WG && x.R == 0) continue;  // nothing to add up: the epilogue writes zeros
-                const int nb = (x.R + kStep - 1) / kStep;
-                if (!wait_cluster(acc_empty + (uc & 1), ((uc >> 1) & 1) ^ 1, abort_flag, wl)) { dead = true; break; }
-                tc::fence_after_sync();
-                const uint32_t acc = tmem + (uint32_t)(uc & 1) * BN;
+                const int b0 = first_stage(x.R), nb = last_stage(x.R);
                 const uint32_t idesc = idesc_bf16(kTileM * CG, x.half * CG, A_MN, WG);
-                for (int b = 0; b < nb; ++b) {
+                // (an expert without rows has no stages: the epilogue writes zeros on its own)
+                for (int b = b0; b < nb; ++b) {
+                    const bool starts = F32 ? (b - b0) % kPartStages == 0 : b == b0;
+                    const bool ends = b == nb - 1 || (F32 && (b - b0) % kPartStages == kPartStages - 1);
+                    if (starts && !wait_cluster(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) { dead = true; break; }
                     if (!wait_cluster(full + s, ph, abort_flag, wl)) { dead = true; break; }
                     tc::fence_after_sync();
-                    const uint32_t a0 = smem_u32(smem + s * T::stage), b0 = a0 + kABytes;
+                    const uint32_t acc = tmem + (uint32_t)(ac & 1) * BN;
+                    const uint32_t a0 = smem_u32(smem + s * T::stage), bb = a0 + kABytes;
                     const int k16 = min(4, (x.R - b * kStep + 15) / 16);  // beyond the contraction's end: not read
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (j >= k16) break;
                         const uint64_t ad = A_MN ? sw128_desc_mn(a0 + 2048 * j) : tc::sw128_desc(a0 + 32 * j);
-                        const uint64_t bd = WG ? sw128_desc_mn(b0 + 2048 * j) : tc::sw128_desc(b0 + 32 * j);
-                        mma_bf16<CG>(acc, ad, bd, idesc, (b | j) != 0);
+                        const uint64_t bd = WG ? sw128_desc_mn(bb + 2048 * j) : tc::sw128_desc(bb + 32 * j);
+                        mma_bf16<CG>(acc, ad, bd, idesc, !starts || j != 0);
                     }
                     commit<CG>(empty + s);
+                    if (ends) {
+                        commit<CG>(acc_full + (ac & 1));
+                        ++ac;
+                    }
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
-                if (dead) break;
-                commit<CG>(acc_full + (uc & 1));
-                ++uc;
             }
             if (dead) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
         }
@@ -252,7 +310,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             if (nb == 0) continue;
             s = (s + nb - 1) % S;  // the unit's last stage
             if (x.R & 15) {
-                if (!warp_wait(tail + s, (phases >> s) & 1, abort_flag, wl)) { dead = true; break; }
+                const uint32_t parity = (phases >> s) & 1;
+                if (!warp_wait(tail + s, parity, abort_flag, wl)) { dead = true; break; }
                 phases ^= 1u << s;
                 const int first = x.R - (nb - 1) * kStep, rows = 16 - (first & 15);
                 unsigned char *sa = smem + s * T::stage;
@@ -264,9 +323,14 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 }
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2) arrive_cluster(map_rank(full + s, 0));
-                    else mbar_arrive(full + s);
+                if (!leader) {
+                    if (lane == 0) arrive_cluster(map_rank(peer_tail + s, 0));
+                } else {
+                    if (CG == 2) {
+                        const bool ok = wait_cluster(peer_tail + s, parity, abort_flag, wl);
+                        if (!__all_sync(0xFFFFFFFFu, ok)) { dead = true; break; }
+                    }
+                    if (lane == 0) mbar_arrive(full + s);
                 }
             }
             if (++s == S) s = 0;
@@ -274,61 +338,153 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ epilogue
-        // thread = TMEM lane = M index; the N indices are the columns
-        const int q = warp & 3;
-        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16);
-        const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : smem_u32(acc_empty);
-        int uc = 0;
+        // thread = TMEM lane = M index; the warp takes columns [h * HC, h * HC + HC) of the tile
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
+        const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : 0;
+        unsigned char *stage_out = extra + (warp - 4) * 2 * 4096;  // wgrad: this warp's two tiles
+        int ac = 0, so = 0;
         for (int u = u0; u < units && !dead; u += du) {
             const Unit x = unit_of(u);
-            const bool none = WG && x.R == 0;
-            if (none && p.accumulate) continue;
-            if (!none) {
-                if (!warp_wait(acc_full + (uc & 1), (uc >> 1) & 1, abort_flag, wl)) { dead = true; break; }
-                tc::fence_after_sync();
-            }
+            const int nb = last_stage(x.R) - first_stage(x.R);
+            const int parts = F32 ? (nb + kPartStages - 1) / kPartStages : nb > 0;
+            if (WG && parts == 0 && p.accumulate) continue;
+            const int mine = min(max(x.cols - h * HC, 0), HC);  // columns of this half in use
             const int m = x.m0 + 32 * q + lane;
-            const int64_t first = WG ? (int64_t)x.e * p.N + x.col0 : x.col0;
-            for (int c0 = 0; c0 < x.cols; c0 += 32) {
-                uint32_t v[32];
-                if (none) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                } else {
-                    tc::ld32(lane_addr + (uint32_t)(uc & 1) * BN + c0, v);
-                    tc::wait_ld();
-                    if (c0 + 32 >= x.cols) {  // read out: the next unit's MMAs may start
-                        tc::fence_before_sync();
+
+            // W columns at offset c of this half, as sums, to where they go
+            auto emit = [&](int c, const float (&v)[W]) {
+                if constexpr (WG) {
+                    // lane = row n of dw, columns k: one row of 128 bytes per lane, its 16-byte
+                    // pieces swizzled as the TMA store expects them (and free of bank conflicts)
+                    constexpr int per = F32 ? 32 : 64;  // columns of one 128-byte row
+                    unsigned char *tile = stage_out + (so & 1) * 4096;
+                    if (c % per == 0) {
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         __syncwarp();
-                        if (lane == 0) arrive_cluster(empty_bar + 8 * (uc & 1));
+                    }
+#pragma unroll
+                    for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+                        uint4 o;
+                        if constexpr (F32)
+                            o = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                           __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                        else
+                            o = make_uint4(bf16x2(v[8 * i], v[8 * i + 1]), bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                           bf16x2(v[8 * i + 4], v[8 * i + 5]), bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                        const int piece = i + (F32 ? 0 : (c % per) / 8);
+                        *reinterpret_cast<uint4 *>(tile + lane * 128 + ((piece ^ (lane & 7)) << 4)) = o;
+                    }
+                    if (c % per == per - W) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        const int k = x.col0 + h * HC + c - c % per, n = x.m0 + 32 * q;
+                        if (lane == 0 && k < p.N && n < p.M) store_3d(&map_c, tile, k, n, x.e, F32 && p.accumulate);
+                        ++so;
+                    }
+                } else if (kSplit && split > 1) {
+                    float *red = reinterpret_cast<float *>(extra);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) red[(h * HC + c + j) * kTileM + 32 * q + lane] = v[j];
+                } else if constexpr (F32) {
+                    const int n = m < p.M ? mine - c : 0;
+                    float *o = static_cast<float *>(p.out) + ((int64_t)x.col0 + h * HC + c) * p.ld + m;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) {
+                        if (j < n) *o = v[j];
+                        o += p.ld;
+                    }
+                } else {
+                    // two rows per store: neighbouring lanes trade one value each, so that a lane
+                    // holds two neighbouring columns m of one row (M is even)
+                    const int odd = lane & 1, n = m < p.M ? mine - c - odd : 0;
+                    uint16_t *o = static_cast<uint16_t *>(p.out) + ((int64_t)x.col0 + h * HC + c + odd) * p.ld + (m - odd);
+#pragma unroll
+                    for (int j = 0; j < W; j += 2) {
+                        const uint32_t a = bf16x2(v[j], v[j + 1]), b = __shfl_xor_sync(0xFFFFFFFFu, a, 1);
+                        if (j < n) *reinterpret_cast<uint32_t *>(o) = __byte_perm(a, b, odd ? 0x3276 : 0x5410);
+                        o += 2 * p.ld;
                     }
                 }
-                const int n = m < p.M ? min(32, x.cols - c0) : 0;
-                if (p.f32) {
-                    float *o = static_cast<float *>(p.out) + (first + c0) * p.ld + m;
+            };
+            float sum[F32 ? HC : 1];  // fp32 outputs: the parts' running sums
+            for (int t = 0; t < parts; ++t, ++ac) {
+                if (!warp_wait(acc_full + (ac & 1), (ac >> 1) & 1, abort_flag, wl)) { dead = true; break; }
+                tc::fence_after_sync();
+                const uint32_t addr = lane_addr + (uint32_t)(ac & 1) * BN;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < n) {
-                            float a = __uint_as_float(v[j]);
-                            if (WG && p.accumulate) a += o[j * p.ld];
-                            o[j * p.ld] = a;
-                        }
-                } else {
-                    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (first + c0) * p.ld + m;
+                for (int c = 0; c < HC; c += W) {
+                    if (c >= mine) break;
+                    uint32_t v[W];
+                    tmem_ld<W>(addr + c, v);
+                    tc::wait_ld();
+                    if constexpr (F32) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < n) o[j * p.ld] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                        for (int j = 0; j < W; ++j) sum[c + j] = t ? sum[c + j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+                    } else {
+                        float f[W];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) f[j] = __uint_as_float(v[j]);
+                        emit(c, f);
+                    }
                 }
+                tc::fence_before_sync();
                 __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) arrive_cluster_relaxed(empty_bar + 8 * (ac & 1));
+                    else mbar_arrive(acc_empty + (ac & 1));
+                }
             }
-            if (!none) ++uc;
+            if (dead) break;
+            if (F32 || parts == 0) {
+#pragma unroll
+                for (int c = 0; c < HC; c += W) {
+                    if (c >= mine) break;
+                    float f[W];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) f[j] = F32 && parts ? sum[F32 ? c + j : 0] : 0.f;
+                    emit(c, f);
+                }
+            }
+            if (WG && !F32 && mine % 64 && mine % 64 <= 32) {  // a half-filled last tile
+                fence_proxy_async_smem();
+                __syncwarp();
+                const int k = x.col0 + h * HC + mine / 64 * 64, n = x.m0 + 32 * q;
+                if (lane == 0 && n < p.M) store_3d(&map_c, stage_out + (so & 1) * 4096, k, n, x.e, false);
+                ++so;
+            }
         }
+        if (WG && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     }
 
-    // wind down; a pair leaves together (its MMAs and barriers reach into both CTAs)
+    // wind down; a cluster leaves together (its MMAs, barriers and sums reach into all its CTAs)
     tc::fence_before_sync();
     __syncthreads();
+    if constexpr (kSplit) {
+        if (split > 1) {  // one unit per cluster: add its CTAs' sums, always in the same order
+            cluster_sync();
+            if (u0 < units) {
+                const Unit x = unit_of(u0);
+                const float *red = reinterpret_cast<const float *>(extra);
+                for (int i = threadIdx.x + kThreadsG * part; i < x.cols * kTileM; i += kThreadsG * split) {
+                    float a = 0.f;
+                    for (int r = 0; r < split; ++r) {
+                        float v;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_rank(red + i, r)) : "memory");
+                        a += v;
+                    }
+                    const int m = x.m0 + i % kTileM;
+                    const int64_t at = (int64_t)(x.col0 + i / kTileM) * p.ld + m;
+                    if (m < p.M) {
+                        if constexpr (F32) static_cast<float *>(p.out)[at] = a;
+                        else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(a);
+                    }
+                }
+            }
+            cluster_sync();
+        }
+    }
     if constexpr (CG == 2) cluster_sync();
     tc::fence_after_sync();
     if (warp == 1) tmem_dealloc<CG>(tmem, 2 * BN);
@@ -336,21 +492,36 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 
 namespace {
 
-template <int CG, int BN, bool A_MN, bool WG>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const GroupParams &p, int64_t max_units, cudaStream_t s)
+template <int CG, int BN, bool A_MN, bool WG, bool F32>
+cudaError_t launch(const CUtensorMap (&maps)[3], GroupParams &p, int64_t max_units, cudaStream_t s)
 {
-    using T = Ring<CG, BN>;
-    auto kern = group_gemm_kernel<CG, BN, A_MN, WG>;
-    const size_t smem = 1024 + T::stages * T::stage + 8 * (3 * T::stages + 4) + 16 + 4 * 2 * (size_t)(p.E + 1);
+    using T = Ring<CG, BN, WG>;
+    auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32>;
+    const size_t smem = 1024 + T::stages * T::stage + T::extra + 8 * (4 * T::stages + 4) + 16 + 4 * 2 * (size_t)(p.E + 1);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = sm_count() / CG;
+    // Few units: the CTAs of a cluster share one unit's contraction, at least two stages each.
+    p.split = 1;
+    if (CG == 1 && BN <= 32)
+        while (p.split < 8 && 2 * p.split * max_units <= sm_count() && p.R >= 4 * kStep * p.split) p.split *= 2;
+    int64_t grid = p.split > 1 ? max_units : CG == 1 ? sm_count() : resident_clusters(kern, CG, kThreadsG, smem);
     if (max_units < grid) grid = max_units;
     if (grid < 1) grid = 1;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * CG), dim3(kThreadsG), smem, CG, s, a, b, p);
+    const int cluster = CG * p.split;
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(kThreadsG), smem, cluster, s, maps[0],
+                                          maps[1], maps[2], p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
+}
+
+template <int CG, int BN, bool A_MN, bool WG>
+cudaError_t launch_typed(const GroupGemm &g, const CUtensorMap (&maps)[3], GroupParams &p, cudaStream_t s)
+{
+    const int64_t m_tiles = (p.M + kTileM * CG - 1) / (kTileM * CG);
+    const int64_t tiles = WG ? (int64_t)g.E * ((p.N + BN - 1) / BN) : g.P / BN + (g.E < g.P ? g.E : g.P);
+    return g.out_f32 ? launch<CG, BN, A_MN, WG, true>(maps, p, m_tiles * tiles, s)
+                     : launch<CG, BN, A_MN, WG, false>(maps, p, m_tiles * tiles, s);
 }
 
 }  // namespace
@@ -363,36 +534,44 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     p.P = g.P;
     p.out = g.out;
     p.ld = g.ld_out;
-    p.f32 = g.out_f32;
     p.accumulate = g.accumulate;
     p.status = g.status;
     injected_stall(&p.wait_ns, &p.skip_producer);
-    const bool wg = g.form == kGroupWgrad;
-    p.M = g.form == kGroupForward ? g.N : g.K;
-    p.N = g.N;
-    p.R = g.form == kGroupForward ? g.K : g.N;
-    constexpr int BN = 256;
-    const int box_rows = Ring<1, BN>::box_rows;
+    const bool wg = g.form == kGroupWgrad, fw = g.form == kGroupForward;
+    p.M = g.form == kGroupDgrad ? g.K : g.N;
+    p.N = g.K;
+    p.R = fw ? g.K : g.N;
+    // rows per expert that has any, at most: picks the tile's extent along the rows
+    const int64_t per = g.P / (g.E < g.P ? g.E : g.P);
+    const int bn = wg ? 256 : per <= 32 ? 32 : per <= 96 ? 128 : 256;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUtensorMap a, b;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    CUtensorMap maps[3];
     bool ok;
-    if (wg) {  // A: x [P][K] read along k; B: dy [P][N] read along n
-        ok = make_tensor_map_2d(&a, bf, g.x, g.K, g.P, 2 * (uint64_t)g.ld_x, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B) &&
-             make_tensor_map_2d(&b, bf, g.dy, g.N, g.P, 2 * (uint64_t)g.ld_dy, 64, kStep, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (wg) {  // A: dy [P][N] read along n; B: x [P][K] read along k; C: dw
+        ok = make_tensor_map_2d(&maps[0], bf, g.dy, g.N, g.P, 2 * (uint64_t)g.ld_dy, 64, kStep, sw) &&
+             make_tensor_map_2d(&maps[1], bf, g.x, g.K, g.P, 2 * (uint64_t)g.ld_x, 64, kStep, sw) &&
+             make_tensor_map_3d(&maps[2], g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf, g.out, g.K, g.N, g.E,
+                                (g.out_f32 ? 4 : 2) * (uint64_t)g.K, (g.out_f32 ? 4 : 2) * (uint64_t)g.K * g.N,
+                                g.out_f32 ? 32 : 64, 32, sw);
     } else {   // A: w [E][N][K]; B: x [P][K] or dy [P][N]
-        const bool fw = g.form == kGroupForward;
-        ok = make_tensor_map_3d(&a, bf, g.w, g.K, g.N, g.E, 2 * (uint64_t)g.K, 2 * (uint64_t)g.K * g.N, 64,
-                                fw ? kTileM : kStep, CU_TENSOR_MAP_SWIZZLE_128B) &&
-             make_tensor_map_2d(&b, bf, fw ? g.x : g.dy, fw ? g.K : g.N, g.P,
-                                2 * (uint64_t)(fw ? g.ld_x : g.ld_dy), 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+        ok = make_tensor_map_3d(&maps[0], bf, g.w, g.K, g.N, g.E, 2 * (uint64_t)g.K, 2 * (uint64_t)g.K * g.N, 64,
+                                fw ? kTileM : kStep, sw) &&
+             make_tensor_map_2d(&maps[1], bf, fw ? g.x : g.dy, fw ? g.K : g.N, g.P, 2 * (uint64_t)(fw ? g.ld_x : g.ld_dy), 64,
+                                bn <= 32 ? Ring<1, 32, false>::box_rows : Ring<1, 128, false>::box_rows, sw);
+        maps[2] = maps[1];  // (not used)
     }
     if (!ok) return cudaErrorInvalidValue;
-    const int64_t m_tiles = (p.M + kTileM - 1) / kTileM;
-    const int64_t tiles = wg ? (int64_t)g.E * ((g.N + BN - 1) / BN) : g.P / BN + (g.E < g.P ? g.E : g.P);
-    const int64_t units = m_tiles * tiles;
-    if (wg) return launch<1, BN, true, true>(a, b, p, units, s);
-    if (g.form == kGroupDgrad) return launch<1, BN, true, false>(a, b, p, units, s);
-    return launch<1, BN, false, false>(a, b, p, units, s);
+    const bool pair = p.M > kTileM;
+    if (wg) return pair ? launch_typed<2, 256, true, true>(g, maps, p, s) : launch_typed<1, 256, true, true>(g, maps, p, s);
+    if (fw) {
+        if (bn == 32) return launch_typed<1, 32, false, false>(g, maps, p, s);
+        if (bn == 128 || !pair) return launch_typed<1, 128, false, false>(g, maps, p, s);
+        return launch_typed<2, 256, false, false>(g, maps, p, s);
+    }
+    if (bn == 32) return launch_typed<1, 32, true, false>(g, maps, p, s);
+    if (bn == 128 || !pair) return launch_typed<1, 128, true, false>(g, maps, p, s);
+    return launch_typed<2, 256, true, false>(g, maps, p, s);
 }
 
 }  // namespace ftmoe

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(full + i, CG);
+            mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < NA; ++i) {
@@ -158,8 +158,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
                     if (!mbar_wait_timed(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
                     const uint32_t bar = CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
-                    if (CG == 2) arrive_expect_tx_cluster(bar, bytes);
-                    else mbar_arrive_expect_tx(full + s, bytes);
+                    if (leader) mbar_arrive_expect_tx(full + s, CG * bytes);  // for both CTAs of a pair
                     load_3d<CG>(sa, &map_w, b * kStep8, x.m0, x.e, bar);
                     for (int i = 0; i < boxes; ++i)
                         load_2d<CG>(sb + i * T::box_rows * kChunkBytes, &map_x, b * kStep8,
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         // thread = TMEM lane = weight row; columns [h * HC, h * HC + HC) of the tile
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
-        const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : smem_u32(acc_empty);
+        const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : 0;
         int a = 0, it = 0;
         uint32_t pa = 0;
         for (int u = u0; u < units && !dead; u += du) {
@@ -270,7 +269,8 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    arrive_cluster(empty_bar + 8 * a);
+                    if (CG == 2) arrive_cluster_relaxed(empty_bar + 8 * a);
+                    else mbar_arrive(acc_empty + a);
                     mbar_arrive(sc_empty + slot);
                 }
                 if (++a == NA) { a = 0; pa ^= 1; }
