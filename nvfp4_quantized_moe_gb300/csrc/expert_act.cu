@@ -89,8 +89,11 @@ constexpr int kRowsPerCta = kActThreads / 16;  // quantizing kernels: 16 lanes p
 
 }  // namespace
 
-// blockIdx.x: 16 rows (so that the scales of a block are written side by side); blockIdx.y:
-// blocks of 128 columns.
+// A CTA takes 16 rows (so that the scales of a block are written side by side) by kBlocks blocks of
+// 128 columns, whose loads are all in flight before the first is used: 65536 x 2048 bf16 rows in
+// one block at a time reached 4.7 TB/s.
+constexpr int kBlocks = 4;
+
 template <bool F32>
 __global__ void __launch_bounds__(kActThreads)
     quantize_fp8_kernel(const void *__restrict__ src, int64_t ld, int rows, int K, uint8_t *__restrict__ codes,
@@ -98,14 +101,23 @@ __global__ void __launch_bounds__(kActThreads)
 {
     pdl_enter();
     const int row = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4), l = threadIdx.x & 15;
-    const int col = blockIdx.y * 128 + 8 * l;
-    const bool in = row < rows && col < K;
-    float v[8] = {};
-    if (in) load8<F32>(static_cast<const char *>(src) + (int64_t)row * ld * (F32 ? 4 : 2), col, v);
-    const float s = block_scale(v);
-    if (in) *reinterpret_cast<uint2 *>(codes + row * ld_codes + col) = block_codes(v, s);
-    if (row < rows && l == 0) scales[blockIdx.y * ld_scales + row] = s;
+    const int b0 = blockIdx.y * kBlocks, c0 = 128 * b0 + 8 * l;
+    const void *from = static_cast<const char *>(src) + (int64_t)row * ld * (F32 ? 4 : 2);
+    float v[kBlocks][8] = {};
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+        if (row < rows && c0 + 128 * i < K) load8<F32>(from, c0 + 128 * i, v[i]);
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+        if (128 * (b0 + i) >= K) break;
+        const float s = block_scale(v[i]);
+        if (row < rows && c0 + 128 * i < K)
+            *reinterpret_cast<uint2 *>(codes + row * ld_codes + c0 + 128 * i) = block_codes(v[i], s);
+        if (row < rows && l == 0) scales[(b0 + i) * ld_scales + row] = s;
+    }
 }
+
+constexpr int kGluBlocks = 2;
 
 __global__ void __launch_bounds__(kActThreads)
     swiglu_quantize_fp8_kernel(const uint16_t *__restrict__ gu, int64_t ld, const float *__restrict__ w, int rows, int I,
@@ -114,20 +126,31 @@ __global__ void __launch_bounds__(kActThreads)
 {
     pdl_enter();
     const int row = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4), l = threadIdx.x & 15;
-    const int col = blockIdx.y * 128 + 8 * l;
-    const bool in = row < rows && col < I;
-    float h[8] = {};
-    if (in) {
-        float g[8], u[8];
-        load8<false>(gu + row * ld, col, g);
-        load8<false>(gu + row * ld + I, col, u);
-        const float f = w ? __ldg(w + row) : 1.0f;
+    const int b0 = blockIdx.y * kGluBlocks, c0 = 128 * b0 + 8 * l;
+    const uint16_t *from = gu + row * ld;
+    float g[kGluBlocks][8] = {}, u[kGluBlocks][8] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = f * (g[i] * sigmoid(g[i]) * u[i]);
+    for (int i = 0; i < kGluBlocks; ++i)
+        if (row < rows && c0 + 128 * i < I) {
+            load8<false>(from, c0 + 128 * i, g[i]);
+            load8<false>(from + I, c0 + 128 * i, u[i]);
+        }
+    const float f = w && row < rows ? __ldg(w + row) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < kGluBlocks; ++i) {
+        if (128 * (b0 + i) >= I) break;
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = f * (g[i][j] * sigmoid(g[i][j]) * u[i][j]);
+        if (!(row < rows && c0 + 128 * i < I)) {  // no values: not part of the block's maximum
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = 0.f;
+        }
+        const float s = block_scale(h);
+        if (row < rows && c0 + 128 * i < I)
+            *reinterpret_cast<uint2 *>(codes + row * ld_codes + c0 + 128 * i) = block_codes(h, s);
+        if (row < rows && l == 0) scales[(b0 + i) * ld_scales + row] = s;
     }
-    const float s = block_scale(h);
-    if (in) *reinterpret_cast<uint2 *>(codes + row * ld_codes + col) = block_codes(h, s);
-    if (row < rows && l == 0) scales[blockIdx.y * ld_scales + row] = s;
 }
 
 // One warp per row. VEC: 8 columns per lane and step (everything 16-byte aligned), else one.
@@ -222,7 +245,7 @@ static int row_grid(int rows)
 cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows, int K, uint8_t *codes, int64_t ld_codes,
                                 float *scales, int64_t ld_scales, cudaStream_t s)
 {
-    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (K + 127) / 128);
+    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (K + 128 * kBlocks - 1) / (128 * kBlocks));
     if (f32) FT_LAUNCH(quantize_fp8_kernel<true>, grid, dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales, ld_scales);
     else FT_LAUNCH(quantize_fp8_kernel<false>, grid, dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales, ld_scales);
     count_launches(1);
@@ -232,7 +255,7 @@ cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows,
 cudaError_t launch_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float *w, int rows, int I, uint8_t *codes,
                                        int64_t ld_codes, float *scales, int64_t ld_scales, cudaStream_t s)
 {
-    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (I + 127) / 128);
+    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (I + 128 * kGluBlocks - 1) / (128 * kGluBlocks));
     FT_LAUNCH(swiglu_quantize_fp8_kernel, grid, dim3(kActThreads), 0, s, static_cast<const uint16_t *>(gu), ld_gu, w, rows, I,
               codes, ld_codes, scales, ld_scales);
     count_launches(1);

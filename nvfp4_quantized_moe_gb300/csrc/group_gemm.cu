@@ -38,9 +38,8 @@ struct Ring {
     // rows of one TMA box of a row-major B operand: short boxes, so that a short tile loads no
     // more rows than it has (to within a box)
     static constexpr int box_rows = BN <= 32 ? 16 : 32;
-    // wgrad's output tiles on their way to TMA: two of 32 rows x 128 bytes per epilogue warp;
-    // the smallest tiles: the partial sums of a split contraction
-    static constexpr int extra = WG ? 8 * 2 * 4096 : BN <= 32 ? BN * kTileM * 4 : 0;
+    // wgrad's output tiles on their way to TMA: two of 32 rows x 128 bytes per epilogue warp
+    static constexpr int extra = WG ? 8 * 2 * 4096 : 0;
     static constexpr int fit = (216 * 1024 - extra) / stage;
     static constexpr int stages = fit < 10 ? fit : 10;
 };
@@ -82,14 +81,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
     }
 }
 
-// W consecutive 32-bit columns of this thread's TMEM lane.
-template <int W>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[W])
-{
-    if constexpr (W == 32) tc::ld32(addr, v);
-    else tc::ld16(addr, v);
-}
-
 // TMA store of a 128-byte x 32-row tile (128-byte swizzle) of a stack of matrices, or its addition.
 __device__ __forceinline__ void store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2, bool add)
 {
@@ -105,12 +96,6 @@ __device__ __forceinline__ void store_3d(const CUtensorMap *map, const void *src
                      "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                      : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&b);
 }
 
 // One unit of work: a 128 x CG by (up to) BN tile of the output.
@@ -133,7 +118,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     using T = Ring<CG, BN, WG>;
     constexpr int S = T::stages;
     constexpr int kGran = WG ? 64 : 16;        // N indices per CTA come in multiples of this
-    constexpr bool kSplit = CG == 1 && BN <= 32;
+    constexpr bool kSplit = CG == 1 && !WG;
     constexpr int HC = BN / 2;                 // columns of one half's epilogue warps
     constexpr int W = HC < 32 ? HC : 32;       // columns per tensor-memory load
     pdl_enter();
@@ -147,7 +132,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int split = kSplit ? p.split : 1;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const bool leader = rank == 0;
@@ -176,11 +161,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     if constexpr (CG == 2) cluster_sync();
     else __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
 
     const int m_tiles = (p.M + kTileM * CG - 1) / (kTileM * CG);
     const int n_tiles = (p.N + BN - 1) / BN;  // wgrad
-    const int units = WG ? p.E * n_tiles * m_tiles : sh_tiles[p.E] * m_tiles;
+    const int units = WG ? p.E * n_tiles * m_tiles : uniform(sh_tiles[p.E]) * m_tiles;
     const int u0 = blockIdx.x / (CG * split), du = gridDim.x / (CG * split);
     const int part = kSplit ? (int)(blockIdx.x % split) : 0;
     auto unit_of = [&](int u) {
@@ -204,6 +189,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         r.half = ((r.cols + CG - 1) / CG + kGran - 1) / kGran * kGran;
         return r;
     };
+    auto uniform_unit = [](Unit x) {
+        x.e = uniform(x.e); x.m0 = uniform(x.m0); x.col0 = uniform(x.col0); x.cols = uniform(x.cols);
+        x.half = uniform(x.half); x.r0 = uniform(x.r0); x.R = uniform(x.R);
+        return x;
+    };
     // this CTA's stages [first, last) of a contraction of R steps
     auto first_stage = [&](int R) { return kSplit ? (R + kStep - 1) / kStep * part / split : 0; };
     auto last_stage = [&](int R) {
@@ -214,47 +204,48 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0 && !p.skip_producer) {
+        if (!p.skip_producer) {
+            const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
             for (int u = u0; u < units && !dead; u += du) {
-                const Unit x = unit_of(u);
+                const Unit x = uniform_unit(unit_of(u));
                 const int nb = last_stage(x.R);
                 const int boxes = WG ? x.half / 64 : (x.half + T::box_rows - 1) / T::box_rows;
                 const uint32_t bytes = kABytes + boxes * (WG ? 64 * kChunkBytes : T::box_rows * kChunkBytes);
                 for (int b = first_stage(x.R); b < nb; ++b, ++it) {
-                    if (!wait_cluster(empty + s, ph, abort_flag, wl)) { dead = true; break; }
+                    if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
                     const int k0 = b * kStep;
-                    uint32_t bar;
-                    if (WG && b == nb - 1 && (x.R & 15)) {  // the tail warp completes this stage
-                        bar = smem_u32(tail + s);
-                        mbar_arrive_expect_tx(tail + s, bytes);
-                    } else {
+                    // a stage with tail rows is completed by the tail warp
+                    const bool tails = WG && b == nb - 1 && (x.R & 15);
+                    const uint32_t bar = tails ? smem_u32(tail + s) : CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
+                    if (one) {
                         // the leader expects both CTAs' bytes (equally many); the other's may land first
-                        bar = CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
-                        if (leader) mbar_arrive_expect_tx(full + s, CG * bytes);
-                    }
-                    if (WG) {
-                        load_2d<CG>(sa, &map_a, x.m0, x.r0 + k0, bar);
-                        load_2d<CG>(sa + 8192, &map_a, x.m0 + 64, x.r0 + k0, bar);
-                        for (int i = 0; i < boxes; ++i)
-                            load_2d<CG>(sb + i * 8192, &map_b, x.col0 + (int)rank * x.half + 64 * i, x.r0 + k0, bar);
-                    } else {
-                        if (A_MN) {
-                            load_3d<CG>(sa, &map_a, x.m0, k0, x.e, bar);
-                            load_3d<CG>(sa + 8192, &map_a, x.m0 + 64, k0, x.e, bar);
+                        if (tails) mbar_arrive_expect_tx(tail + s, bytes);
+                        else if (leader) mbar_arrive_expect_tx(full + s, CG * bytes);
+                        if (WG) {
+                            load_2d<CG>(sa, &map_a, x.m0, x.r0 + k0, bar);
+                            load_2d<CG>(sa + 8192, &map_a, x.m0 + 64, x.r0 + k0, bar);
+                            for (int i = 0; i < boxes; ++i)
+                                load_2d<CG>(sb + i * 8192, &map_b, x.col0 + (int)rank * x.half + 64 * i, x.r0 + k0, bar);
                         } else {
-                            load_3d<CG>(sa, &map_a, k0, x.m0, x.e, bar);
+                            if (A_MN) {
+                                load_3d<CG>(sa, &map_a, x.m0, k0, x.e, bar);
+                                load_3d<CG>(sa + 8192, &map_a, x.m0 + 64, k0, x.e, bar);
+                            } else {
+                                load_3d<CG>(sa, &map_a, k0, x.m0, x.e, bar);
+                            }
+                            for (int i = 0; i < boxes; ++i)
+                                load_2d<CG>(sb + i * T::box_rows * kChunkBytes, &map_b, k0,
+                                            x.col0 + (int)rank * x.half + i * T::box_rows, bar);
                         }
-                        for (int i = 0; i < boxes; ++i)
-                            load_2d<CG>(sb + i * T::box_rows * kChunkBytes, &map_b, k0,
-                                        x.col0 + (int)rank * x.half + i * T::box_rows, bar);
                     }
+                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
-            if (dead) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
             if (dead && leader)  // every issued copy lands before the exit (normally the MMAs have waited for them)
                 for (int i = 0; i < S && i < it; ++i) {
                     const int last = it - 1 - i;
@@ -263,39 +254,41 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && leader) {
+        if (leader) {
+            const bool one = elect_one();
             int s = 0, ac = 0;
             uint32_t ph = 0;
             for (int u = u0; u < units && !dead; u += du) {
-                const Unit x = unit_of(u);
+                const Unit x = uniform_unit(unit_of(u));
                 const int b0 = first_stage(x.R), nb = last_stage(x.R);
                 const uint32_t idesc = idesc_bf16(kTileM * CG, x.half * CG, A_MN, WG);
                 // (an expert without rows has no stages: the epilogue writes zeros on its own)
                 for (int b = b0; b < nb; ++b) {
                     const bool starts = F32 ? (b - b0) % kPartStages == 0 : b == b0;
                     const bool ends = b == nb - 1 || (F32 && (b - b0) % kPartStages == kPartStages - 1);
-                    if (starts && !wait_cluster(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) { dead = true; break; }
-                    if (!wait_cluster(full + s, ph, abort_flag, wl)) { dead = true; break; }
+                    if (starts && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) { dead = true; break; }
+                    if (!warp_wait(full + s, ph, abort_flag, wl)) { dead = true; break; }
                     tc::fence_after_sync();
                     const uint32_t acc = tmem + (uint32_t)(ac & 1) * BN;
                     const uint32_t a0 = smem_u32(smem + s * T::stage), bb = a0 + kABytes;
                     const int k16 = min(4, (x.R - b * kStep + 15) / 16);  // beyond the contraction's end: not read
+                    // 16 contraction steps further: 2048 bytes (transposed) or 32, in units of 16
+                    const uint64_t ad = A_MN ? sw128_desc_mn(a0) : tc::sw128_desc(a0);
+                    const uint64_t bd = WG ? sw128_desc_mn(bb) : tc::sw128_desc(bb);
+                    if (one) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= k16) break;
-                        const uint64_t ad = A_MN ? sw128_desc_mn(a0 + 2048 * j) : tc::sw128_desc(a0 + 32 * j);
-                        const uint64_t bd = WG ? sw128_desc_mn(bb + 2048 * j) : tc::sw128_desc(bb + 32 * j);
-                        mma_bf16<CG>(acc, ad, bd, idesc, !starts || j != 0);
+                        for (int j = 0; j < 4; ++j)
+                            if (j < k16)
+                                mma_bf16<CG>(acc, ad + j * (A_MN ? 128 : 2), bd + j * (WG ? 128 : 2), idesc, !starts || j != 0);
+                        commit<CG>(empty + s);
+                        if (ends) commit<CG>(acc_full + (ac & 1));
                     }
-                    commit<CG>(empty + s);
-                    if (ends) {
-                        commit<CG>(acc_full + (ac & 1));
-                        ++ac;
-                    }
+                    __syncwarp();
+                    if (ends) ++ac;
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
-            if (dead) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
         }
     } else if (WG && warp == 2 && !p.skip_producer) {
         // ------------------------------------------------------------ tail rows (wgrad)
@@ -383,28 +376,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                         ++so;
                     }
                 } else if (kSplit && split > 1) {
-                    float *red = reinterpret_cast<float *>(extra);
+                    // (every stage of the ring has been read by the time the last sums are complete)
+                    float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
                     for (int j = 0; j < W; ++j) red[(h * HC + c + j) * kTileM + 32 * q + lane] = v[j];
-                } else if constexpr (F32) {
-                    const int n = m < p.M ? mine - c : 0;
-                    float *o = static_cast<float *>(p.out) + ((int64_t)x.col0 + h * HC + c) * p.ld + m;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        if (j < n) *o = v[j];
-                        o += p.ld;
-                    }
                 } else {
-                    // two rows per store: neighbouring lanes trade one value each, so that a lane
-                    // holds two neighbouring columns m of one row (M is even)
-                    const int odd = lane & 1, n = m < p.M ? mine - c - odd : 0;
-                    uint16_t *o = static_cast<uint16_t *>(p.out) + ((int64_t)x.col0 + h * HC + c + odd) * p.ld + (m - odd);
-#pragma unroll
-                    for (int j = 0; j < W; j += 2) {
-                        const uint32_t a = bf16x2(v[j], v[j + 1]), b = __shfl_xor_sync(0xFFFFFFFFu, a, 1);
-                        if (j < n) *reinterpret_cast<uint32_t *>(o) = __byte_perm(a, b, odd ? 0x3276 : 0x5410);
-                        o += 2 * p.ld;
-                    }
+                    store_rows<F32, W>(v, m, p.M, x.col0 + h * HC + c, mine - c, p.out, p.ld);
                 }
             };
             float sum[F32 ? HC : 1];  // fp32 outputs: the parts' running sums
@@ -466,21 +443,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             cluster_sync();
             if (u0 < units) {
                 const Unit x = unit_of(u0);
-                const float *red = reinterpret_cast<const float *>(extra);
-                for (int i = threadIdx.x + kThreadsG * part; i < x.cols * kTileM; i += kThreadsG * split) {
-                    float a = 0.f;
-                    for (int r = 0; r < split; ++r) {
-                        float v;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_rank(red + i, r)) : "memory");
-                        a += v;
-                    }
-                    const int m = x.m0 + i % kTileM;
-                    const int64_t at = (int64_t)(x.col0 + i / kTileM) * p.ld + m;
-                    if (m < p.M) {
-                        if constexpr (F32) static_cast<float *>(p.out)[at] = a;
-                        else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(a);
-                    }
-                }
+                add_parts<F32>(reinterpret_cast<const float *>(smem), x.cols, x.m0, p.M, x.col0, p.out, p.ld, split, part);
             }
             cluster_sync();
         }
@@ -502,7 +465,7 @@ cudaError_t launch(const CUtensorMap (&maps)[3], GroupParams &p, int64_t max_uni
     if (e != cudaSuccess) return e;
     // Few units: the CTAs of a cluster share one unit's contraction, at least two stages each.
     p.split = 1;
-    if (CG == 1 && BN <= 32)
+    if (CG == 1 && !WG)
         while (p.split < 8 && 2 * p.split * max_units <= sm_count() && p.R >= 4 * kStep * p.split) p.split *= 2;
     int64_t grid = p.split > 1 ? max_units : CG == 1 ? sm_count() : resident_clusters(kern, CG, kThreadsG, smem);
     if (max_units < grid) grid = max_units;
@@ -543,7 +506,8 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     p.R = fw ? g.K : g.N;
     // rows per expert that has any, at most: picks the tile's extent along the rows
     const int64_t per = g.P / (g.E < g.P ? g.E : g.P);
-    const int bn = wg ? 256 : per <= 32 ? 32 : per <= 96 ? 128 : 256;
+    const int64_t pairs = (p.M + 255) / 256 * (g.P / 256 + (g.E < g.P ? g.E : g.P));
+    const int bn = wg ? 256 : per <= 32 ? 32 : per <= 96 || 2 * pairs < sm_count() / 2 ? 128 : 256;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap maps[3];

@@ -9,6 +9,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,6 +23,23 @@ namespace grp {
 constexpr int kTileM = 128;          // weight rows of one CTA's tile (TMEM lanes)
 constexpr int kChunkBytes = 128;     // bytes of the contraction axis per stage (the swizzle width)
 constexpr int kABytes = kTileM * kChunkBytes;
+
+// ---------------------------------------------------------------- issuing warps
+//
+// One thread issues the copies and the MMAs, but its whole warp runs the loop around them: their
+// operands live in registers that a warp shares, and only where the compiler sees that a value is
+// the same in all lanes does it keep the value there. In a branch of lane 0 alone every operand of
+// every instruction was moved over first: 94 cycles per MMA, and 700 per stage of four that the
+// tensor cores finish in 512.
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 
 // ---------------------------------------------------------------- clusters
 
@@ -173,6 +191,91 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t smem_addr)
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
+}
+
+// W consecutive 32-bit columns of this thread's TMEM lane.
+template <int W>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[W])
+{
+    if constexpr (W == 32) tc::ld32(addr, v);
+    else tc::ld16(addr, v);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// ---------------------------------------------------------------- stores
+
+// W columns of a tile whose lane is the M index m: columns are the rows row0, row0 + 1, ... of
+// `out` (`rows` of them at most), m (< M) is the place in the row. Called by whole warps.
+// bf16 rows with pairs (M even, every row 4-byte aligned): neighbouring lanes trade one value each,
+// so that a lane holds two neighbours of one row and a store covers two rows.
+template <bool F32, int W, bool PAIRS = true>
+__device__ __forceinline__ void store_rows(const float (&v)[W], int m, int M, int64_t row0, int rows, void *out, int64_t ld)
+{
+    if constexpr (F32) {
+        const int n = m < M ? rows : 0;
+        float *o = static_cast<float *>(out) + row0 * ld + m;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            if (j < n) *o = v[j];
+            o += ld;
+        }
+    } else if constexpr (PAIRS) {
+        const int odd = m & 1, n = m < M ? rows - odd : 0;
+        uint16_t *o = static_cast<uint16_t *>(out) + (row0 + odd) * ld + (m - odd);
+#pragma unroll
+        for (int j = 0; j < W; j += 2) {
+            const uint32_t a = bf16x2(v[j], v[j + 1]), b = __shfl_xor_sync(0xFFFFFFFFu, a, 1);
+            if (j < n) *reinterpret_cast<uint32_t *>(o) = __byte_perm(a, b, odd ? 0x3276 : 0x5410);
+            o += 2 * ld;
+        }
+    } else {
+        const int n = m < M ? rows : 0;
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out) + row0 * ld + m;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            if (j < n) *o = __float2bfloat16_rn(v[j]);
+            o += ld;
+        }
+    }
+}
+
+// The sums of a tile whose contraction the `split` CTAs of a cluster shared: each left its part in
+// its own `red` [cols][128]; the CTAs add and store a share of the elements each, parts always in
+// the same order. Between two cluster barriers, by all threads.
+template <bool F32>
+__device__ __forceinline__ void add_parts(const float *red, int cols, int m0, int M, int64_t row0, void *out, int64_t ld,
+                                          int split, int part)
+{
+    constexpr int kMax = 8;
+    // four neighbours of one row at a time, all parts' loads in flight together
+    for (int i = 4 * (threadIdx.x + blockDim.x * part); i < cols * kTileM; i += 4 * blockDim.x * split) {
+        float4 v[kMax];
+#pragma unroll
+        for (int r = 0; r < kMax; ++r)
+            if (r < split)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                             : "r"(map_rank(red + i, r))
+                             : "memory");
+        float4 a = v[0];
+#pragma unroll
+        for (int r = 1; r < kMax; ++r)
+            if (r < split) { a.x += v[r].x; a.y += v[r].y; a.z += v[r].z; a.w += v[r].w; }
+        const int m = m0 + i % kTileM;
+        const int64_t at = (row0 + i / kTileM) * ld + m;
+        const float o[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (m + j < M) {
+                if constexpr (F32) static_cast<float *>(out)[at + j] = o[j];
+                else static_cast<__nv_bfloat16 *>(out)[at + j] = __float2bfloat16_rn(o[j]);
+            }
+    }
 }
 
 // ---------------------------------------------------------------- the experts' rows

@@ -21,13 +21,15 @@ using namespace grp;
 constexpr int kThreads8 = 384;  // warps: 0 TMA, 1 MMA, 2-3 scales, 4..11 sums and epilogue
 constexpr int kStep8 = 128;     // contraction steps per stage: one scale block
 
+// Tile variants, as in group_gemm.cu.
 template <int CG, int BN>
 struct Ring8 {
     static constexpr int b_bytes = BN / CG * kChunkBytes;
     static constexpr int stage = kABytes + b_bytes;
-    static constexpr int stages = (192 * 1024) / stage < 10 ? (192 * 1024) / stage : 10;
+    static constexpr int fit = 208 * 1024 / stage;
+    static constexpr int stages = fit < 10 ? fit : 10;
     static constexpr int box_rows = BN <= 32 ? 16 : 32;
-    static constexpr int acc = BN >= 256 ? 2 : 8;    // partial-sum buffers in tensor memory
+    static constexpr int acc = BN >= 256 ? 2 : BN >= 128 ? 4 : 8;  // partial-sum buffers in tensor memory
     static constexpr int slots = 8;                  // scale slots in shared memory
 };
 
@@ -39,7 +41,9 @@ struct Group8Params {
     const float *ws;      // [E][ceil(N / 128)][ceil(K / 128)]
     void *out;            // [P][ld]
     int64_t ld;
-    int f32;
+    int split;            // CTAs (one cluster) that share a unit's contraction
+    int pairs;            // bf16 out: N even and rows 4-byte aligned
+    int vec;              // N and the rows of out are multiples of 16 bytes
     int *status;
     uint64_t wait_ns;
     int skip_producer;
@@ -72,19 +76,26 @@ __device__ __forceinline__ void fma2(float2 &a, float s0, float s1, uint32_t v0,
         : "f"(s0), "f"(s1), "r"(v0), "r"(v1));
 }
 
+// kind::f8f6f4 instruction descriptor: e4m3 operands (type fields 0), fp32 D.
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 struct Unit8 {
     int e, m0, row0, rows, half;
 };
 
 }  // namespace
 
-template <int CG, int BN>
+template <int CG, int BN, bool F32>
 __global__ void __launch_bounds__(kThreads8, 1)
     group_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                           const __grid_constant__ Group8Params p)
 {
     using T = Ring8<CG, BN>;
     constexpr int S = T::stages, NA = T::acc, NS = T::slots;
+    constexpr bool kSplit = CG == 1;
     constexpr int HC = BN / 2;  // columns of one half's warps
     pdl_enter();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -97,7 +108,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const bool leader = rank == 0;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
@@ -126,12 +137,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
     if constexpr (CG == 2) cluster_sync();
     else __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
 
     const int m_tiles = (p.N + kTileM * CG - 1) / (kTileM * CG);
-    const int units = sh_tiles[p.E] * m_tiles;
-    const int nb = (p.K + kStep8 - 1) / kStep8;
-    const int u0 = blockIdx.x / CG, du = gridDim.x / CG;
+    const int units = uniform(sh_tiles[p.E]) * m_tiles;
+    const int split = kSplit ? p.split : 1, part = kSplit ? (int)(blockIdx.x % split) : 0;
+    const int nblocks = (p.K + kStep8 - 1) / kStep8;
+    const int b0 = nblocks * part / split, nb = nblocks * (part + 1) / split;  // this CTA's blocks
+    const int u0 = blockIdx.x / (CG * split), du = gridDim.x / (CG * split);
     auto unit_of = [&](int u) {
         const int t = u / m_tiles;
         const Tile x = find_tile(t, p.E, BN, 16 * CG, sh_offs, sh_tiles);
@@ -143,31 +156,38 @@ __global__ void __launch_bounds__(kThreads8, 1)
         r.half = ((x.rows + CG - 1) / CG + 15) / 16 * 16;
         return r;
     };
+    auto uniform_unit = [](Unit8 x) {
+        x.e = uniform(x.e); x.m0 = uniform(x.m0); x.row0 = uniform(x.row0); x.rows = uniform(x.rows); x.half = uniform(x.half);
+        return x;
+    };
     bool dead = false;
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0 && !p.skip_producer) {
+        if (!p.skip_producer) {
+            const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
             for (int u = u0; u < units && !dead; u += du) {
-                const Unit8 x = unit_of(u);
+                const Unit8 x = uniform_unit(unit_of(u));
                 const int boxes = (x.half + T::box_rows - 1) / T::box_rows;
                 const uint32_t bytes = kABytes + boxes * T::box_rows * kChunkBytes;
-                for (int b = 0; b < nb; ++b, ++it) {
-                    if (!mbar_wait_timed(empty + s, ph, abort_flag, wl)) { dead = true; break; }
+                for (int b = b0; b < nb; ++b, ++it) {
+                    if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
-                    const uint32_t bar = CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
-                    if (leader) mbar_arrive_expect_tx(full + s, CG * bytes);  // for both CTAs of a pair
-                    load_3d<CG>(sa, &map_w, b * kStep8, x.m0, x.e, bar);
-                    for (int i = 0; i < boxes; ++i)
-                        load_2d<CG>(sb + i * T::box_rows * kChunkBytes, &map_x, b * kStep8,
-                                    x.row0 + (int)rank * x.half + i * T::box_rows, bar);
+                    const uint32_t bar = smem_u32(full + s);
+                    if (one) {
+                        mbar_arrive_expect_tx(full + s, bytes);
+                        load_3d<1>(sa, &map_w, b * kStep8, x.m0, x.e, bar);
+                        for (int i = 0; i < boxes; ++i)
+                            load_2d<1>(sb + i * T::box_rows * kChunkBytes, &map_x, b * kStep8, x.row0 + i * T::box_rows, bar);
+                    }
+                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
-            if (dead) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
-            if (dead && leader)  // every issued copy lands before the exit
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+            if (dead)  // every issued copy lands before the exit
                 for (int i = 0; i < S && i < it; ++i) {
                     const int last = it - 1 - i;
                     mbar_wait_timed(full + last % S, (last / S) & 1, nullptr, wl);
@@ -175,32 +195,32 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && leader) {
-            int s = 0, a = 0;
-            uint32_t ph = 0, pa = 1;
-            for (int u = u0; u < units && !dead; u += du) {
-                const Unit8 x = unit_of(u);
-                // kind::f8f6f4: e4m3 operands (type fields 0), fp32 sums
-                const uint32_t idesc = (1u << 4) | ((uint32_t)(x.half * CG >> 3) << 17) | ((uint32_t)(kTileM * CG >> 4) << 24);
-                for (int b = 0; b < nb; ++b) {
-                    if (!wait_cluster(acc_empty + a, pa, abort_flag, wl) || !wait_cluster(full + s, ph, abort_flag, wl)) {
-                        dead = true;
-                        break;
-                    }
-                    tc::fence_after_sync();
-                    const uint32_t a0 = smem_u32(smem + s * T::stage), b0 = a0 + kABytes;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_e4m3<CG>(tmem + (uint32_t)a * BN, tc::sw128_desc(a0 + 32 * j), tc::sw128_desc(b0 + 32 * j), idesc,
-                                     j != 0);
-                    commit<CG>(empty + s);
-                    commit<CG>(acc_full + a);
-                    if (++s == S) { s = 0; ph ^= 1; }
-                    if (++a == NA) { a = 0; pa ^= 1; }
+        const bool one = elect_one();
+        int s = 0, a = 0;
+        uint32_t ph = 0, pa = 1;
+        for (int u = u0; u < units && !dead; u += du) {
+            const Unit8 x = uniform_unit(unit_of(u));
+            const uint32_t idesc = idesc_e4m3(kTileM, x.half);
+            for (int b = b0; b < nb; ++b) {
+                if (!warp_wait(acc_empty + a, pa, abort_flag, wl) || !warp_wait(full + s, ph, abort_flag, wl)) {
+                    dead = true;
+                    break;
                 }
+                tc::fence_after_sync();
+                const uint32_t sa = smem_u32(smem + s * T::stage);
+                const uint64_t ad = tc::sw128_desc(sa), bd = tc::sw128_desc(sa + kABytes);
+                if (one) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_e4m3<1>(tmem + (uint32_t)a * BN, ad + 2 * j, bd + 2 * j, idesc, j != 0);
+                    commit<1>(empty + s);
+                    commit<1>(acc_full + a);
+                }
+                __syncwarp();
+                if (++s == S) { s = 0; ph ^= 1; }
+                if (++a == NA) { a = 0; pa ^= 1; }
             }
-            if (dead) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
         }
+        if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     } else if (warp < 4) {
         // ------------------------------------------------------------ scales
         // The two warps take the blocks in turn: slot c of block it = xs[b, row of c] * ws[e, tile, b]
@@ -210,9 +230,9 @@ __global__ void __launch_bounds__(kThreads8, 1)
         for (int u = u0; u < units && !dead; u += du) {
             const Unit8 x = unit_of(u);
             const int tile_m = min(x.m0 / 128, n_blocks128 - 1);
-            const float *w = p.ws + ((int64_t)x.e * n_blocks128 + tile_m) * nb;
+            const float *w = p.ws + ((int64_t)x.e * n_blocks128 + tile_m) * nblocks;
             const float *xr = p.xs + x.row0;
-            for (int b = 0; b < nb; ++b, ++it) {
+            for (int b = b0; b < nb; ++b, ++it) {
                 if ((it & 1) != warp - 2) continue;
                 float v[BN / 32];
                 const float wb = __ldg(w + b);
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
 #pragma unroll
             for (int j = 0; j < HC / 2; ++j) sum[j] = make_float2(0.f, 0.f);
             const int mine = min(max(x.rows - h * HC, 0), HC);  // columns of this half in use
-            for (int b = 0; b < nb; ++b, ++it) {
+            for (int b = b0; b < nb; ++b, ++it) {
                 const int slot = it % NS;
                 if (!warp_wait(sc_full + slot, (it / NS) & 1, abort_flag, wl) ||
                     !warp_wait(acc_full + a, pa, abort_flag, wl)) {
@@ -277,24 +297,303 @@ __global__ void __launch_bounds__(kThreads8, 1)
             }
             if (dead) break;
             const int m = x.m0 + 32 * q + lane;
-            const int n = m < p.N ? mine : 0;
-            const int64_t at = ((int64_t)x.row0 + h * HC) * p.ld + m;
-            if (p.f32) {
-                float *o = static_cast<float *>(p.out) + at;
+            if (kSplit && split > 1) {
+                // (every stage of the ring has been read by the time the last sums are complete)
+                float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-                for (int j = 0; j < HC; ++j)
-                    if (j < n) o[j * p.ld] = j & 1 ? sum[j / 2].y : sum[j / 2].x;
+                for (int j = 0; j < HC; ++j) red[(h * HC + j) * kTileM + 32 * q + lane] = j & 1 ? sum[j / 2].y : sum[j / 2].x;
             } else {
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
 #pragma unroll
-                for (int j = 0; j < HC; ++j)
-                    if (j < n) o[j * p.ld] = __float2bfloat16_rn(j & 1 ? sum[j / 2].y : sum[j / 2].x);
+                for (int c = 0; c < HC; c += 16) {
+                    if (c >= mine) break;
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = j & 1 ? sum[(c + j) / 2].y : sum[(c + j) / 2].x;
+                    if (F32 || p.pairs) store_rows<F32, 16>(v, m, p.N, x.row0 + h * HC + c, mine - c, p.out, p.ld);
+                    else store_rows<F32, 16, false>(v, m, p.N, x.row0 + h * HC + c, mine - c, p.out, p.ld);
+                }
             }
             __syncwarp();
         }
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     }
 
+    // wind down; a cluster leaves together
+    tc::fence_before_sync();
+    __syncthreads();
+    if constexpr (kSplit) {
+        if (split > 1) {
+            cluster_sync();
+            if (u0 < units) {
+                const Unit8 x = unit_of(u0);
+                add_parts<F32>(reinterpret_cast<const float *>(smem), x.rows, x.m0, p.N, x.row0, p.out, p.ld, split, part);
+            }
+            cluster_sync();
+        }
+    }
+    if constexpr (CG == 2) cluster_sync();
+    tc::fence_after_sync();
+    if (warp == 1) tmem_dealloc<CG>(tmem, NA * BN);
+}
+
+// ---------------------------------------------------------------- many rows per expert
+//
+// The same product with the rows along the M axis (thread = lane = row) and the weight rows along
+// N. The scale of a block is then one number per thread, loaded a block ahead, and the running
+// sums cost nothing but the tensor-memory read and half an instruction per column; with the rows
+// along N each column's scale has to be read from shared memory, which the tensor cores' operands
+// already fill. The price is that rows come in tiles of 128 x CG, paid for by every expert's
+// remainder.
+
+namespace {
+
+template <int CG>
+struct RingW {
+    static constexpr int BN = 256;
+    static constexpr int b_bytes = BN / CG * kChunkBytes;
+    static constexpr int stage = kABytes + b_bytes;
+    static constexpr int stages = (208 * 1024) / stage;
+    static constexpr int box_rows = 32;  // rows of x per TMA box
+    static constexpr int acc = 2;
+    // Sum warps: four per group of 64 columns. Sixteen warps of 64 sums a thread hide the
+    // tensor-memory reads' latency; eight of 128 left the tensor cores idle half the time.
+    static constexpr int groups = 2;
+    static constexpr int threads = 128 + 128 * groups;
+};
+
+// Wait for this thread's tensor-memory loads into v (the values are tied to the wait, so that
+// nothing that uses them moves before it).
+__device__ __forceinline__ void wait_ld16(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
+}  // namespace
+
+template <int CG, bool F32>
+__global__ void __launch_bounds__(RingW<CG>::threads, 1)
+    group_gemm_fp8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                               const __grid_constant__ Group8Params p)
+{
+    using T = RingW<CG>;
+    constexpr int S = T::stages, NA = T::acc, BN = T::BN, HC = BN / T::groups;
+    pdl_enter();
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * T::stage);
+    uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + NA;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + NA);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
+    int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const bool leader = rank == 0;
+    const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 4 * T::groups * CG);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tc::prefetch_map(&map_w);
+        tc::prefetch_map(&map_x);
+    }
+    if (warp == 1) tmem_alloc<CG>(tmem_slot, NA * BN);
+    const bool valid = build_table(p.offs, p.E, p.P, kTileM * CG, sh_offs, sh_tiles, sh_flag);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
+    tc::fence_before_sync();
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = uniform(*tmem_slot);
+
+    const int n_tiles = (p.N + BN - 1) / BN;
+    const int units = uniform(sh_tiles[p.E]) * n_tiles;
+    const int nb = (p.K + kStep8 - 1) / kStep8;
+    const int u0 = blockIdx.x / CG, du = gridDim.x / CG;
+    struct UnitW {
+        int e, row0, rows;  // the unit's rows (of both CTAs of a pair)
+        int n0, cols, half; // weight rows; how many of them this CTA loads
+    };
+    auto unit_of = [&](int u) {
+        const int t = u / n_tiles;
+        const Tile x = find_tile(t, p.E, kTileM * CG, kTileM, sh_offs, sh_tiles);
+        UnitW r;
+        r.e = x.e;
+        r.row0 = x.row0;
+        r.rows = x.rows;
+        r.n0 = (u - t * n_tiles) * BN;
+        r.cols = min(BN, p.N - r.n0);
+        r.half = ((r.cols + CG - 1) / CG + 15) / 16 * 16;
+        return r;
+    };
+    auto uniform_unit = [](UnitW x) {
+        x.e = uniform(x.e); x.row0 = uniform(x.row0); x.rows = uniform(x.rows);
+        x.n0 = uniform(x.n0); x.cols = uniform(x.cols); x.half = uniform(x.half);
+        return x;
+    };
+    bool dead = false;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 0 && !p.skip_producer) {
+            // -------------------------------------------------------- producer
+            const bool one = elect_one();
+            int s = 0, it = 0;
+            uint32_t ph = 1;
+            for (int u = u0; u < units && !dead; u += du) {
+                const UnitW x = uniform_unit(unit_of(u));
+                // boxes of x rows: this CTA's and, for a pair, both CTAs' (the leader expects them all)
+                auto boxes_of = [&](int r) { return (min(max(x.rows - r * kTileM, 0), kTileM) + T::box_rows - 1) / T::box_rows; };
+                const int boxes = boxes_of(rank);
+                const uint32_t w_bytes = CG == 2 ? 128 * kChunkBytes : 256 * kChunkBytes;
+                uint32_t bytes = 0;
+                for (int r = 0; r < CG; ++r) bytes += boxes_of(r) * T::box_rows * kChunkBytes + w_bytes;
+                for (int b = 0; b < nb; ++b, ++it) {
+                    if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
+                    unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
+                    const uint32_t bar = CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
+                    if (one) {
+                        if (leader) mbar_arrive_expect_tx(full + s, bytes);
+                        for (int i = 0; i < boxes; ++i)
+                            load_2d<CG>(sa + i * T::box_rows * kChunkBytes, &map_x, b * kStep8,
+                                        x.row0 + (int)rank * kTileM + i * T::box_rows, bar);
+                        load_3d<CG>(sb, &map_w, b * kStep8, x.n0 + (int)rank * x.half, x.e, bar);
+                        if (CG == 1) load_3d<CG>(sb + 128 * kChunkBytes, &map_w, b * kStep8, x.n0 + 128, x.e, bar);
+                    }
+                    __syncwarp();
+                    if (++s == S) { s = 0; ph ^= 1; }
+                }
+            }
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+            if (dead && leader)  // every issued copy lands before the exit
+                for (int i = 0; i < S && i < it; ++i) {
+                    const int last = it - 1 - i;
+                    mbar_wait_timed(full + last % S, (last / S) & 1, nullptr, wl);
+                }
+        } else if (warp == 1 && leader) {
+            // -------------------------------------------------------- MMA issuer
+            const bool one = elect_one();
+            int s = 0, a = 0;
+            uint32_t ph = 0, pa = 1;
+            for (int u = u0; u < units && !dead; u += du) {
+                const UnitW x = uniform_unit(unit_of(u));
+                const uint32_t idesc = idesc_e4m3(kTileM * CG, x.half * CG);
+                for (int b = 0; b < nb; ++b) {
+                    if (!warp_wait(acc_empty + a, pa, abort_flag, wl) || !warp_wait(full + s, ph, abort_flag, wl)) {
+                        dead = true;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t sa = smem_u32(smem + s * T::stage);
+                    const uint64_t ad = tc::sw128_desc(sa), bd = tc::sw128_desc(sa + kABytes);
+                    if (one) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_e4m3<CG>(tmem + (uint32_t)a * BN, ad + 2 * j, bd + 2 * j, idesc, j != 0);
+                        commit<CG>(empty + s);
+                        commit<CG>(acc_full + a);
+                    }
+                    __syncwarp();
+                    if (++s == S) { s = 0; ph ^= 1; }
+                    if (++a == NA) { a = 0; pa ^= 1; }
+                }
+            }
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+        }
+    } else {
+        // ------------------------------------------------------------ sums and epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
+        const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : 0;
+        const int n_blocks128 = (p.N + 127) / 128;
+        int a = 0;
+        uint32_t pa = 0;
+        for (int u = u0; u < units && !dead; u += du) {
+            const UnitW x = unit_of(u);
+            float2 sum[HC / 2];
+#pragma unroll
+            for (int j = 0; j < HC / 2; ++j) sum[j] = make_float2(0.f, 0.f);
+            const int mine = min(max(x.cols - h * HC, 0), HC);  // columns of this group in use
+            const int r = (int)rank * kTileM + 32 * q + lane;   // this thread's row of the unit
+            const bool live = r < x.rows;
+            const float *xs = p.xs + x.row0 + (live ? r : 0);
+            const float *ws = p.ws + ((int64_t)x.e * n_blocks128 + min((x.n0 + h * HC) / 128, n_blocks128 - 1)) * nb;
+            float xn = __ldg(xs), wn = __ldg(ws);
+            for (int b = 0; b < nb; ++b) {
+                const float f = xn * wn;
+                if (b + 1 < nb) {  // the next block's, while this one's sums are added
+                    xn = __ldg(xs + (int64_t)(b + 1) * p.ld_xs);
+                    wn = __ldg(ws + b + 1);
+                }
+                if (!warp_wait(acc_full + a, pa, abort_flag, wl)) { dead = true; break; }
+                tc::fence_after_sync();
+                if (mine > 0) {
+                    const uint32_t addr = lane_addr + (uint32_t)a * BN;
+                    uint32_t v[2][16];
+                    tc::ld16(addr, v[0]);
+                    wait_ld16(v[0]);
+#pragma unroll
+                    for (int c = 0; c < HC / 16; ++c) {
+                        if (c + 1 < HC / 16) tc::ld16(addr + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) fma2(sum[8 * c + j], f, f, v[c & 1][2 * j], v[c & 1][2 * j + 1]);
+                        if (c + 1 < HC / 16) wait_ld16(v[(c + 1) & 1]);
+                    }
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2) arrive_cluster_relaxed(empty_bar + 8 * a);
+                    else mbar_arrive(acc_empty + a);
+                }
+                if (++a == NA) { a = 0; pa ^= 1; }
+            }
+            if (dead) break;
+            if (live) {
+                const int64_t at = (int64_t)(x.row0 + r) * p.ld + x.n0 + h * HC;
+                if (p.vec) {  // 16 bytes at a time (N and the rows are multiples of them)
+                    if constexpr (F32) {
+                        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+#pragma unroll
+                        for (int j = 0; j < HC / 4; ++j)
+                            if (4 * j < mine) o[j] = make_float4(sum[2 * j].x, sum[2 * j].y, sum[2 * j + 1].x, sum[2 * j + 1].y);
+                    } else {
+                        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at);
+#pragma unroll
+                        for (int j = 0; j < HC / 8; ++j)
+                            if (8 * j < mine)
+                                o[j] = make_uint4(bf16x2(sum[4 * j].x, sum[4 * j].y), bf16x2(sum[4 * j + 1].x, sum[4 * j + 1].y),
+                                                  bf16x2(sum[4 * j + 2].x, sum[4 * j + 2].y),
+                                                  bf16x2(sum[4 * j + 3].x, sum[4 * j + 3].y));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < HC; ++j)
+                        if (j < mine) {
+                            const float v = j & 1 ? sum[j / 2].y : sum[j / 2].x;
+                            if constexpr (F32) static_cast<float *>(p.out)[at + j] = v;
+                            else static_cast<__nv_bfloat16 *>(p.out)[at + j] = __float2bfloat16_rn(v);
+                        }
+                }
+            }
+            __syncwarp();
+        }
+        if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+    }
+
+    // wind down; a cluster leaves together
     tc::fence_before_sync();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
@@ -304,19 +603,43 @@ __global__ void __launch_bounds__(kThreads8, 1)
 
 namespace {
 
-template <int CG, int BN>
-cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, const Group8Params &p, int64_t max_units, cudaStream_t s)
+template <int CG, int BN, bool F32>
+cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p, cudaStream_t s)
 {
     using T = Ring8<CG, BN>;
-    auto kern = group_gemm_fp8_kernel<CG, BN>;
-    const size_t smem = 1024 + T::stages * T::stage + 4 * T::slots * BN + 8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) +
-                        16 + 4 * 2 * (size_t)(p.E + 1);
+    auto kern = group_gemm_fp8_kernel<CG, BN, F32>;
+    const size_t smem = 1024 + T::stages * T::stage + 4 * T::slots * BN +
+                        8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) + 16 + 4 * 2 * (size_t)(p.E + 1);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = sm_count() / CG;
-    if (max_units < grid) grid = max_units;
+    const int64_t m_tiles = (p.N + kTileM * CG - 1) / (kTileM * CG);
+    const int64_t units = m_tiles * (p.P / BN + (p.E < p.P ? p.E : p.P));  // at most
+    // Few units: the CTAs of a cluster share one unit's contraction, at least two blocks each.
+    p.split = 1;
+    if (CG == 1)
+        while (p.split < 8 && 2 * p.split * units <= sm_count() && p.K >= 4 * kStep8 * p.split) p.split *= 2;
+    int64_t grid = p.split > 1 ? units : CG == 1 ? sm_count() : resident_clusters(kern, CG, kThreads8, smem);
+    if (units < grid) grid = units;
     if (grid < 1) grid = 1;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * CG), dim3(kThreads8), smem, CG, s, w, x, p);
+    const int cluster = CG * p.split;
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(kThreads8), smem, cluster, s, w, x, p);
+    if (le != cudaSuccess) return le;
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <int CG, bool F32>
+cudaError_t launch_wide(const CUtensorMap &w, const CUtensorMap &x, const Group8Params &p, cudaStream_t s)
+{
+    using T = RingW<CG>;
+    auto kern = group_gemm_fp8_wide_kernel<CG, F32>;
+    const size_t smem = 1024 + T::stages * T::stage + 8 * (2 * T::stages + 2 * T::acc) + 16 + 4 * 2 * (size_t)(p.E + 1);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t units = (int64_t)((p.N + T::BN - 1) / T::BN) * (p.P / (kTileM * CG) + (p.E < p.P ? p.E : p.P));  // at most
+    int64_t grid = CG == 1 ? sm_count() : resident_clusters(kern, CG, T::threads, smem);
+    if (units < grid) grid = units;
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * CG), dim3(T::threads), smem, CG, s, w, x, p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
@@ -337,18 +660,23 @@ cudaError_t launch_group_gemm_fp8(const GroupGemm8 &g, cudaStream_t s)
     p.ws = g.ws;
     p.out = g.out;
     p.ld = g.ld_out;
-    p.f32 = g.out_f32;
+    p.pairs = g.N % 2 == 0 && g.ld_out % 2 == 0;
+    p.vec = g.N % (g.out_f32 ? 4 : 8) == 0 && g.ld_out % (g.out_f32 ? 4 : 8) == 0;
     p.status = g.status;
     injected_stall(&p.wait_ns, &p.skip_producer);
-    constexpr int BN = 256;
+    const int64_t per = g.P / (g.E < g.P ? g.E : g.P);  // rows per expert that has any
+    const int64_t pairs = (g.N + 255) / 256 * (g.P / 256 + (g.E < g.P ? g.E : g.P));
+    const int bn = per <= 32 ? 32 : per <= 96 || g.N <= kTileM || 2 * pairs < sm_count() / 2 ? 128 : 256;
     CUtensorMap w, x;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (!make_tensor_map_3d(&w, u8, g.w, g.K, g.N, g.E, g.K, (uint64_t)g.K * g.N, kStep8, kTileM,
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map_2d(&x, u8, g.x, g.K, g.P, g.ld_x, kStep8, Ring8<1, BN>::box_rows, CU_TENSOR_MAP_SWIZZLE_128B))
+        !make_tensor_map_2d(&x, u8, g.x, g.K, g.P, g.ld_x, kStep8, bn == 32 ? Ring8<1, 32>::box_rows : Ring8<1, 128>::box_rows,
+                            CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    const int64_t units = (int64_t)((g.N + kTileM - 1) / kTileM) * (g.P / BN + (g.E < g.P ? g.E : g.P));
-    return launch8<1, BN>(w, x, p, units, s);
+    if (bn == 32) return g.out_f32 ? launch8<1, 32, true>(w, x, p, s) : launch8<1, 32, false>(w, x, p, s);
+    if (bn == 128) return g.out_f32 ? launch8<1, 128, true>(w, x, p, s) : launch8<1, 128, false>(w, x, p, s);
+    return g.out_f32 ? launch_wide<2, true>(w, x, p, s) : launch_wide<2, false>(w, x, p, s);
 }
 
 }  // namespace ftmoe
