@@ -89,12 +89,11 @@ constexpr int kRowsPerCta = kActThreads / 16;  // quantizing kernels: 16 lanes p
 
 }  // namespace
 
-// A CTA takes 16 rows (so that the scales of a block are written side by side) by kBlocks blocks of
+// A CTA takes 16 rows (so that the scales of a block are written side by side) by several blocks of
 // 128 columns, whose loads are all in flight before the first is used: 65536 x 2048 bf16 rows in
 // one block at a time reached 4.7 TB/s.
-constexpr int kBlocks = 4;
-
-template <bool F32>
+// (A launch that does not fill the SMs takes one: more CTAs are then faster.)
+template <bool F32, int kBlocks>
 __global__ void __launch_bounds__(kActThreads)
     quantize_fp8_kernel(const void *__restrict__ src, int64_t ld, int rows, int K, uint8_t *__restrict__ codes,
                         int64_t ld_codes, float *__restrict__ scales, int64_t ld_scales)
@@ -117,8 +116,7 @@ __global__ void __launch_bounds__(kActThreads)
     }
 }
 
-constexpr int kGluBlocks = 2;
-
+template <int kGluBlocks>
 __global__ void __launch_bounds__(kActThreads)
     swiglu_quantize_fp8_kernel(const uint16_t *__restrict__ gu, int64_t ld, const float *__restrict__ w, int rows, int I,
                                uint8_t *__restrict__ codes, int64_t ld_codes, float *__restrict__ scales,
@@ -245,9 +243,12 @@ static int row_grid(int rows)
 cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows, int K, uint8_t *codes, int64_t ld_codes,
                                 float *scales, int64_t ld_scales, cudaStream_t s)
 {
-    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (K + 128 * kBlocks - 1) / (128 * kBlocks));
-    if (f32) FT_LAUNCH(quantize_fp8_kernel<true>, grid, dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales, ld_scales);
-    else FT_LAUNCH(quantize_fp8_kernel<false>, grid, dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales, ld_scales);
+    const int by_rows = (rows + kRowsPerCta - 1) / kRowsPerCta, nb = (K + 127) / 128;
+    const int per = (int64_t)by_rows * nb < 16 * sm_count() ? 1 : 4;
+    auto kern = f32 ? (per == 1 ? quantize_fp8_kernel<true, 1> : quantize_fp8_kernel<true, 4>)
+                    : (per == 1 ? quantize_fp8_kernel<false, 1> : quantize_fp8_kernel<false, 4>);
+    FT_LAUNCH(kern, dim3(by_rows, (nb + per - 1) / per), dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales,
+              ld_scales);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -255,9 +256,11 @@ cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows,
 cudaError_t launch_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float *w, int rows, int I, uint8_t *codes,
                                        int64_t ld_codes, float *scales, int64_t ld_scales, cudaStream_t s)
 {
-    const dim3 grid((rows + kRowsPerCta - 1) / kRowsPerCta, (I + 128 * kGluBlocks - 1) / (128 * kGluBlocks));
-    FT_LAUNCH(swiglu_quantize_fp8_kernel, grid, dim3(kActThreads), 0, s, static_cast<const uint16_t *>(gu), ld_gu, w, rows, I,
-              codes, ld_codes, scales, ld_scales);
+    const int by_rows = (rows + kRowsPerCta - 1) / kRowsPerCta, nb = (I + 127) / 128;
+    const int per = (int64_t)by_rows * nb < 16 * sm_count() ? 1 : 2;
+    auto kern = per == 1 ? swiglu_quantize_fp8_kernel<1> : swiglu_quantize_fp8_kernel<2>;
+    FT_LAUNCH(kern, dim3(by_rows, (nb + per - 1) / per), dim3(kActThreads), 0, s, static_cast<const uint16_t *>(gu), ld_gu, w,
+              rows, I, codes, ld_codes, scales, ld_scales);
     count_launches(1);
     return cudaGetLastError();
 }

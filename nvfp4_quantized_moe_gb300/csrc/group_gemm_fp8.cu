@@ -339,26 +339,26 @@ __global__ void __launch_bounds__(kThreads8, 1)
 // ---------------------------------------------------------------- many rows per expert
 //
 // The same product with the rows along the M axis (thread = lane = row) and the weight rows along
-// N. The scale of a block is then one number per thread, loaded a block ahead, and the running
-// sums cost nothing but the tensor-memory read and half an instruction per column; with the rows
-// along N each column's scale has to be read from shared memory, which the tensor cores' operands
-// already fill. The price is that rows come in tiles of 128 x CG, paid for by every expert's
-// remainder.
+// N, by pairs of CTAs: 256 rows x 256 columns, each CTA its own 128 rows and half of the shared
+// weight tile. The scale of a block is then one number per thread, loaded ahead, and the
+// running sums cost the tensor-memory read and a multiply-add per column; with the rows along N each
+// column's scale has to be read from shared memory too. The price is that rows come in tiles of
+// 256, paid for by every expert's remainder.
+//
+// A block's columns are two pieces of 128 with their own MMAs and tensor-memory buffers (two each):
+// a buffer's way from the tensor cores through the sums and back takes longer than its MMAs, and
+// overlaps three others this way.
 
 namespace {
 
-template <int CG>
 struct RingW {
-    static constexpr int BN = 256;
-    static constexpr int b_bytes = BN / CG * kChunkBytes;
-    static constexpr int stage = kABytes + b_bytes;
-    static constexpr int stages = (208 * 1024) / stage;
-    static constexpr int box_rows = 32;  // rows of x per TMA box
-    static constexpr int acc = 2;
-    // Sum warps: four per group of 64 columns. Sixteen warps of 64 sums a thread hide the
-    // tensor-memory reads' latency; eight of 128 left the tensor cores idle half the time.
-    static constexpr int groups = 2;
-    static constexpr int threads = 128 + 128 * groups;
+    static constexpr int BN = 256, piece = 128;
+    static constexpr int stage = kABytes + BN / 2 * kChunkBytes;
+    static constexpr int stages = 4;
+    static constexpr int box_rows = 32;           // rows of x per TMA box
+    static constexpr int warps = 16;              // sum warps: eight per piece, 64 columns each
+    static constexpr int threads = 128 + 32 * warps;
+    static constexpr int out = warps * 32 * 128;  // 32 rows x 128 bytes per sum warp, on their way out
 };
 
 // Wait for this thread's tensor-memory loads into v (the values are tied to the wait, so that
@@ -374,24 +374,25 @@ __device__ __forceinline__ void wait_ld16(uint32_t (&v)[16])
 
 }  // namespace
 
-template <int CG, bool F32>
-__global__ void __launch_bounds__(RingW<CG>::threads, 1)
+template <bool F32>
+__global__ void __launch_bounds__(RingW::threads, 1)
     group_gemm_fp8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                                const __grid_constant__ Group8Params p)
 {
-    using T = RingW<CG>;
-    constexpr int S = T::stages, NA = T::acc, BN = T::BN, HC = BN / T::groups;
+    using T = RingW;
+    constexpr int S = T::stages, BN = T::BN, HC = T::piece / 2;
     pdl_enter();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * T::stage);
-    uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + NA;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + NA);
+    unsigned char *sh_out = smem + S * T::stage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sh_out + T::out);
+    uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 4;  // [piece][buffer]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
     if (threadIdx.x == 0) {
@@ -399,77 +400,69 @@ __global__ void __launch_bounds__(RingW<CG>::threads, 1)
             mbar_init(full + i, 1);
             mbar_init(empty + i, 1);
         }
-        for (int i = 0; i < NA; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4 * T::groups * CG);
+            mbar_init(acc_empty + i, T::warps);  // the piece's sum warps in both CTAs
         }
         *abort_flag = 0;
         fence_mbar_init();
         tc::prefetch_map(&map_w);
         tc::prefetch_map(&map_x);
     }
-    if (warp == 1) tmem_alloc<CG>(tmem_slot, NA * BN);
-    const bool valid = build_table(p.offs, p.E, p.P, kTileM * CG, sh_offs, sh_tiles, sh_flag);
+    if (warp == 1) tmem_alloc<2>(tmem_slot, 2 * BN);
+    const bool valid = build_table(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles, sh_flag);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
-    if constexpr (CG == 2) cluster_sync();
-    else __syncthreads();
+    cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = uniform(*tmem_slot);
 
     const int n_tiles = (p.N + BN - 1) / BN;
     const int units = uniform(sh_tiles[p.E]) * n_tiles;
     const int nb = (p.K + kStep8 - 1) / kStep8;
-    const int u0 = blockIdx.x / CG, du = gridDim.x / CG;
+    const int u0 = blockIdx.x / 2, du = gridDim.x / 2;
     struct UnitW {
-        int e, row0, rows;  // the unit's rows (of both CTAs of a pair)
-        int n0, cols, half; // weight rows; how many of them this CTA loads
+        int e, row0, rows;  // the unit's rows (of both CTAs)
+        int n0;             // its first weight row
     };
     auto unit_of = [&](int u) {
         const int t = u / n_tiles;
-        const Tile x = find_tile(t, p.E, kTileM * CG, kTileM, sh_offs, sh_tiles);
+        const Tile x = find_tile(t, p.E, 2 * kTileM, kTileM, sh_offs, sh_tiles);
         UnitW r;
-        r.e = x.e;
-        r.row0 = x.row0;
-        r.rows = x.rows;
-        r.n0 = (u - t * n_tiles) * BN;
-        r.cols = min(BN, p.N - r.n0);
-        r.half = ((r.cols + CG - 1) / CG + 15) / 16 * 16;
+        r.e = uniform(x.e);
+        r.row0 = uniform(x.row0);
+        r.rows = uniform(x.rows);
+        r.n0 = uniform((u - t * n_tiles) * BN);
         return r;
     };
-    auto uniform_unit = [](UnitW x) {
-        x.e = uniform(x.e); x.row0 = uniform(x.row0); x.rows = uniform(x.rows);
-        x.n0 = uniform(x.n0); x.cols = uniform(x.cols); x.half = uniform(x.half);
-        return x;
-    };
+    // weight rows of piece j that one CTA loads: half the piece's, in steps of 16
+    auto half_of = [&](const UnitW &x, int j) { return (min(max(p.N - x.n0 - T::piece * j, 1), T::piece) + 31) / 32 * 16; };
     bool dead = false;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 0 && !p.skip_producer) {
             // -------------------------------------------------------- producer
             const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
             for (int u = u0; u < units && !dead; u += du) {
-                const UnitW x = uniform_unit(unit_of(u));
-                // boxes of x rows: this CTA's and, for a pair, both CTAs' (the leader expects them all)
+                const UnitW x = unit_of(u);
+                // boxes of x rows: this CTA's, and both CTAs' (the leader expects them all)
                 auto boxes_of = [&](int r) { return (min(max(x.rows - r * kTileM, 0), kTileM) + T::box_rows - 1) / T::box_rows; };
                 const int boxes = boxes_of(rank);
-                const uint32_t w_bytes = CG == 2 ? 128 * kChunkBytes : 256 * kChunkBytes;
-                uint32_t bytes = 0;
-                for (int r = 0; r < CG; ++r) bytes += boxes_of(r) * T::box_rows * kChunkBytes + w_bytes;
+                const uint32_t bytes = ((boxes_of(0) + boxes_of(1)) * T::box_rows + 4 * 64) * kChunkBytes;
+                const int w0 = x.n0 + (int)rank * half_of(x, 0), w1 = x.n0 + T::piece + (int)rank * half_of(x, 1);
                 for (int b = 0; b < nb; ++b, ++it) {
                     if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
-                    const uint32_t bar = CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
+                    const uint32_t bar = map_rank(full + s, 0);
                     if (one) {
                         if (leader) mbar_arrive_expect_tx(full + s, bytes);
                         for (int i = 0; i < boxes; ++i)
-                            load_2d<CG>(sa + i * T::box_rows * kChunkBytes, &map_x, b * kStep8,
-                                        x.row0 + (int)rank * kTileM + i * T::box_rows, bar);
-                        load_3d<CG>(sb, &map_w, b * kStep8, x.n0 + (int)rank * x.half, x.e, bar);
-                        if (CG == 1) load_3d<CG>(sb + 128 * kChunkBytes, &map_w, b * kStep8, x.n0 + 128, x.e, bar);
+                            load_2d<2>(sa + i * T::box_rows * kChunkBytes, &map_x, b * kStep8,
+                                       x.row0 + (int)rank * kTileM + i * T::box_rows, bar);
+                        load_3d<2>(sb, &map_w, b * kStep8, w0, x.e, bar);
+                        load_3d<2>(sb + 64 * kChunkBytes, &map_w, b * kStep8, w1, x.e, bar);
                     }
                     __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
@@ -487,36 +480,39 @@ __global__ void __launch_bounds__(RingW<CG>::threads, 1)
             int s = 0, a = 0;
             uint32_t ph = 0, pa = 1;
             for (int u = u0; u < units && !dead; u += du) {
-                const UnitW x = uniform_unit(unit_of(u));
-                const uint32_t idesc = idesc_e4m3(kTileM * CG, x.half * CG);
-                for (int b = 0; b < nb; ++b) {
-                    if (!warp_wait(acc_empty + a, pa, abort_flag, wl) || !warp_wait(full + s, ph, abort_flag, wl)) {
-                        dead = true;
-                        break;
-                    }
-                    tc::fence_after_sync();
+                const UnitW x = unit_of(u);
+                const uint32_t idesc[2] = {idesc_e4m3(2 * kTileM, 2 * half_of(x, 0)), idesc_e4m3(2 * kTileM, 2 * half_of(x, 1))};
+                for (int b = 0; b < nb && !dead; ++b) {
+                    if (!warp_wait(full + s, ph, abort_flag, wl)) { dead = true; break; }
                     const uint32_t sa = smem_u32(smem + s * T::stage);
-                    const uint64_t ad = tc::sw128_desc(sa), bd = tc::sw128_desc(sa + kABytes);
-                    if (one) {
+                    const uint64_t ad = tc::sw128_desc(sa);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_e4m3<CG>(tmem + (uint32_t)a * BN, ad + 2 * j, bd + 2 * j, idesc, j != 0);
-                        commit<CG>(empty + s);
-                        commit<CG>(acc_full + a);
+                    for (int j = 0; j < 2; ++j) {
+                        if (!warp_wait(acc_empty + 2 * j + a, pa, abort_flag, wl)) { dead = true; break; }
+                        tc::fence_after_sync();
+                        const uint64_t bd = tc::sw128_desc(sa + kABytes + j * 64 * kChunkBytes);
+                        if (one) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_e4m3<2>(tmem + (uint32_t)a * BN + j * T::piece, ad + 2 * i, bd + 2 * i, idesc[j], i != 0);
+                            commit<2>(acc_full + 2 * j + a);
+                            if (j == 1) commit<2>(empty + s);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
-                    if (++a == NA) { a = 0; pa ^= 1; }
+                    a ^= 1;
+                    if (a == 0) pa ^= 1;
                 }
             }
             if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
         }
     } else {
         // ------------------------------------------------------------ sums and epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int q = warp & 3, h = (warp - 4) >> 2;
-        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
-        const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : 0;
+        const int q = warp & 3, j = (warp - 4) >> 3, h = ((warp - 4) >> 2) & 1;  // lane quarter, piece, its half
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + j * T::piece + h * HC;
+        const uint32_t empty_bar = map_rank(acc_empty + 2 * j, 0);
+        unsigned char *tile = sh_out + (warp - 4) * 32 * 128;
         const int n_blocks128 = (p.N + 127) / 128;
         int a = 0;
         uint32_t pa = 0;
@@ -524,67 +520,94 @@ __global__ void __launch_bounds__(RingW<CG>::threads, 1)
             const UnitW x = unit_of(u);
             float2 sum[HC / 2];
 #pragma unroll
-            for (int j = 0; j < HC / 2; ++j) sum[j] = make_float2(0.f, 0.f);
-            const int mine = min(max(x.cols - h * HC, 0), HC);  // columns of this group in use
-            const int r = (int)rank * kTileM + 32 * q + lane;   // this thread's row of the unit
-            const bool live = r < x.rows;
-            const float *xs = p.xs + x.row0 + (live ? r : 0);
-            const float *ws = p.ws + ((int64_t)x.e * n_blocks128 + min((x.n0 + h * HC) / 128, n_blocks128 - 1)) * nb;
-            float xn = __ldg(xs), wn = __ldg(ws);
+            for (int i = 0; i < HC / 2; ++i) sum[i] = make_float2(0.f, 0.f);
+            const int first = (int)rank * kTileM + 32 * q;    // the warp's first row of the unit
+            const int live = min(max(x.rows - first, 0), 32);  // how many of its rows are the unit's
+            const float *xs = p.xs + x.row0 + (lane < live ? first + lane : 0);
+            const float *ws = p.ws + ((int64_t)x.e * n_blocks128 + min(x.n0 / 128 + j, n_blocks128 - 1)) * nb;
+            // the scales of this block and the next three (a load takes longer than a block)
+            float xn[4], wn[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xn[i] = i < nb ? __ldg(xs + i * p.ld_xs) : 0.f;
+                wn[i] = i < nb ? __ldg(ws + i) : 0.f;
+            }
             for (int b = 0; b < nb; ++b) {
-                const float f = xn * wn;
-                if (b + 1 < nb) {  // the next block's, while this one's sums are added
-                    xn = __ldg(xs + (int64_t)(b + 1) * p.ld_xs);
-                    wn = __ldg(ws + b + 1);
+                const float f = xn[0] * wn[0];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    xn[i] = xn[i + 1];
+                    wn[i] = wn[i + 1];
                 }
-                if (!warp_wait(acc_full + a, pa, abort_flag, wl)) { dead = true; break; }
+                if (b + 4 < nb) {
+                    xn[3] = __ldg(xs + (b + 4) * p.ld_xs);
+                    wn[3] = __ldg(ws + b + 4);
+                }
+                if (!warp_wait(acc_full + 2 * j + a, pa, abort_flag, wl)) { dead = true; break; }
                 tc::fence_after_sync();
-                if (mine > 0) {
-                    const uint32_t addr = lane_addr + (uint32_t)a * BN;
-                    uint32_t v[2][16];
-                    tc::ld16(addr, v[0]);
-                    wait_ld16(v[0]);
+                const uint32_t addr = lane_addr + (uint32_t)a * BN;
 #pragma unroll
-                    for (int c = 0; c < HC / 16; ++c) {
-                        if (c + 1 < HC / 16) tc::ld16(addr + 16 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) fma2(sum[8 * c + j], f, f, v[c & 1][2 * j], v[c & 1][2 * j + 1]);
-                        if (c + 1 < HC / 16) wait_ld16(v[(c + 1) & 1]);
+                for (int c = 0; c < HC / 16; ++c) {
+                    uint32_t v[16];
+                    tc::ld16(addr + 16 * c, v);
+                    wait_ld16(v);
+                    if (c == HC / 16 - 1) {  // read out: the tensor cores may have the buffer back
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster_relaxed(empty_bar + 8 * a);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) fma2(sum[8 * c + i], f, f, v[2 * i], v[2 * i + 1]);
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2) arrive_cluster_relaxed(empty_bar + 8 * a);
-                    else mbar_arrive(acc_empty + a);
-                }
-                if (++a == NA) { a = 0; pa ^= 1; }
+                a ^= 1;
+                if (a == 0) pa ^= 1;
             }
             if (dead) break;
-            if (live) {
-                const int64_t at = (int64_t)(x.row0 + r) * p.ld + x.n0 + h * HC;
-                if (p.vec) {  // 16 bytes at a time (N and the rows are multiples of them)
-                    if constexpr (F32) {
-                        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+            {
+                const int n0 = x.n0 + j * T::piece + h * HC;               // these 64 columns
+                const int mine = min(max(p.N - n0, 0), HC);               // how many of them exist
+                const int64_t at = (int64_t)(x.row0 + first) * p.ld + n0;  // their first element
+                if (p.vec) {
+                    // 128 bytes of each row at a time through shared memory (16-byte pieces swizzled by
+                    // the row, free of bank conflicts), so that a store instruction writes whole lines
+                    // of four rows instead of 16 bytes of 32
+                    constexpr int per = F32 ? 32 : 64;
+                    const int l8 = lane & 7, r4 = lane >> 3;
 #pragma unroll
-                        for (int j = 0; j < HC / 4; ++j)
-                            if (4 * j < mine) o[j] = make_float4(sum[2 * j].x, sum[2 * j].y, sum[2 * j + 1].x, sum[2 * j + 1].y);
-                    } else {
-                        uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at);
+                    for (int c = 0; c < HC; c += per) {
+                        if (c >= mine) break;
+                        __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < HC / 8; ++j)
-                            if (8 * j < mine)
-                                o[j] = make_uint4(bf16x2(sum[4 * j].x, sum[4 * j].y), bf16x2(sum[4 * j + 1].x, sum[4 * j + 1].y),
-                                                  bf16x2(sum[4 * j + 2].x, sum[4 * j + 2].y),
-                                                  bf16x2(sum[4 * j + 3].x, sum[4 * j + 3].y));
+                        for (int i = 0; i < 8; ++i) {
+                            uint4 o;
+                            if constexpr (F32) {
+                                const float2 s0 = sum[c / 2 + 2 * i], s1 = sum[c / 2 + 2 * i + 1];
+                                o = make_uint4(__float_as_uint(s0.x), __float_as_uint(s0.y), __float_as_uint(s1.x),
+                                               __float_as_uint(s1.y));
+                            } else {
+                                const float2 *t = sum + 4 * i;
+                                o = make_uint4(bf16x2(t[0].x, t[0].y), bf16x2(t[1].x, t[1].y), bf16x2(t[2].x, t[2].y),
+                                               bf16x2(t[3].x, t[3].y));
+                            }
+                            *reinterpret_cast<uint4 *>(tile + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
+                        }
+                        __syncwarp();
+                        const int col = c + l8 * (per / 8);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + r4;
+                            const uint4 o = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((l8 ^ (r & 7)) << 4));
+                            if (r < live && col < mine)
+                                *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + (at + r * p.ld + col) * (F32 ? 4 : 2)) = o;
+                        }
                     }
-                } else {
+                } else if (lane < live) {
 #pragma unroll
-                    for (int j = 0; j < HC; ++j)
-                        if (j < mine) {
-                            const float v = j & 1 ? sum[j / 2].y : sum[j / 2].x;
-                            if constexpr (F32) static_cast<float *>(p.out)[at + j] = v;
-                            else static_cast<__nv_bfloat16 *>(p.out)[at + j] = __float2bfloat16_rn(v);
+                    for (int i = 0; i < HC; ++i)
+                        if (i < mine) {
+                            const float v = i & 1 ? sum[i / 2].y : sum[i / 2].x;
+                            if constexpr (F32) static_cast<float *>(p.out)[at + lane * p.ld + i] = v;
+                            else static_cast<__nv_bfloat16 *>(p.out)[at + lane * p.ld + i] = __float2bfloat16_rn(v);
                         }
                 }
             }
@@ -596,9 +619,9 @@ __global__ void __launch_bounds__(RingW<CG>::threads, 1)
     // wind down; a cluster leaves together
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();
+    cluster_sync();
     tc::fence_after_sync();
-    if (warp == 1) tmem_dealloc<CG>(tmem, NA * BN);
+    if (warp == 1) tmem_dealloc<2>(tmem, 2 * BN);
 }
 
 namespace {
@@ -628,18 +651,18 @@ cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p,
     return cudaGetLastError();
 }
 
-template <int CG, bool F32>
+template <bool F32>
 cudaError_t launch_wide(const CUtensorMap &w, const CUtensorMap &x, const Group8Params &p, cudaStream_t s)
 {
-    using T = RingW<CG>;
-    auto kern = group_gemm_fp8_wide_kernel<CG, F32>;
-    const size_t smem = 1024 + T::stages * T::stage + 8 * (2 * T::stages + 2 * T::acc) + 16 + 4 * 2 * (size_t)(p.E + 1);
+    using T = RingW;
+    auto kern = group_gemm_fp8_wide_kernel<F32>;
+    const size_t smem = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 8) + 16 + 4 * 2 * (size_t)(p.E + 1);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int64_t units = (int64_t)((p.N + T::BN - 1) / T::BN) * (p.P / (kTileM * CG) + (p.E < p.P ? p.E : p.P));  // at most
-    int64_t grid = CG == 1 ? sm_count() : resident_clusters(kern, CG, T::threads, smem);
+    const int64_t units = (int64_t)((p.N + T::BN - 1) / T::BN) * (p.P / (2 * kTileM) + (p.E < p.P ? p.E : p.P));  // at most
+    int64_t grid = resident_clusters(kern, 2, T::threads, smem);
     if (units < grid) grid = units;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * CG), dim3(T::threads), smem, CG, s, w, x, p);
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), smem, 2, s, w, x, p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
@@ -669,14 +692,14 @@ cudaError_t launch_group_gemm_fp8(const GroupGemm8 &g, cudaStream_t s)
     const int bn = per <= 32 ? 32 : per <= 96 || g.N <= kTileM || 2 * pairs < sm_count() / 2 ? 128 : 256;
     CUtensorMap w, x;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    if (!make_tensor_map_3d(&w, u8, g.w, g.K, g.N, g.E, g.K, (uint64_t)g.K * g.N, kStep8, kTileM,
+    if (!make_tensor_map_3d(&w, u8, g.w, g.K, g.N, g.E, g.K, (uint64_t)g.K * g.N, kStep8, bn == 256 ? 64 : kTileM,
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_tensor_map_2d(&x, u8, g.x, g.K, g.P, g.ld_x, kStep8, bn == 32 ? Ring8<1, 32>::box_rows : Ring8<1, 128>::box_rows,
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     if (bn == 32) return g.out_f32 ? launch8<1, 32, true>(w, x, p, s) : launch8<1, 32, false>(w, x, p, s);
     if (bn == 128) return g.out_f32 ? launch8<1, 128, true>(w, x, p, s) : launch8<1, 128, false>(w, x, p, s);
-    return g.out_f32 ? launch_wide<2, true>(w, x, p, s) : launch_wide<2, false>(w, x, p, s);
+    return g.out_f32 ? launch_wide<true>(w, x, p, s) : launch_wide<false>(w, x, p, s);
 }
 
 }  // namespace ftmoe
