@@ -21,7 +21,7 @@ namespace {
 
 using namespace grp;
 
-constexpr int kThreadsG = 384;  // warps: 0 TMA, 1 MMA, 2 tail rows (wgrad), 3 idle, 4..11 epilogue
+constexpr int kThreadsG = 384;  // warps: 0 TMA, 1 MMA, 2 tail rows (wgrad), 3 units, 4..11 epilogue
 constexpr int kStep = 64;       // contraction steps per stage
 // Long sums into fp32 outputs are cut into parts of this many stages, added in registers: the
 // tensor cores truncate where an fp32 addition rounds, so that the error of one long
@@ -38,8 +38,9 @@ struct Ring {
     // rows of one TMA box of a row-major B operand: short boxes, so that a short tile loads no
     // more rows than it has (to within a box)
     static constexpr int box_rows = BN <= 32 ? 16 : 32;
-    // wgrad's output tiles on their way to TMA: two of 32 rows x 128 bytes per epilogue warp
-    static constexpr int extra = WG ? 8 * 2 * 4096 : 0;
+    // wgrad: 32 rows x 128 bytes of output per epilogue warp, on their way out. (Not by TMA: its
+    // stores, held back by the memory, held the loads behind them back too.)
+    static constexpr int extra = WG ? 8 * 4096 : 0;
     static constexpr int fit = (216 * 1024 - extra) / stage;
     static constexpr int stages = fit < 10 ? fit : 10;
 };
@@ -50,10 +51,11 @@ struct GroupParams {
     int M;                // size of the M axis
     int N;                // wgrad: size of the N axis
     int R;                // forward, dgrad: contraction length
-    void *out;            // forward, dgrad: [P][ld]
+    void *out;            // forward, dgrad: [P][ld]; wgrad: [E][M][N]
     int64_t ld;
     int accumulate;       // wgrad, fp32: add to what dw holds
     int split;            // CTAs (one cluster) that share a unit's contraction
+    int *counter;         // units handed out so far (zero at launch), or null: units go in turn
     int *status;
     uint64_t wait_ns;
     int skip_producer;
@@ -81,23 +83,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
     }
 }
 
-// TMA store of a 128-byte x 32-row tile (128-byte swizzle) of a stack of matrices, or its addition.
-__device__ __forceinline__ void store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2, bool add)
-{
-    if (add)
-        asm volatile(
-            "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                reinterpret_cast<uint64_t>(map)),
-            "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
-            : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                         reinterpret_cast<uint64_t>(map)),
-                     "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
-                     : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
 // One unit of work: a 128 x CG by (up to) BN tile of the output.
 struct Unit {
     int e, m0;        // expert, first M index of this CTA
@@ -112,7 +97,7 @@ struct Unit {
 template <int CG, int BN, bool A_MN, bool WG, bool F32>
 __global__ void __launch_bounds__(kThreadsG, 1)
     group_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                      const __grid_constant__ CUtensorMap map_c, const __grid_constant__ GroupParams p)
+                      const __grid_constant__ GroupParams p)
 {
     static_assert(!WG || A_MN, "wgrad reads both operands transposed");
     using T = Ring<CG, BN, WG>;
@@ -127,8 +112,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     unsigned char *extra = smem + S * T::stage;
     uint64_t *full = reinterpret_cast<uint64_t *>(extra + T::extra);
     uint64_t *empty = full + S, *tail = empty + S, *peer_tail = tail + S, *acc_full = peer_tail + S,
-             *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+             *acc_empty = acc_full + 2, *unit_full = acc_empty + 2, *unit_empty = unit_full + 2;
+    int *sh_unit = reinterpret_cast<int *>(unit_empty + 2);  // the next two units
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
@@ -147,12 +133,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
             mbar_init(acc_empty + i, 8 * CG);  // every epilogue warp
+            mbar_init(unit_full + i, 1);
+            mbar_init(unit_empty + i, CG * 10 + 1);  // the MMA warp and, in each CTA, producer, tail and epilogue warps
         }
         *abort_flag = 0;
         fence_mbar_init();
         tc::prefetch_map(&map_a);
         tc::prefetch_map(&map_b);
-        if (WG) tc::prefetch_map(&map_c);
     }
     if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
     const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles, sh_flag);
@@ -201,14 +188,62 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         return kSplit ? nb * (part + 1) / split : nb;
     };
     bool dead = false;
+    // The warp's next unit, or -1 after the last one. With a counter (wgrad, whose units cost as much
+    // as their expert has rows), the leader's unit warp hands them out, at most two ahead of the
+    // epilogue: whoever is done takes the next. Dealt out in turn, the largest experts' units ended
+    // last on some CTAs (65536 rows over 256 experts, Zipf: 622 us against 555). Forward and dgrad
+    // units cost about the same; there the counter gained nothing.
+    const bool counted = WG && p.counter;
+    const uint32_t unit_empty_bar = CG == 2 ? map_rank(unit_empty, 0) : 0;
+    int turn = 0;
+    auto next_unit = [&]() {
+        int u;
+        if (!counted) {
+            u = u0 + turn * du;
+        } else {
+            const int i = turn & 1;
+            if (!warp_wait(unit_full + i, (turn >> 1) & 1, abort_flag, wl)) { dead = true; return -1; }
+            u = uniform(*(volatile int *)(sh_unit + i));
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) arrive_cluster_relaxed(unit_empty_bar + 8 * i);
+                else mbar_arrive(unit_empty + i);
+            }
+        }
+        ++turn;
+        return u < units ? u : -1;
+    };
 
-    if (warp == 0) {
+    if (WG && warp == 3) {
+        // ------------------------------------------------------------ units
+        if (counted && leader) {
+            for (int n = 0; !dead; ++n) {
+                const int i = n & 1;
+                int u = u0;  // the first is this CTA's (or pair's) own
+                if (n > 0 && lane == 0) u = du + atomicAdd(p.counter, 1);
+                u = uniform(u);
+                if (!warp_wait(unit_empty + i, ((n >> 1) & 1) ^ 1, abort_flag, wl)) { dead = true; break; }
+                if (lane < CG) {
+                    if (CG == 2) {
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(sh_unit + i, lane)), "r"(u) : "memory");
+                        arrive_cluster(map_rank(unit_full + i, lane));
+                    } else {
+                        sh_unit[i] = u;
+                        mbar_arrive(unit_full + i);
+                    }
+                }
+                __syncwarp();
+                if (u >= units) break;
+            }
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+        }
+    } else if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (!p.skip_producer) {
             const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
-            for (int u = u0; u < units && !dead; u += du) {
+            for (int u; (u = next_unit()) >= 0 && !dead;) {
                 const Unit x = uniform_unit(unit_of(u));
                 const int nb = last_stage(x.R);
                 const int boxes = WG ? x.half / 64 : (x.half + T::box_rows - 1) / T::box_rows;
@@ -258,7 +293,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             const bool one = elect_one();
             int s = 0, ac = 0;
             uint32_t ph = 0;
-            for (int u = u0; u < units && !dead; u += du) {
+            for (int u; (u = next_unit()) >= 0 && !dead;) {
                 const Unit x = uniform_unit(unit_of(u));
                 const int b0 = first_stage(x.R), nb = last_stage(x.R);
                 const uint32_t idesc = idesc_bf16(kTileM * CG, x.half * CG, A_MN, WG);
@@ -297,7 +332,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         // operands (also where the neighbour's values are not finite).
         int s = 0;
         uint32_t phases = 0;  // bit s: parity of tail[s]
-        for (int u = u0; u < units && !dead; u += du) {
+        for (int u; (u = next_unit()) >= 0 && !dead;) {
             const Unit x = unit_of(u);
             const int nb = (x.R + kStep - 1) / kStep;
             if (nb == 0) continue;
@@ -335,9 +370,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
         const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : 0;
-        unsigned char *stage_out = extra + (warp - 4) * 2 * 4096;  // wgrad: this warp's two tiles
-        int ac = 0, so = 0;
-        for (int u = u0; u < units && !dead; u += du) {
+        unsigned char *tile = extra + (warp - 4) * 4096;  // wgrad: 32 rows x 128 bytes
+        int ac = 0;
+        for (int u; (u = next_unit()) >= 0 && !dead;) {
             const Unit x = unit_of(u);
             const int nb = last_stage(x.R) - first_stage(x.R);
             const int parts = F32 ? (nb + kPartStages - 1) / kPartStages : nb > 0;
@@ -348,14 +383,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             // W columns at offset c of this half, as sums, to where they go
             auto emit = [&](int c, const float (&v)[W]) {
                 if constexpr (WG) {
-                    // lane = row n of dw, columns k: one row of 128 bytes per lane, its 16-byte
-                    // pieces swizzled as the TMA store expects them (and free of bank conflicts)
-                    constexpr int per = F32 ? 32 : 64;  // columns of one 128-byte row
-                    unsigned char *tile = stage_out + (so & 1) * 4096;
-                    if (c % per == 0) {
-                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        __syncwarp();
-                    }
+                    // lane = row n of dw, columns k: 128 bytes of each row at a time through shared
+                    // memory (16-byte pieces swizzled by the row, free of bank conflicts), so that a
+                    // store instruction writes whole lines of four rows
+                    constexpr int per = F32 ? 32 : 64;  // columns of 128 bytes
 #pragma unroll
                     for (int i = 0; i < (F32 ? 8 : 4); ++i) {
                         uint4 o;
@@ -368,12 +399,31 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                         const int piece = i + (F32 ? 0 : (c % per) / 8);
                         *reinterpret_cast<uint4 *>(tile + lane * 128 + ((piece ^ (lane & 7)) << 4)) = o;
                     }
-                    if (c % per == per - W) {
-                        fence_proxy_async_smem();
+                    if (c % per == per - W || c + W >= mine) {  // the 128 bytes, or what there is of them, are complete
                         __syncwarp();
-                        const int k = x.col0 + h * HC + c - c % per, n = x.m0 + 32 * q;
-                        if (lane == 0 && k < p.N && n < p.M) store_3d(&map_c, tile, k, n, x.e, F32 && p.accumulate);
-                        ++so;
+                        const int l8 = lane & 7, col = c / per * per + l8 * (per / 8), n0 = x.m0 + 32 * q;
+                        char *o = static_cast<char *>(p.out) +
+                                  (((int64_t)x.e * p.M + n0) * p.N + x.col0 + h * HC + col) * (F32 ? 4 : 2);
+                        const int64_t row = (int64_t)p.N * (F32 ? 4 : 2);
+                        const int rows = col < mine ? min(p.M - n0, 32) : 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3);
+                            uint4 w = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((l8 ^ (r & 7)) << 4));
+                            if (r < rows) {
+                                if constexpr (F32) {
+                                    if (p.accumulate) {
+                                        const float4 was = *reinterpret_cast<const float4 *>(o + r * row);
+                                        w = make_uint4(__float_as_uint(__uint_as_float(w.x) + was.x),
+                                                       __float_as_uint(__uint_as_float(w.y) + was.y),
+                                                       __float_as_uint(__uint_as_float(w.z) + was.z),
+                                                       __float_as_uint(__uint_as_float(w.w) + was.w));
+                                    }
+                                }
+                                *reinterpret_cast<uint4 *>(o + r * row) = w;
+                            }
+                        }
+                        __syncwarp();
                     }
                 } else if (kSplit && split > 1) {
                     // (every stage of the ring has been read by the time the last sums are complete)
@@ -423,15 +473,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                     emit(c, f);
                 }
             }
-            if (WG && !F32 && mine % 64 && mine % 64 <= 32) {  // a half-filled last tile
-                fence_proxy_async_smem();
-                __syncwarp();
-                const int k = x.col0 + h * HC + mine / 64 * 64, n = x.m0 + 32 * q;
-                if (lane == 0 && n < p.M) store_3d(&map_c, stage_out + (so & 1) * 4096, k, n, x.e, false);
-                ++so;
-            }
         }
-        if (WG && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     }
 
@@ -456,11 +498,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 namespace {
 
 template <int CG, int BN, bool A_MN, bool WG, bool F32>
-cudaError_t launch(const CUtensorMap (&maps)[3], GroupParams &p, int64_t max_units, cudaStream_t s)
+cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_units, cudaStream_t s)
 {
     using T = Ring<CG, BN, WG>;
     auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32>;
-    const size_t smem = 1024 + T::stages * T::stage + T::extra + 8 * (4 * T::stages + 4) + 16 + 4 * 2 * (size_t)(p.E + 1);
+    const size_t smem = 1024 + T::stages * T::stage + T::extra + 8 * (4 * T::stages + 8) + 24 + 4 * 2 * (size_t)(p.E + 1);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // Few units: the CTAs of a cluster share one unit's contraction, at least two stages each.
@@ -470,16 +512,21 @@ cudaError_t launch(const CUtensorMap (&maps)[3], GroupParams &p, int64_t max_uni
     int64_t grid = p.split > 1 ? max_units : CG == 1 ? sm_count() : resident_clusters(kern, CG, kThreadsG, smem);
     if (max_units < grid) grid = max_units;
     if (grid < 1) grid = 1;
+    if (WG && p.E > 1 && max_units > 4 * grid) {  // units of unlike cost, several each
+        const cudaError_t me = cudaMemsetAsync(p.status + 16, 0, sizeof(int), s);
+        if (me != cudaSuccess) return me;
+        p.counter = p.status + 16;
+    }
     const int cluster = CG * p.split;
     const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(kThreadsG), smem, cluster, s, maps[0],
-                                          maps[1], maps[2], p);
+                                          maps[1], p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
 }
 
 template <int CG, int BN, bool A_MN, bool WG>
-cudaError_t launch_typed(const GroupGemm &g, const CUtensorMap (&maps)[3], GroupParams &p, cudaStream_t s)
+cudaError_t launch_typed(const GroupGemm &g, const CUtensorMap (&maps)[2], GroupParams &p, cudaStream_t s)
 {
     const int64_t m_tiles = (p.M + kTileM * CG - 1) / (kTileM * CG);
     const int64_t tiles = WG ? (int64_t)g.E * ((p.N + BN - 1) / BN) : g.P / BN + (g.E < g.P ? g.E : g.P);
@@ -510,20 +557,16 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     const int bn = wg ? 256 : per <= 32 ? 32 : per <= 96 || 2 * pairs < sm_count() / 2 ? 128 : 256;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap maps[3];
+    CUtensorMap maps[2];
     bool ok;
-    if (wg) {  // A: dy [P][N] read along n; B: x [P][K] read along k; C: dw
+    if (wg) {  // A: dy [P][N] read along n; B: x [P][K] read along k
         ok = make_tensor_map_2d(&maps[0], bf, g.dy, g.N, g.P, 2 * (uint64_t)g.ld_dy, 64, kStep, sw) &&
-             make_tensor_map_2d(&maps[1], bf, g.x, g.K, g.P, 2 * (uint64_t)g.ld_x, 64, kStep, sw) &&
-             make_tensor_map_3d(&maps[2], g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf, g.out, g.K, g.N, g.E,
-                                (g.out_f32 ? 4 : 2) * (uint64_t)g.K, (g.out_f32 ? 4 : 2) * (uint64_t)g.K * g.N,
-                                g.out_f32 ? 32 : 64, 32, sw);
+             make_tensor_map_2d(&maps[1], bf, g.x, g.K, g.P, 2 * (uint64_t)g.ld_x, 64, kStep, sw);
     } else {   // A: w [E][N][K]; B: x [P][K] or dy [P][N]
         ok = make_tensor_map_3d(&maps[0], bf, g.w, g.K, g.N, g.E, 2 * (uint64_t)g.K, 2 * (uint64_t)g.K * g.N, 64,
                                 fw ? kTileM : kStep, sw) &&
              make_tensor_map_2d(&maps[1], bf, fw ? g.x : g.dy, fw ? g.K : g.N, g.P, 2 * (uint64_t)(fw ? g.ld_x : g.ld_dy), 64,
                                 bn <= 32 ? Ring<1, 32, false>::box_rows : Ring<1, 128, false>::box_rows, sw);
-        maps[2] = maps[1];  // (not used)
     }
     if (!ok) return cudaErrorInvalidValue;
     const bool pair = p.M > kTileM;
