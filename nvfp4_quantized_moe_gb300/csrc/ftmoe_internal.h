@@ -157,7 +157,9 @@ bool make_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *ba
                         uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
 
 // The same for a stack of `mats` matrices mat_bytes apart (boxes lie inside one matrix; what a box
-// reaches beyond its matrix reads as zero).
+// reaches beyond its matrix reads as zero). Lines come into L2 in pairs: a 128-byte wide box walks
+// along the rows, and its next step reads the other half (64 decode rows over 256 experts: 152 us
+// with single lines, 144 with pairs).
 bool make_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t mats, uint64_t row_bytes, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_rows,
                         CUtensorMapSwizzle swz);
@@ -247,32 +249,52 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
-// Clusters of `cluster` CTAs of a kernel that can run at once: the grid of a persistent kernel. A
-// die's SMs need not divide into whole clusters, and a cluster beyond this number would start
-// only when another one ends. Looked up once per kernel and device (the answer is the device's).
-template <typename... KArgs>
-int resident_clusters(void (*kern)(KArgs...), int cluster, int threads, size_t smem)
-{
-    static int cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count() / cluster;
-    if (cache[dev] == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(cluster * sm_count());
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = cluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = sm_count() / cluster;
-        cache[dev] = n < sm_count() / cluster ? n : sm_count() / cluster;
+// The dynamic shared memory that one kernel may be launched with (a static per kernel), raised when
+// a launch needs more than an earlier one did on the same device.
+struct SharedMemoryLimit {
+    size_t raised[64] = {};
+    template <typename Kernel>
+    cudaError_t raise(Kernel *kern, size_t bytes)
+    {
+        int dev = 0;
+        const cudaError_t de = cudaGetDevice(&dev);
+        if (de != cudaSuccess) return de;
+        if (dev >= 0 && dev < 64 && raised[dev] >= bytes) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess && dev >= 0 && dev < 64) raised[dev] = bytes;
+        return e;
     }
-    return cache[dev];
-}
+};
+// Clusters of `cluster` CTAs (up to 8) of a kernel that can run at once: the grid of a persistent
+// kernel. A die's SMs need not divide into whole clusters, and a cluster beyond this number would
+// start only when another one ends: 152 SMs hold 76 pairs, but 36 clusters of four and 15 of eight.
+// A static per kernel (and shared memory size); the answer is looked up once per device.
+struct ClusterLimit {
+    int found[64][9] = {};
+    template <typename Kernel>
+    int get(Kernel *kern, int cluster, int threads, size_t smem)
+    {
+        int dev = 0;
+        if (cluster <= 1) return sm_count();
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || cluster > 8) return sm_count() / cluster;
+        if (found[dev][cluster] == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(cluster * sm_count());
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = cluster;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = sm_count() / cluster;
+            found[dev][cluster] = n < sm_count() / cluster ? n : sm_count() / cluster;
+        }
+        return found[dev][cluster];
+    }
+};
 // launch_pdl inside a function returning cudaError_t: return the launch error, if any.
 #define FT_LAUNCH(...)                                                                                         \
     do {                                                                                                       \

@@ -42,7 +42,8 @@ struct Ring {
     // stores, held back by the memory, held the loads behind them back too.)
     static constexpr int extra = WG ? 8 * 4096 : 0;
     static constexpr int fit = (216 * 1024 - extra) / stage;
-    static constexpr int stages = fit < 10 ? fit : 10;
+    // (eight keep memory busy; with ten a decode step of 64 tokens took 152 us, with eight 142)
+    static constexpr int stages = fit < 8 ? fit : 8;
 };
 
 struct GroupParams {
@@ -106,7 +107,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     constexpr bool kSplit = CG == 1 && !WG;
     constexpr int HC = BN / 2;                 // columns of one half's epilogue warps
     constexpr int W = HC < 32 ? HC : 32;       // columns per tensor-memory load
-    pdl_enter();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *extra = smem + S * T::stage;
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         tc::prefetch_map(&map_b);
     }
     if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
+    pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
     const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles, sh_flag);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
@@ -503,13 +504,17 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
     using T = Ring<CG, BN, WG>;
     auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32>;
     const size_t smem = 1024 + T::stages * T::stage + T::extra + 8 * (4 * T::stages + 8) + 24 + 4 * 2 * (size_t)(p.E + 1);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SharedMemoryLimit limit;
+    const cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
-    // Few units: the CTAs of a cluster share one unit's contraction, at least two stages each.
+    static ClusterLimit clusters;
+    // Few units: the CTAs of a cluster share one unit's contraction, at least two stages each, as
+    // long as all clusters run at once.
     p.split = 1;
     if (CG == 1 && !WG)
-        while (p.split < 8 && 2 * p.split * max_units <= sm_count() && p.R >= 4 * kStep * p.split) p.split *= 2;
-    int64_t grid = p.split > 1 ? max_units : CG == 1 ? sm_count() : resident_clusters(kern, CG, kThreadsG, smem);
+        while (p.split < 8 && p.R >= 4 * kStep * p.split && max_units <= clusters.get(kern, 2 * p.split, kThreadsG, smem))
+            p.split *= 2;
+    int64_t grid = p.split > 1 ? max_units : clusters.get(kern, CG, kThreadsG, smem);
     if (max_units < grid) grid = max_units;
     if (grid < 1) grid = 1;
     if (WG && p.E > 1 && max_units > 4 * grid) {  // units of unlike cost, several each
@@ -551,10 +556,14 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     p.M = g.form == kGroupDgrad ? g.K : g.N;
     p.N = g.K;
     p.R = fw ? g.K : g.N;
-    // rows per expert that has any, at most: picks the tile's extent along the rows
+    // The tile's extent along the rows, by the rows per expert that has any. Measured on 256 experts
+    // of 1024 x 2048 (forward, us, with 32 / 128 / 256 = a pair of CTAs): 12 rows 162 / 165 / 165, 32
+    // rows 184 / 171 / 170, 96 rows 403 / 191 / 185, 256 rows 959 / 328 / 235. Where the pairs' tiles
+    // leave most SMs idle, smaller tiles and a shared contraction win: one expert of 2048 x 2048 with
+    // 192 rows 11.9 / 9.6 / 13.1.
     const int64_t per = g.P / (g.E < g.P ? g.E : g.P);
     const int64_t pairs = (p.M + 255) / 256 * (g.P / 256 + (g.E < g.P ? g.E : g.P));
-    const int bn = wg ? 256 : per <= 32 ? 32 : per <= 96 || 2 * pairs < sm_count() / 2 ? 128 : 256;
+    const int bn = wg ? 256 : per <= 24 ? 32 : p.M <= kTileM || 4 * pairs < sm_count() ? 128 : 256;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap maps[2];
@@ -569,15 +578,15 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
                                 bn <= 32 ? Ring<1, 32, false>::box_rows : Ring<1, 128, false>::box_rows, sw);
     }
     if (!ok) return cudaErrorInvalidValue;
-    const bool pair = p.M > kTileM;
-    if (wg) return pair ? launch_typed<2, 256, true, true>(g, maps, p, s) : launch_typed<1, 256, true, true>(g, maps, p, s);
+    if (wg)
+        return p.M > kTileM ? launch_typed<2, 256, true, true>(g, maps, p, s) : launch_typed<1, 256, true, true>(g, maps, p, s);
     if (fw) {
         if (bn == 32) return launch_typed<1, 32, false, false>(g, maps, p, s);
-        if (bn == 128 || !pair) return launch_typed<1, 128, false, false>(g, maps, p, s);
+        if (bn == 128) return launch_typed<1, 128, false, false>(g, maps, p, s);
         return launch_typed<2, 256, false, false>(g, maps, p, s);
     }
     if (bn == 32) return launch_typed<1, 32, true, false>(g, maps, p, s);
-    if (bn == 128 || !pair) return launch_typed<1, 128, true, false>(g, maps, p, s);
+    if (bn == 128) return launch_typed<1, 128, true, false>(g, maps, p, s);
     return launch_typed<2, 256, true, false>(g, maps, p, s);
 }
 

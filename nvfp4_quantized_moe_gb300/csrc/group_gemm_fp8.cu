@@ -21,15 +21,15 @@ using namespace grp;
 constexpr int kThreads8 = 384;  // warps: 0 TMA, 1 MMA, 2-3 scales, 4..11 sums and epilogue
 constexpr int kStep8 = 128;     // contraction steps per stage: one scale block
 
-// Tile variants, as in group_gemm.cu.
-template <int CG, int BN>
+// Tiles of up to BN rows.
+template <int BN>
 struct Ring8 {
-    static constexpr int b_bytes = BN / CG * kChunkBytes;
+    static constexpr int b_bytes = BN * kChunkBytes;
     static constexpr int stage = kABytes + b_bytes;
     static constexpr int fit = 208 * 1024 / stage;
-    static constexpr int stages = fit < 10 ? fit : 10;
+    static constexpr int stages = fit < 8 ? fit : 8;
     static constexpr int box_rows = BN <= 32 ? 16 : 32;
-    static constexpr int acc = BN >= 256 ? 2 : BN >= 128 ? 4 : 8;  // partial-sum buffers in tensor memory
+    static constexpr int acc = BN >= 128 ? 4 : 8;  // partial-sum buffers in tensor memory
     static constexpr int slots = 8;                  // scale slots in shared memory
 };
 
@@ -83,21 +83,19 @@ __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N)
 }
 
 struct Unit8 {
-    int e, m0, row0, rows, half;
+    int e, m0, row0, rows, cols;  // cols: rows in whole MMA columns
 };
 
 }  // namespace
 
-template <int CG, int BN, bool F32>
+template <int BN, bool F32>
 __global__ void __launch_bounds__(kThreads8, 1)
     group_gemm_fp8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                           const __grid_constant__ Group8Params p)
 {
-    using T = Ring8<CG, BN>;
+    using T = Ring8<BN>;
     constexpr int S = T::stages, NA = T::acc, NS = T::slots;
-    constexpr bool kSplit = CG == 1;
     constexpr int HC = BN / 2;  // columns of one half's warps
-    pdl_enter();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *sh_scale = reinterpret_cast<float *>(smem + S * T::stage);  // [NS][BN]
@@ -109,8 +107,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const bool leader = rank == 0;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
@@ -119,7 +115,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         }
         for (int i = 0; i < NA; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 8 * CG);
+            mbar_init(acc_empty + i, 8);  // every sum warp
         }
         for (int i = 0; i < NS; ++i) {
             mbar_init(sc_full + i, 1);
@@ -130,34 +126,34 @@ __global__ void __launch_bounds__(kThreads8, 1)
         tc::prefetch_map(&map_w);
         tc::prefetch_map(&map_x);
     }
-    if (warp == 1) tmem_alloc<CG>(tmem_slot, NA * BN);
+    if (warp == 1) tmem_alloc<1>(tmem_slot, NA * BN);
+    pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
     const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles, sh_flag);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
-    if constexpr (CG == 2) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = uniform(*tmem_slot);
 
-    const int m_tiles = (p.N + kTileM * CG - 1) / (kTileM * CG);
+    const int m_tiles = (p.N + kTileM - 1) / kTileM;
     const int units = uniform(sh_tiles[p.E]) * m_tiles;
-    const int split = kSplit ? p.split : 1, part = kSplit ? (int)(blockIdx.x % split) : 0;
+    const int split = p.split, part = (int)(blockIdx.x % split);
     const int nblocks = (p.K + kStep8 - 1) / kStep8;
     const int b0 = nblocks * part / split, nb = nblocks * (part + 1) / split;  // this CTA's blocks
-    const int u0 = blockIdx.x / (CG * split), du = gridDim.x / (CG * split);
+    const int u0 = blockIdx.x / split, du = gridDim.x / split;
     auto unit_of = [&](int u) {
         const int t = u / m_tiles;
-        const Tile x = find_tile(t, p.E, BN, 16 * CG, sh_offs, sh_tiles);
+        const Tile x = find_tile(t, p.E, BN, 16, sh_offs, sh_tiles);
         Unit8 r;
         r.e = x.e;
-        r.m0 = ((u - t * m_tiles) * CG + (int)rank) * kTileM;
+        r.m0 = (u - t * m_tiles) * kTileM;
         r.row0 = x.row0;
         r.rows = x.rows;
-        r.half = ((x.rows + CG - 1) / CG + 15) / 16 * 16;
+        r.cols = (x.rows + 15) / 16 * 16;
         return r;
     };
     auto uniform_unit = [](Unit8 x) {
-        x.e = uniform(x.e); x.m0 = uniform(x.m0); x.row0 = uniform(x.row0); x.rows = uniform(x.rows); x.half = uniform(x.half);
+        x.e = uniform(x.e); x.m0 = uniform(x.m0); x.row0 = uniform(x.row0); x.rows = uniform(x.rows); x.cols = uniform(x.cols);
         return x;
     };
     bool dead = false;
@@ -170,7 +166,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
             uint32_t ph = 1;
             for (int u = u0; u < units && !dead; u += du) {
                 const Unit8 x = uniform_unit(unit_of(u));
-                const int boxes = (x.half + T::box_rows - 1) / T::box_rows;
+                const int boxes = (x.cols + T::box_rows - 1) / T::box_rows;
                 const uint32_t bytes = kABytes + boxes * T::box_rows * kChunkBytes;
                 for (int b = b0; b < nb; ++b, ++it) {
                     if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
@@ -200,7 +196,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
         uint32_t ph = 0, pa = 1;
         for (int u = u0; u < units && !dead; u += du) {
             const Unit8 x = uniform_unit(unit_of(u));
-            const uint32_t idesc = idesc_e4m3(kTileM, x.half);
+            const uint32_t idesc = idesc_e4m3(kTileM, x.cols);
             for (int b = b0; b < nb; ++b) {
                 if (!warp_wait(acc_empty + a, pa, abort_flag, wl) || !warp_wait(full + s, ph, abort_flag, wl)) {
                     dead = true;
@@ -255,7 +251,6 @@ __global__ void __launch_bounds__(kThreads8, 1)
         // thread = TMEM lane = weight row; columns [h * HC, h * HC + HC) of the tile
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
-        const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : 0;
         int a = 0, it = 0;
         uint32_t pa = 0;
         for (int u = u0; u < units && !dead; u += du) {
@@ -289,15 +284,14 @@ __global__ void __launch_bounds__(kThreads8, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if (CG == 2) arrive_cluster_relaxed(empty_bar + 8 * a);
-                    else mbar_arrive(acc_empty + a);
+                    mbar_arrive(acc_empty + a);
                     mbar_arrive(sc_empty + slot);
                 }
                 if (++a == NA) { a = 0; pa ^= 1; }
             }
             if (dead) break;
             const int m = x.m0 + 32 * q + lane;
-            if (kSplit && split > 1) {
+            if (split > 1) {
                 // (every stage of the ring has been read by the time the last sums are complete)
                 float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
@@ -321,19 +315,16 @@ __global__ void __launch_bounds__(kThreads8, 1)
     // wind down; a cluster leaves together
     tc::fence_before_sync();
     __syncthreads();
-    if constexpr (kSplit) {
-        if (split > 1) {
-            cluster_sync();
-            if (u0 < units) {
-                const Unit8 x = unit_of(u0);
-                add_parts<F32>(reinterpret_cast<const float *>(smem), x.rows, x.m0, p.N, x.row0, p.out, p.ld, split, part);
-            }
-            cluster_sync();
+    if (split > 1) {
+        cluster_sync();
+        if (u0 < units) {
+            const Unit8 x = unit_of(u0);
+            add_parts<F32>(reinterpret_cast<const float *>(smem), x.rows, x.m0, p.N, x.row0, p.out, p.ld, split, part);
         }
+        cluster_sync();
     }
-    if constexpr (CG == 2) cluster_sync();
     tc::fence_after_sync();
-    if (warp == 1) tmem_dealloc<CG>(tmem, NA * BN);
+    if (warp == 1) tmem_dealloc<1>(tmem, NA * BN);
 }
 
 // ---------------------------------------------------------------- many rows per expert
@@ -381,7 +372,6 @@ __global__ void __launch_bounds__(RingW::threads, 1)
 {
     using T = RingW;
     constexpr int S = T::stages, BN = T::BN, HC = T::piece / 2;
-    pdl_enter();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *sh_out = smem + S * T::stage;
@@ -410,6 +400,7 @@ __global__ void __launch_bounds__(RingW::threads, 1)
         tc::prefetch_map(&map_x);
     }
     if (warp == 1) tmem_alloc<2>(tmem_slot, 2 * BN);
+    pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
     const bool valid = build_table(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles, sh_flag);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
@@ -626,26 +617,27 @@ __global__ void __launch_bounds__(RingW::threads, 1)
 
 namespace {
 
-template <int CG, int BN, bool F32>
+template <int BN, bool F32>
 cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p, cudaStream_t s)
 {
-    using T = Ring8<CG, BN>;
-    auto kern = group_gemm_fp8_kernel<CG, BN, F32>;
+    using T = Ring8<BN>;
+    auto kern = group_gemm_fp8_kernel<BN, F32>;
     const size_t smem = 1024 + T::stages * T::stage + 4 * T::slots * BN +
                         8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) + 16 + 4 * 2 * (size_t)(p.E + 1);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SharedMemoryLimit limit;
+    const cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
-    const int64_t m_tiles = (p.N + kTileM * CG - 1) / (kTileM * CG);
+    const int64_t m_tiles = (p.N + kTileM - 1) / kTileM;
     const int64_t units = m_tiles * (p.P / BN + (p.E < p.P ? p.E : p.P));  // at most
-    // Few units: the CTAs of a cluster share one unit's contraction, at least two blocks each.
+    static ClusterLimit clusters;
+    // Few units: the CTAs of a cluster share one unit's contraction, at least two blocks each, as
+    // long as all clusters run at once.
     p.split = 1;
-    if (CG == 1)
-        while (p.split < 8 && 2 * p.split * units <= sm_count() && p.K >= 4 * kStep8 * p.split) p.split *= 2;
-    int64_t grid = p.split > 1 ? units : CG == 1 ? sm_count() : resident_clusters(kern, CG, kThreads8, smem);
+    while (p.split < 8 && p.K >= 4 * kStep8 * p.split && units <= clusters.get(kern, 2 * p.split, kThreads8, smem)) p.split *= 2;
+    int64_t grid = p.split > 1 ? units : sm_count();
     if (units < grid) grid = units;
     if (grid < 1) grid = 1;
-    const int cluster = CG * p.split;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(kThreads8), smem, cluster, s, w, x, p);
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * p.split), dim3(kThreads8), smem, p.split, s, w, x, p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
@@ -657,10 +649,12 @@ cudaError_t launch_wide(const CUtensorMap &w, const CUtensorMap &x, const Group8
     using T = RingW;
     auto kern = group_gemm_fp8_wide_kernel<F32>;
     const size_t smem = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 8) + 16 + 4 * 2 * (size_t)(p.E + 1);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SharedMemoryLimit limit;
+    const cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)((p.N + T::BN - 1) / T::BN) * (p.P / (2 * kTileM) + (p.E < p.P ? p.E : p.P));  // at most
-    int64_t grid = resident_clusters(kern, 2, T::threads, smem);
+    static ClusterLimit clusters;
+    int64_t grid = clusters.get(kern, 2, T::threads, smem);
     if (units < grid) grid = units;
     const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), smem, 2, s, w, x, p);
     if (le != cudaSuccess) return le;
@@ -687,18 +681,23 @@ cudaError_t launch_group_gemm_fp8(const GroupGemm8 &g, cudaStream_t s)
     p.vec = g.N % (g.out_f32 ? 4 : 8) == 0 && g.ld_out % (g.out_f32 ? 4 : 8) == 0;
     p.status = g.status;
     injected_stall(&p.wait_ns, &p.skip_producer);
-    const int64_t per = g.P / (g.E < g.P ? g.E : g.P);  // rows per expert that has any
-    const int64_t pairs = (g.N + 255) / 256 * (g.P / 256 + (g.E < g.P ? g.E : g.P));
-    const int bn = per <= 32 ? 32 : per <= 96 || g.N <= kTileM || 2 * pairs < sm_count() / 2 ? 128 : 256;
+    // The tile, by the rows per expert that has any. Measured on 256 experts of 1024 x 2048 (us, with 32
+    // or 128 rows along N / 256 rows along M): 12 rows 88 / 87 / 126, 32 rows 114 / 96 / 138, 96 rows
+    // 247 / 118 / 154, 128 rows 319 / 159 / 158, 512 rows 1142 / 470 / 396. Where the wide tiles
+    // leave most SMs idle, smaller tiles and a shared contraction win: one expert of 2048 x 2048 with
+    // 256 rows 8.4 / 8.7 / 12.8.
+    const int64_t per = g.P / (g.E < g.P ? g.E : g.P);
+    const int64_t pairs = (int64_t)(g.N + 255) / 256 * (g.P / 256 + (g.E < g.P ? g.E : g.P));
+    const int bn = per <= 24 ? 32 : per < 128 || g.N <= kTileM || 4 * pairs < sm_count() ? 128 : 256;
     CUtensorMap w, x;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (!make_tensor_map_3d(&w, u8, g.w, g.K, g.N, g.E, g.K, (uint64_t)g.K * g.N, kStep8, bn == 256 ? 64 : kTileM,
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_tensor_map_2d(&x, u8, g.x, g.K, g.P, g.ld_x, kStep8, bn == 32 ? Ring8<1, 32>::box_rows : Ring8<1, 128>::box_rows,
+        !make_tensor_map_2d(&x, u8, g.x, g.K, g.P, g.ld_x, kStep8, bn == 32 ? Ring8<32>::box_rows : Ring8<128>::box_rows,
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    if (bn == 32) return g.out_f32 ? launch8<1, 32, true>(w, x, p, s) : launch8<1, 32, false>(w, x, p, s);
-    if (bn == 128) return g.out_f32 ? launch8<1, 128, true>(w, x, p, s) : launch8<1, 128, false>(w, x, p, s);
+    if (bn == 32) return g.out_f32 ? launch8<32, true>(w, x, p, s) : launch8<32, false>(w, x, p, s);
+    if (bn == 128) return g.out_f32 ? launch8<128, true>(w, x, p, s) : launch8<128, false>(w, x, p, s);
     return g.out_f32 ? launch_wide<true>(w, x, p, s) : launch_wide<false>(w, x, p, s);
 }
 
