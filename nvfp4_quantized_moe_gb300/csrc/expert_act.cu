@@ -201,15 +201,27 @@ __global__ void __launch_bounds__(kActThreads)
             sum = fmaf(d, gs * u, sum);
         };
         if constexpr (VEC) {
-            for (int c = 8 * lane; c < I; c += 256) {
-                float g[8], u[8], d[8];
-                load8<false>(gr, c, g);
-                load8<false>(ur, c, u);
-                load8<false>(dr, c, d);
+            for (int c = 8 * lane; c < I; c += 512) {  // two steps' loads in flight together
+                uint4 q[2][3];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) one(g[i], u[i], d[i], g[i], u[i]);
-                *reinterpret_cast<uint4 *>(og + c) = pack8(g);
-                *reinterpret_cast<uint4 *>(ou + c) = pack8(u);
+                for (int k = 0; k < 2; ++k) {
+                    if (c + 256 * k >= I) break;
+                    q[k][0] = ldg_nc_v4(gr + c + 256 * k);
+                    q[k][1] = ldg_nc_v4(ur + c + 256 * k);
+                    q[k][2] = ldg_nc_v4(dr + c + 256 * k);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (c + 256 * k >= I) break;
+                    float g[8], u[8], d[8];
+                    unpack8(q[k][0], g);
+                    unpack8(q[k][1], u);
+                    unpack8(q[k][2], d);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) one(g[i], u[i], d[i], g[i], u[i]);
+                    *reinterpret_cast<uint4 *>(og + c + 256 * k) = pack8(g);
+                    *reinterpret_cast<uint4 *>(ou + c + 256 * k) = pack8(u);
+                }
             }
         } else {
             for (int c = lane; c < I; c += 32) {

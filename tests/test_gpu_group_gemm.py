@@ -394,6 +394,78 @@ def test_fp8_large_batches_and_strides(ft):
     _fp8_case(ft, [20, 0, 33], 130, 272, torch.float32, seed=4, strided=True)
 
 
+def test_fp8_wide_tiles(ft):
+    """Both output types, widths that end inside a tile, rows without 16-byte pieces."""
+    sizes = [700, 1300, 0, 513, 256, 1025, 3, 900]
+    for N, K, out, strided in ((1300, 272, torch.float32, False), (1024, 144, torch.float32, True),
+                               (1101, 128, torch.bfloat16, False), (1040, 1040, torch.bfloat16, True)):
+        _fp8_case(ft, sizes, N, K, out, seed=5, strided=strided)
+
+
+def test_fp8_on_another_stream_and_captured(ft):
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    P, N, K = 300, 256, 384
+    x, w = _randn(gen, P, K), _e4m3(gen, 2, N, K)
+    wsc, offs = torch.rand((2, 2, 3), generator=gen, device="cuda"), _offs([100, 200])
+    codes, scales = torch.empty((P, K), dtype=torch.uint8, device="cuda"), torch.empty((3, P), device="cuda")
+    y, ws = torch.empty((P, N), device="cuda"), _ws(ft, 2, P, N, K)
+
+    def step():
+        ft.ft_moe_quantize_fp8(x, codes, scales)
+        ft.ft_moe_group_gemm_fp8(codes, scales, w, wsc, offs, y, ws)
+
+    step()
+    first = y.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y.zero_()
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, first)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        step()
+    y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, first)
+
+
+def test_offsets_beyond_32_bits(ft):
+    """Outputs and weights of more than 2^31 elements: the last rows and the last expert are right."""
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    P, N, K = 1 << 18, 8448, 64  # 2.2e9 output elements
+    x, w = _randn(gen, P, K), _randn(gen, 1, N, K)
+    y = torch.empty((P, N), dtype=torch.bfloat16, device="cuda")
+    ft.ft_moe_group_gemm(x, w, None, y, _ws(ft, 1, P, N, K))
+    xq, xs = torch.empty((P, K), dtype=torch.uint8, device="cuda"), torch.empty((1, P), device="cuda")
+    ft.ft_moe_quantize_fp8(x, xq, xs)
+    wq, wsc = w.float().to(torch.float8_e4m3fn), torch.ones((1, N // 128, 1), device="cuda")
+    rows = slice(P - 300, P)
+    ref = x[rows].double() @ w[0].double().t()
+    mag = x[rows].double().abs() @ w[0].double().abs().t()
+    _close(y[rows], ref, mag, K, torch.bfloat16)
+    ft.ft_moe_group_gemm_fp8(xq, xs, wq, wsc, None, y, _ws(ft, 1, P, N, K))
+    xd = xq[rows].view(torch.float8_e4m3fn).double() * xs[0, rows, None].double()
+    _close(y[rows], xd @ wq[0].double().t(), xd.abs() @ wq[0].double().abs().t(), K, torch.bfloat16, extra=4 * 2.0 ** -23)
+    del y
+    E, N, K = 520, 2048, 2048    # 2.2e9 weights
+    sizes = [0] * (E - 2) + [40, 25]
+    x, dy = _randn(gen, 65, K), _randn(gen, 65, N)
+    dw = torch.empty((E, N, K), dtype=torch.bfloat16, device="cuda")
+    ft.ft_moe_group_gemm_wgrad(dy, x, _offs(sizes), dw, _ws(ft, E, 65, N, K))
+    assert not dw[E - 3].any()
+    for e, r in ((E - 2, slice(0, 40)), (E - 1, slice(40, 65))):
+        ref = dy[r].double().t() @ x[r].double()
+        _close(dw[e], ref, dy[r].double().abs().t() @ x[r].double().abs(), 40, torch.bfloat16)
+    out = torch.empty((65, N), device="cuda")
+    ft.ft_moe_group_gemm(x, dw, _offs(sizes), out, _ws(ft, E, 65, N, K))
+    _close(out[40:], x[40:].double() @ dw[E - 1].double().t(), x[40:].double().abs() @ dw[E - 1].double().abs().t(), K,
+           torch.float32)
+
+
 def test_fp8_values_that_are_not_finite_stay_in_their_rows(ft):
     """0x7F is NaN; an infinite scale: only the rows that hold them notice."""
     gen = torch.Generator(device="cuda").manual_seed(11)
