@@ -345,20 +345,20 @@ namespace {
 struct RingW {
     static constexpr int BN = 256, piece = 128;
     static constexpr int stage = kABytes + BN / 2 * kChunkBytes;
-    static constexpr int stages = 4;
+    static constexpr int stages = 5;
     static constexpr int box_rows = 32;           // rows of x per TMA box
     static constexpr int warps = 16;              // sum warps: eight per piece, 64 columns each
     static constexpr int threads = 128 + 32 * warps;
-    static constexpr int out = warps * 32 * 128;  // 32 rows x 128 bytes per sum warp, on their way out
+    static constexpr int out = warps * 16 * 128;  // 16 rows x 128 bytes per sum warp, on their way out
 };
 
 // Wait for this thread's tensor-memory loads into v (the values are tied to the wait, so that
-// nothing that uses them moves before it).
-__device__ __forceinline__ void wait_ld16(uint32_t (&v)[16])
+// nothing that uses them moves before it). Eight columns at a time: longer reads hold the tensor
+// cores' own traffic to tensor memory up (4864 x 4096 x 4096: 68 us, with 16 columns 71, 32: 98).
+__device__ __forceinline__ void wait_ld8(uint32_t (&v)[8])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
                  :
                  : "memory");
 }
@@ -503,26 +503,31 @@ __global__ void __launch_bounds__(RingW::threads, 1)
         const int q = warp & 3, j = (warp - 4) >> 3, h = ((warp - 4) >> 2) & 1;  // lane quarter, piece, its half
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + j * T::piece + h * HC;
         const uint32_t empty_bar = map_rank(acc_empty + 2 * j, 0);
-        unsigned char *tile = sh_out + (warp - 4) * 32 * 128;
+        unsigned char *tile = sh_out + (warp - 4) * 16 * 128;
         const int n_blocks128 = (p.N + 127) / 128;
         int a = 0;
         uint32_t pa = 0;
-        for (int u = u0; u < units && !dead; u += du) {
-            const UnitW x = unit_of(u);
-            float2 sum[HC / 2];
-#pragma unroll
-            for (int i = 0; i < HC / 2; ++i) sum[i] = make_float2(0.f, 0.f);
-            const int first = (int)rank * kTileM + 32 * q;    // the warp's first row of the unit
-            const int live = min(max(x.rows - first, 0), 32);  // how many of its rows are the unit's
-            const float *xs = p.xs + x.row0 + (lane < live ? first + lane : 0);
-            const float *ws = p.ws + ((int64_t)x.e * n_blocks128 + min(x.n0 / 128 + j, n_blocks128 - 1)) * nb;
-            // the scales of this block and the next three (a load takes longer than a block)
-            float xn[4], wn[4];
+        UnitW x;
+        int first, live;           // the warp's first row of the unit, and how many of its rows are the unit's
+        const float *xs, *ws;      // this thread's row's and the piece's scales
+        float xn[4], wn[4];        // those of this block and the next three (a load takes longer than a block)
+        auto enter = [&](int u) {
+            x = unit_of(u);
+            first = (int)rank * kTileM + 32 * q;
+            live = min(max(x.rows - first, 0), 32);
+            xs = p.xs + x.row0 + (lane < live ? first + lane : 0);
+            ws = p.ws + ((int64_t)x.e * n_blocks128 + min(x.n0 / 128 + j, n_blocks128 - 1)) * nb;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 xn[i] = i < nb ? __ldg(xs + i * p.ld_xs) : 0.f;
                 wn[i] = i < nb ? __ldg(ws + i) : 0.f;
             }
+        };
+        if (u0 < units) enter(u0);
+        for (int u = u0; u < units && !dead; u += du) {
+            float2 sum[HC / 2];
+#pragma unroll
+            for (int i = 0; i < HC / 2; ++i) sum[i] = make_float2(0.f, 0.f);
             for (int b = 0; b < nb; ++b) {
                 const float f = xn[0] * wn[0];
 #pragma unroll
@@ -538,17 +543,17 @@ __global__ void __launch_bounds__(RingW::threads, 1)
                 tc::fence_after_sync();
                 const uint32_t addr = lane_addr + (uint32_t)a * BN;
 #pragma unroll
-                for (int c = 0; c < HC / 16; ++c) {
-                    uint32_t v[16];
-                    tc::ld16(addr + 16 * c, v);
-                    wait_ld16(v);
-                    if (c == HC / 16 - 1) {  // read out: the tensor cores may have the buffer back
+                for (int c = 0; c < HC / 8; ++c) {
+                    uint32_t v[8];
+                    tc::ld8(addr + 8 * c, v);
+                    wait_ld8(v);
+                    if (c == HC / 8 - 1) {  // read out: the tensor cores may have the buffer back
                         tc::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) arrive_cluster_relaxed(empty_bar + 8 * a);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fma2(sum[8 * c + i], f, f, v[2 * i], v[2 * i + 1]);
+                    for (int i = 0; i < 4; ++i) fma2(sum[4 * c + i], f, f, v[2 * i], v[2 * i + 1]);
                 }
                 a ^= 1;
                 if (a == 0) pa ^= 1;
@@ -558,6 +563,8 @@ __global__ void __launch_bounds__(RingW::threads, 1)
                 const int n0 = x.n0 + j * T::piece + h * HC;               // these 64 columns
                 const int mine = min(max(p.N - n0, 0), HC);               // how many of them exist
                 const int64_t at = (int64_t)(x.row0 + first) * p.ld + n0;  // their first element
+                const int rows = live;
+                if (u + du < units) enter(u + du);  // the next unit's first scales, while this one is stored
                 if (p.vec) {
                     // 128 bytes of each row at a time through shared memory (16-byte pieces swizzled by
                     // the row, free of bank conflicts), so that a store instruction writes whole lines
@@ -567,32 +574,40 @@ __global__ void __launch_bounds__(RingW::threads, 1)
 #pragma unroll
                     for (int c = 0; c < HC; c += per) {
                         if (c >= mine) break;
-                        __syncwarp();
+                        uint4 o[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            uint4 o;
                             if constexpr (F32) {
                                 const float2 s0 = sum[c / 2 + 2 * i], s1 = sum[c / 2 + 2 * i + 1];
-                                o = make_uint4(__float_as_uint(s0.x), __float_as_uint(s0.y), __float_as_uint(s1.x),
-                                               __float_as_uint(s1.y));
+                                o[i] = make_uint4(__float_as_uint(s0.x), __float_as_uint(s0.y), __float_as_uint(s1.x),
+                                                  __float_as_uint(s1.y));
                             } else {
                                 const float2 *t = sum + 4 * i;
-                                o = make_uint4(bf16x2(t[0].x, t[0].y), bf16x2(t[1].x, t[1].y), bf16x2(t[2].x, t[2].y),
-                                               bf16x2(t[3].x, t[3].y));
+                                o[i] = make_uint4(bf16x2(t[0].x, t[0].y), bf16x2(t[1].x, t[1].y), bf16x2(t[2].x, t[2].y),
+                                                  bf16x2(t[3].x, t[3].y));
                             }
-                            *reinterpret_cast<uint4 *>(tile + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
                         }
-                        __syncwarp();
                         const int col = c + l8 * (per / 8);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + r4;
-                            const uint4 o = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((l8 ^ (r & 7)) << 4));
-                            if (r < live && col < mine)
-                                *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + (at + r * p.ld + col) * (F32 ? 4 : 2)) = o;
+                        for (int g = 0; g < 2; ++g) {  // 16 rows at a time
+                            __syncwarp();
+                            if (lane >> 4 == g) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    *reinterpret_cast<uint4 *>(tile + (lane & 15) * 128 + ((i ^ l8) << 4)) = o[i];
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = 4 * i + r4;
+                                const uint4 w = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((l8 ^ (r & 7)) << 4));
+                                if (16 * g + r < rows && col < mine)
+                                    *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) +
+                                                               (at + (16 * g + r) * p.ld + col) * (F32 ? 4 : 2)) = w;
+                            }
                         }
                     }
-                } else if (lane < live) {
+                } else if (lane < rows) {
 #pragma unroll
                     for (int i = 0; i < HC; ++i)
                         if (i < mine) {
