@@ -402,6 +402,15 @@ def test_fp8_wide_tiles(ft):
         _fp8_case(ft, sizes, N, K, out, seed=5, strided=strided)
 
 
+@pytest.mark.parametrize("N", [256, 300, 200, 1000])
+def test_fp8_remainders_of_wide_tiles(ft, N):
+    """Remainders on both sides of half a tile (128 rows), of a CTA's share (64) and of a box (32)."""
+    sizes = [256 + r for r in (0, 1, 31, 33, 64, 65, 127, 128, 129, 255)] + [512 + 100, 512 + 190, 40, 0, 130]
+    sizes = sizes * 3 if N <= 300 else sizes
+    _fp8_case(ft, sizes, N, 272, torch.float32, seed=6)
+    _fp8_case(ft, sizes, N, 400, torch.bfloat16, seed=7)
+
+
 def test_fp8_on_another_stream_and_captured(ft):
     gen = torch.Generator(device="cuda").manual_seed(12)
     P, N, K = 300, 256, 384
