@@ -85,16 +85,18 @@ __device__ __forceinline__ uint2 block_codes(const float (&v)[8], float scale)
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 constexpr int kActThreads = 256;
-constexpr int kRowsPerCta = kActThreads / 16;  // quantizing kernels: 16 lanes per row and block
+// Quantizing kernels: 16 lanes per row and block of 128; 8 rows per CTA, so that the scales of a block
+// fill a 32-byte sector. (65536 x 2048 bf16: 67.7 us, with 16 rows per CTA 70.0.)
+constexpr int kQuantThreads = 128;
+constexpr int kRowsPerCta = kQuantThreads / 16;
 
 }  // namespace
 
-// A CTA takes 16 rows (so that the scales of a block are written side by side) by several blocks of
-// 128 columns, whose loads are all in flight before the first is used: 65536 x 2048 bf16 rows in
-// one block at a time reached 4.7 TB/s.
+// A CTA takes its rows by several blocks of 128 columns, whose loads are all in flight before the
+// first is used: 65536 x 2048 bf16 rows take 67.7 us (5.9 TB/s), one block at a time 86, eight 79.
 // (A launch that does not fill the SMs takes one: more CTAs are then faster.)
 template <bool F32, int kBlocks>
-__global__ void __launch_bounds__(kActThreads)
+__global__ void __launch_bounds__(kQuantThreads)
     quantize_fp8_kernel(const void *__restrict__ src, int64_t ld, int rows, int K, uint8_t *__restrict__ codes,
                         int64_t ld_codes, float *__restrict__ scales, int64_t ld_scales)
 {
@@ -116,39 +118,29 @@ __global__ void __launch_bounds__(kActThreads)
     }
 }
 
-template <int kGluBlocks>
+// (One block per thread and 16 rows per CTA here: with the exponentials in between, more threads hide
+// more than longer ones: 65536 x 512 takes 31.5 us, two blocks 33.9, four 43.2, 8 rows 34.3.)
 __global__ void __launch_bounds__(kActThreads)
     swiglu_quantize_fp8_kernel(const uint16_t *__restrict__ gu, int64_t ld, const float *__restrict__ w, int rows, int I,
                                uint8_t *__restrict__ codes, int64_t ld_codes, float *__restrict__ scales,
                                int64_t ld_scales)
 {
     pdl_enter();
-    const int row = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4), l = threadIdx.x & 15;
-    const int b0 = blockIdx.y * kGluBlocks, c0 = 128 * b0 + 8 * l;
-    const uint16_t *from = gu + row * ld;
-    float g[kGluBlocks][8] = {}, u[kGluBlocks][8] = {};
+    const int row = blockIdx.x * (kActThreads / 16) + (threadIdx.x >> 4), l = threadIdx.x & 15;
+    const int col = blockIdx.y * 128 + 8 * l;
+    const bool in = row < rows && col < I;
+    float h[8] = {};
+    if (in) {
+        float g[8], u[8];
+        load8<false>(gu + row * ld, col, g);
+        load8<false>(gu + row * ld + I, col, u);
+        const float f = w ? __ldg(w + row) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < kGluBlocks; ++i)
-        if (row < rows && c0 + 128 * i < I) {
-            load8<false>(from, c0 + 128 * i, g[i]);
-            load8<false>(from + I, c0 + 128 * i, u[i]);
-        }
-    const float f = w && row < rows ? __ldg(w + row) : 1.0f;
-#pragma unroll
-    for (int i = 0; i < kGluBlocks; ++i) {
-        if (128 * (b0 + i) >= I) break;
-        float h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = f * (g[i][j] * sigmoid(g[i][j]) * u[i][j]);
-        if (!(row < rows && c0 + 128 * i < I)) {  // no values: not part of the block's maximum
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[j] = 0.f;
-        }
-        const float s = block_scale(h);
-        if (row < rows && c0 + 128 * i < I)
-            *reinterpret_cast<uint2 *>(codes + row * ld_codes + c0 + 128 * i) = block_codes(h, s);
-        if (row < rows && l == 0) scales[(b0 + i) * ld_scales + row] = s;
+        for (int i = 0; i < 8; ++i) h[i] = f * (g[i] * sigmoid(g[i]) * u[i]);
     }
+    const float s = block_scale(h);
+    if (in) *reinterpret_cast<uint2 *>(codes + row * ld_codes + col) = block_codes(h, s);
+    if (row < rows && l == 0) scales[blockIdx.y * ld_scales + row] = s;
 }
 
 // One warp per row. VEC: 8 columns per lane and step (everything 16-byte aligned), else one.
@@ -164,13 +156,24 @@ __global__ void __launch_bounds__(kActThreads)
         uint16_t *o = h + row * ld_h;
         const float f = w ? __ldg(w + row) : 1.0f;
         if constexpr (VEC) {
-            for (int c = 8 * lane; c < I; c += 256) {
-                float g[8], u[8];
-                load8<false>(gr, c, g);
-                load8<false>(ur, c, u);
+            for (int c = 8 * lane; c < I; c += 512) {  // two steps' loads in flight together
+                uint4 q[2][2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = f * (g[i] * sigmoid(g[i]) * u[i]);
-                *reinterpret_cast<uint4 *>(o + c) = pack8(g);
+                for (int k = 0; k < 2; ++k) {
+                    if (c + 256 * k >= I) break;
+                    q[k][0] = ldg_nc_v4(gr + c + 256 * k);
+                    q[k][1] = ldg_nc_v4(ur + c + 256 * k);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (c + 256 * k >= I) break;
+                    float g[8], u[8];
+                    unpack8(q[k][0], g);
+                    unpack8(q[k][1], u);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = f * (g[i] * sigmoid(g[i]) * u[i]);
+                    *reinterpret_cast<uint4 *>(o + c + 256 * k) = pack8(g);
+                }
             }
         } else {
             for (int c = lane; c < I; c += 32) {
@@ -256,10 +259,10 @@ cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows,
                                 float *scales, int64_t ld_scales, cudaStream_t s)
 {
     const int by_rows = (rows + kRowsPerCta - 1) / kRowsPerCta, nb = (K + 127) / 128;
-    const int per = (int64_t)by_rows * nb < 16 * sm_count() ? 1 : 4;
+    const int per = (int64_t)by_rows * nb < 32 * sm_count() ? 1 : 4;
     auto kern = f32 ? (per == 1 ? quantize_fp8_kernel<true, 1> : quantize_fp8_kernel<true, 4>)
                     : (per == 1 ? quantize_fp8_kernel<false, 1> : quantize_fp8_kernel<false, 4>);
-    FT_LAUNCH(kern, dim3(by_rows, (nb + per - 1) / per), dim3(kActThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales,
+    FT_LAUNCH(kern, dim3(by_rows, (nb + per - 1) / per), dim3(kQuantThreads), 0, s, src, ld, rows, K, codes, ld_codes, scales,
               ld_scales);
     count_launches(1);
     return cudaGetLastError();
@@ -268,11 +271,8 @@ cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows,
 cudaError_t launch_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float *w, int rows, int I, uint8_t *codes,
                                        int64_t ld_codes, float *scales, int64_t ld_scales, cudaStream_t s)
 {
-    const int by_rows = (rows + kRowsPerCta - 1) / kRowsPerCta, nb = (I + 127) / 128;
-    const int per = (int64_t)by_rows * nb < 16 * sm_count() ? 1 : 2;
-    auto kern = per == 1 ? swiglu_quantize_fp8_kernel<1> : swiglu_quantize_fp8_kernel<2>;
-    FT_LAUNCH(kern, dim3(by_rows, (nb + per - 1) / per), dim3(kActThreads), 0, s, static_cast<const uint16_t *>(gu), ld_gu, w,
-              rows, I, codes, ld_codes, scales, ld_scales);
+    FT_LAUNCH(swiglu_quantize_fp8_kernel, dim3((rows + kActThreads / 16 - 1) / (kActThreads / 16), (I + 127) / 128), dim3(kActThreads),
+              0, s, static_cast<const uint16_t *>(gu), ld_gu, w, rows, I, codes, ld_codes, scales, ld_scales);
     count_launches(1);
     return cudaGetLastError();
 }
