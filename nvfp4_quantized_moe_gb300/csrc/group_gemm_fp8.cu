@@ -8,6 +8,14 @@
 // outer sum cannot be left to the tensor cores: eight warps read every block's partial sums and
 // add them, times the two scales, to fp32 accumulators in registers (two columns per
 // fma.rn.f32x2) while the tensor cores work on the next block.
+//
+// What bounds it, measured on one GB300:
+//   - many rows: the way of each block's partial sums from the tensor cores through registers and
+//     back. Dense 4864 x 4096 x 4096 takes 68 us, 2400 TFLOP/s; the MMAs alone took 42.
+//   - few rows: the weights' one pass through memory. 64 tokens over 256 experts of 1024 x 2048 (0.47 GB)
+//     take 75 us after 2 us for the quantizer, 6.2 TB/s.
+//   - one row: latency. 1024 x 2048 takes 4.3 us after the quantizer, the contraction split over
+//     clusters of eight CTAs.
 #include <cuda_bf16.h>
 
 #include "group_gemm.cuh"
