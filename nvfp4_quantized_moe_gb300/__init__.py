@@ -271,13 +271,13 @@ def _refuse(name, t, dtypes, shape):
 
 
 def _rows(name, t, dtypes, rows, cols):
-    """Row stride of a [rows, cols] tensor whose rows are contiguous."""
+    """Row stride of a [rows, cols] tensor whose rows are contiguous (a single row's does not matter)."""
     if t.dtype not in dtypes or t.shape != (rows, cols):
         _refuse(name, t, dtypes, (rows, cols))
     ld, step = t.stride()
     if step != 1 and cols > 1:
         _refuse(name, t, dtypes, (rows, cols))
-    return ld if rows > 1 else max(ld, cols)
+    return ld if rows > 1 else cols
 
 
 def _whole(name, t, dtypes, shape):
@@ -297,9 +297,11 @@ def _dims(name, t, n):
 
 def _stream_of(stream, t):
     """The stream to launch on, as an integer: the one given, or the current one of t's device."""
+    if not t.is_cuda:
+        raise ValueError("expected tensors on the GPU")
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _offsets(offs, E):

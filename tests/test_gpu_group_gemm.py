@@ -269,6 +269,39 @@ def test_runs_are_bitwise_equal_and_capture(ft):
     assert all(torch.equal(a, b) for a, b in zip(first, (y, dx, dw)))
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_wgrad_of_many_units_is_bitwise_equal_and_captures(ft, out):
+    """Enough units that they are handed out by a counter: which CTA computes a unit must not show."""
+    sizes = [(37 * i) % 150 for i in range(200)] + [0, 900, 1, 2000]
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    P, E, N, K = sum(sizes), len(sizes), 512, 512
+    x, dy, offs = _randn(gen, P, K), _randn(gen, P, N), _offs(sizes)
+    got, ref, mag = _forms(ft, "wgrad", x, torch.empty((E, N, K), device="cuda"), dy, offs, sizes, out)
+    _close(got, ref, mag, 2000, out)
+    dw, ws = torch.empty((E, N, K), dtype=out, device="cuda"), _ws(ft, E, P, N, K)
+    for _ in range(3):
+        ft.ft_moe_group_gemm_wgrad(dy, x, offs, dw, ws)
+        assert torch.equal(dw, got)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ft.ft_moe_group_gemm_wgrad(dy, x, offs, dw, ws)
+    for _ in range(2):
+        dw.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dw, got)
+
+
+def test_one_row_of_any_stride(ft):
+    """A single row has no stride: one cut out of an odd-sized buffer is as good as any."""
+    buf = torch.ones((3, 64 + 5), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((1, 128, 64), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((1, 128), device="cuda")
+    ft.ft_moe_group_gemm(buf[:1, :64], w, None, y, _ws(ft, 1, 1, 128, 64))
+    assert (y == 64).all()
+
+
 @pytest.mark.parametrize("offs", [[0, 5, 3, 12], [0, 4, 8, 99], [-2, 4, 8, 12]])
 def test_bad_offsets_are_reported(ft, offs):
     """Offsets that decrease or leave [0, P]: reported, and nothing outside the output is touched."""

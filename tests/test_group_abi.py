@@ -105,6 +105,8 @@ def test_binding_refuses_what_it_cannot_pass(ft):
         lambda: ft.ft_moe_swiglu(y, torch.zeros(7), x),
         lambda: ft.ft_moe_swiglu(y, torch.zeros(8, dtype=torch.float64), x),
         lambda: ft.ft_moe_swiglu_backward(y, None, x, bf(8, 64)),
+        lambda: ft.ft_moe_group_gemm(x, w, offs, y, ws),   # all well formed, but not on the GPU
+        lambda: ft.ft_moe_swiglu(y, None, x),
     ]
     for call in bad:
         with pytest.raises(ValueError):
