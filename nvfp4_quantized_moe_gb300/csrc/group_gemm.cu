@@ -3,7 +3,7 @@
 //
 //   forward  y[p, n]     = sum_k x[p, k]  w[e, n, k]      M axis n, N axis p, contraction k
 //   dgrad    dx[p, k]    = sum_n dy[p, n] w[e, n, k]      M axis k, N axis p, contraction n
-//   wgrad    dw[e, n, k] = sum_p dy[p, n] x[p, k]         M axis n, N axis k, contraction p
+//   wgrad    dw[e, n, k] = sum_p dy[p, n] x[p, k]         M axis k, N axis n, contraction p
 //
 // Operands go from global memory through TMA (128-byte swizzle) into a ring of shared-memory
 // stages of 64 contraction steps and from there into tcgen05.mma (kind::f16, bf16 operands,
@@ -21,8 +21,9 @@
 //     1.18 ms, 7.6 TB/s. DRAM traffic equals what the operands hold.
 //   - a handful of rows: the chain of latencies from launch to store. One token over 8 of 256
 //     experts (2048 x 512) takes 6.7 us, one expert of 2048 x 2048 with 4 rows 7.0 us.
-//   - wgrad: the output. fp32 dw [256, 1024, 2048] (2.1 GB) of 65536 rows takes 403 us with 256 rows
-//     per expert (4.8 TB/s of output) and 535 us with Zipf-distributed ones.
+//   - wgrad: the output. fp32 dw [256, 1024, 2048] (2.1 GB) of 65536 rows takes 394 us with 256 rows
+//     per expert (6.5 TB/s read and written) and 510 us with Zipf-distributed ones, where the large
+//     experts' MMAs and the small ones' stores add up in each SM.
 #include <cuda_bf16.h>
 
 #include "group_gemm.cuh"
@@ -33,13 +34,16 @@ namespace {
 
 using namespace grp;
 
-constexpr int kThreadsG = 384;  // warps: 0 TMA, 1 MMA, 2 tail rows (wgrad), 3 units, 4..11 epilogue
 constexpr int kStep = 64;       // contraction steps per stage
 // Long sums into fp32 outputs are cut into parts of this many stages, added in registers: the
 // tensor cores truncate where an fp32 addition rounds, so that the error of one long
 // accumulation grows with its length (5e-6 relative over 8192 steps, against 2e-7 for sums in
 // parts of 512). A bf16 output rounds 300 times coarser and keeps one accumulation.
 constexpr int kPartStages = 8;
+// wgrad: units handed out ahead of the epilogue. Small units need the distance to keep loads in
+// flight, and a large one in between makes those behind it wait (Zipf-distributed rows, fp32 dw
+// [256, 1024, 2048]: 2 ahead 524 us, 3 502, 4 513, 6 534).
+constexpr int kAhead = 3;
 
 // Tile variants. CG: CTAs per tile of the M axis (a pair shares its B operand and halves what
 // each SM must load per multiplication); BN: largest extent along the N axis.
@@ -50,10 +54,11 @@ struct Ring {
     // rows of one TMA box of a row-major B operand: short boxes, so that a short tile loads no
     // more rows than it has (to within a box)
     static constexpr int box_rows = BN <= 32 ? 16 : 32;
-    // wgrad: 32 rows x 128 bytes of output per epilogue warp, on their way out. (Not by TMA: its
-    // stores, held back by the memory, held the loads behind them back too.)
-    static constexpr int extra = WG ? 8 * 4096 : 0;
-    static constexpr int fit = (216 * 1024 - extra) / stage;
+    // warps: 0 TMA, 1 MMA, 2 tail rows (wgrad only), then eight for the epilogue. No more: an fp32
+    // epilogue holds 128 running sums a thread, and every further warp takes registers from it.
+    static constexpr int roles = WG ? 3 : 2;
+    static constexpr int threads = 32 * (roles + 8);
+    static constexpr int fit = 216 * 1024 / stage;
     // (eight keep memory busy; with ten a decode step of 64 tokens took 152 us, with eight 142)
     static constexpr int stages = fit < 8 ? fit : 8;
 };
@@ -64,7 +69,7 @@ struct GroupParams {
     int M;                // size of the M axis
     int N;                // wgrad: size of the N axis
     int R;                // forward, dgrad: contraction length
-    void *out;            // forward, dgrad: [P][ld]; wgrad: [E][M][N]
+    void *out;            // forward, dgrad: [P][ld]; wgrad: [E][N][ld]
     int64_t ld;
     int accumulate;       // wgrad, fp32: add to what dw holds
     int split;            // CTAs (one cluster) that share a unit's contraction
@@ -99,7 +104,7 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
 // One unit of work: a 128 x CG by (up to) BN tile of the output.
 struct Unit {
     int e, m0;        // expert, first M index of this CTA
-    int col0, cols;   // N axis: first index and count (rows p, or columns k of wgrad)
+    int col0, cols;   // N axis: first index and count (rows p, or n of wgrad)
     int half;         // N indices this CTA loads (all, or its half of a pair's)
     int r0, R;        // contraction range
 };
@@ -108,7 +113,7 @@ struct Unit {
 
 // WG: the wgrad form (both operands transposed, ragged contraction); A_MN: A transposed.
 template <int CG, int BN, bool A_MN, bool WG, bool F32>
-__global__ void __launch_bounds__(kThreadsG, 1)
+__global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
     group_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ GroupParams p)
 {
@@ -121,12 +126,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     constexpr int W = HC < 32 ? HC : 32;       // columns per tensor-memory load
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    unsigned char *extra = smem + S * T::stage;
-    uint64_t *full = reinterpret_cast<uint64_t *>(extra + T::extra);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * T::stage);
     uint64_t *empty = full + S, *tail = empty + S, *peer_tail = tail + S, *acc_full = peer_tail + S,
-             *acc_empty = acc_full + 2, *unit_full = acc_empty + 2, *unit_empty = unit_full + 2;
-    int *sh_unit = reinterpret_cast<int *>(unit_empty + 2);  // the next two units
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + 2);
+             *acc_empty = acc_full + 2, *unit_full = acc_empty + 2, *unit_empty = unit_full + kAhead;
+    int *sh_unit = reinterpret_cast<int *>(unit_empty + kAhead);  // the next units
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + kAhead);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
@@ -145,9 +149,14 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
             mbar_init(acc_empty + i, 8 * CG);  // every epilogue warp
-            mbar_init(unit_full + i, 1);
-            mbar_init(unit_empty + i, CG * 10 + 1);  // the MMA warp and, in each CTA, producer, tail and epilogue warps
         }
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(unit_full + i, 1);
+            mbar_init(unit_empty + i, CG * 10);  // all warps that take units: MMA, tail and epilogue; the other CTA's
+                                                 // producer, tail and epilogue
+        }
+        if (CG == 2 && !leader)
+            for (int i = 0; i < kAhead; ++i) mbar_arrive_expect_tx(unit_full + i, 4);
         *abort_flag = 0;
         fence_mbar_init();
         tc::prefetch_map(&map_a);
@@ -202,11 +211,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     };
     bool dead = false;
     // The warp's next unit, or -1 after the last one. With a counter (wgrad, whose units cost as much
-    // as their expert has rows), the leader's unit warp hands them out, at most two ahead of the
-    // epilogue: whoever is done takes the next. Dealt out in turn, the largest experts' units ended
-    // last on some CTAs (65536 rows over 256 experts, Zipf: 622 us against 555). Forward and dgrad
-    // units cost about the same; there the counter gained nothing.
-    const bool counted = WG && p.counter;
+    // as their expert has rows), the leader's producer hands them out: whoever is done takes the
+    // next. Dealt out in turn, the largest experts' units ended last on some CTAs (Zipf-distributed
+    // rows, fp32 dw [256, 1024, 2048]: 587 us). Forward and dgrad units cost about the same; there
+    // the counter gained nothing. (Pairs only: the ring's stores go from CTA to CTA of a cluster.)
+    constexpr bool kCounted = WG && CG == 2;
+    const bool counted = kCounted && p.counter;
     const uint32_t unit_empty_bar = CG == 2 ? map_rank(unit_empty, 0) : 0;
     int turn = 0;
     auto next_unit = [&]() {
@@ -214,49 +224,44 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         if (!counted) {
             u = u0 + turn * du;
         } else {
-            const int i = turn & 1;
-            if (!warp_wait(unit_full + i, (turn >> 1) & 1, abort_flag, wl)) { dead = true; return -1; }
+            const int i = turn % kAhead;
+            if (!warp_wait(unit_full + i, (turn / kAhead) & 1, abort_flag, wl)) { dead = true; return -1; }
             u = uniform(*(volatile int *)(sh_unit + i));
             __syncwarp();
             if (lane == 0) {
-                if (CG == 2) arrive_cluster_relaxed(unit_empty_bar + 8 * i);
-                else mbar_arrive(unit_empty + i);
+                if (warp == 0) mbar_arrive_expect_tx(unit_full + i, 4);  // (the other CTA's producer: the slot's next unit)
+                arrive_cluster_relaxed(unit_empty_bar + 8 * i);
             }
         }
         ++turn;
         return u < units ? u : -1;
     };
 
-    if (WG && warp == 3) {
-        // ------------------------------------------------------------ units
-        if (counted && leader) {
-            for (int n = 0; !dead; ++n) {
-                const int i = n & 1;
-                int u = u0;  // the first is this CTA's (or pair's) own
-                if (n > 0 && lane == 0) u = du + atomicAdd(p.counter, 1);
-                u = uniform(u);
-                if (!warp_wait(unit_empty + i, ((n >> 1) & 1) ^ 1, abort_flag, wl)) { dead = true; break; }
-                if (lane < CG) {
-                    if (CG == 2) {
-                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(sh_unit + i, lane)), "r"(u) : "memory");
-                        arrive_cluster(map_rank(unit_full + i, lane));
-                    } else {
-                        sh_unit[i] = u;
-                        mbar_arrive(unit_full + i);
-                    }
-                }
-                __syncwarp();
-                if (u >= units) break;
-            }
-            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
-        }
-    } else if (warp == 0) {
+    // The leader's producer: the counter's next unit, for itself and the ring.
+    int ticket = u0;  // (the first is this CTA's or pair's own)
+    auto hand_out = [&]() {
+        const int i = turn % kAhead, u = uniform(ticket);
+        if (!warp_wait(unit_empty + i, ((turn / kAhead) & 1) ^ 1, abort_flag, wl)) { dead = true; return -1; }
+        // into both CTAs; the asynchronous store completes the barrier's phase by itself
+        if (lane == 0) mbar_arrive_expect_tx(unit_full + i, 4);
+        if (lane < CG)
+            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+                             map_rank(sh_unit + i, lane)),
+                         "r"(u), "r"(map_rank(unit_full + i, lane))
+                         : "memory");
+        __syncwarp();
+        if (lane == 0 && u < units) ticket = du + atomicAdd(p.counter, 1);  // (known by the next turn)
+        ++turn;
+        return u < units ? u : -1;
+    };
+
+    if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (!p.skip_producer) {
             const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
-            for (int u; (u = next_unit()) >= 0 && !dead;) {
+            for (int u; (u = kCounted && counted && leader ? hand_out() : next_unit()) >= 0 && !dead;) {
                 const Unit x = uniform_unit(unit_of(u));
                 const int nb = last_stage(x.R);
                 const int boxes = WG ? x.half / 64 : (x.half + T::box_rows - 1) / T::box_rows;
@@ -377,13 +382,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             if (++s == S) s = 0;
         }
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
-    } else if (warp >= 4) {
+    } else if (warp >= T::roles) {
         // ------------------------------------------------------------ epilogue
         // thread = TMEM lane = M index; the warp takes columns [h * HC, h * HC + HC) of the tile
-        const int q = warp & 3, h = (warp - 4) >> 2;
+        const int q = warp & 3, h = (warp - T::roles) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
         const uint32_t empty_bar = CG == 2 ? map_rank(acc_empty, 0) : 0;
-        unsigned char *tile = extra + (warp - 4) * 4096;  // wgrad: 32 rows x 128 bytes
         int ac = 0;
         for (int u; (u = next_unit()) >= 0 && !dead;) {
             const Unit x = unit_of(u);
@@ -393,50 +397,22 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             const int mine = min(max(x.cols - h * HC, 0), HC);  // columns of this half in use
             const int m = x.m0 + 32 * q + lane;
 
-            // W columns at offset c of this half, as sums, to where they go
+            // W columns at offset c of this half, as sums, to where they go: lanes lie along the contiguous
+            // axis of out, so that a store instruction writes a whole line without a detour
+            const int64_t row0 = (WG ? (int64_t)x.e * p.N : 0) + x.col0 + h * HC;
             auto emit = [&](int c, const float (&v)[W]) {
-                if constexpr (WG) {
-                    // lane = row n of dw, columns k: 128 bytes of each row at a time through shared
-                    // memory (16-byte pieces swizzled by the row, free of bank conflicts), so that a
-                    // store instruction writes whole lines of four rows
-                    constexpr int per = F32 ? 32 : 64;  // columns of 128 bytes
+                if (WG && F32 && p.accumulate) {
+                    const int n = m < p.M ? mine - c : 0;
+                    float *o = static_cast<float *>(p.out) + (row0 + c) * p.ld + m;
 #pragma unroll
-                    for (int i = 0; i < (F32 ? 8 : 4); ++i) {
-                        uint4 o;
-                        if constexpr (F32)
-                            o = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                           __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-                        else
-                            o = make_uint4(bf16x2(v[8 * i], v[8 * i + 1]), bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                           bf16x2(v[8 * i + 4], v[8 * i + 5]), bf16x2(v[8 * i + 6], v[8 * i + 7]));
-                        const int piece = i + (F32 ? 0 : (c % per) / 8);
-                        *reinterpret_cast<uint4 *>(tile + lane * 128 + ((piece ^ (lane & 7)) << 4)) = o;
-                    }
-                    if (c % per == per - W || c + W >= mine) {  // the 128 bytes, or what there is of them, are complete
-                        __syncwarp();
-                        const int l8 = lane & 7, col = c / per * per + l8 * (per / 8), n0 = x.m0 + 32 * q;
-                        char *o = static_cast<char *>(p.out) +
-                                  (((int64_t)x.e * p.M + n0) * p.N + x.col0 + h * HC + col) * (F32 ? 4 : 2);
-                        const int64_t row = (int64_t)p.N * (F32 ? 4 : 2);
-                        const int rows = col < mine ? min(p.M - n0, 32) : 0;
+                    for (int j = 0; j < W; j += 4) {
+                        float was[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3);
-                            uint4 w = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((l8 ^ (r & 7)) << 4));
-                            if (r < rows) {
-                                if constexpr (F32) {
-                                    if (p.accumulate) {
-                                        const float4 was = *reinterpret_cast<const float4 *>(o + r * row);
-                                        w = make_uint4(__float_as_uint(__uint_as_float(w.x) + was.x),
-                                                       __float_as_uint(__uint_as_float(w.y) + was.y),
-                                                       __float_as_uint(__uint_as_float(w.z) + was.z),
-                                                       __float_as_uint(__uint_as_float(w.w) + was.w));
-                                    }
-                                }
-                                *reinterpret_cast<uint4 *>(o + r * row) = w;
-                            }
-                        }
-                        __syncwarp();
+                        for (int i = 0; i < 4; ++i) was[i] = j + i < n ? o[i * p.ld] : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (j + i < n) o[i * p.ld] = was[i] + v[j + i];
+                        o += 4 * p.ld;
                     }
                 } else if (kSplit && split > 1) {
                     // (every stage of the ring has been read by the time the last sums are complete)
@@ -444,7 +420,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll
                     for (int j = 0; j < W; ++j) red[(h * HC + c + j) * kTileM + 32 * q + lane] = v[j];
                 } else {
-                    store_rows<F32, W>(v, m, p.M, x.col0 + h * HC + c, mine - c, p.out, p.ld);
+                    store_rows<F32, W>(v, m, p.M, row0 + c, mine - c, p.out, p.ld);
                 }
             };
             float sum[F32 ? HC : 1];  // fp32 outputs: the parts' running sums
@@ -515,7 +491,7 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
 {
     using T = Ring<CG, BN, WG>;
     auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32>;
-    const size_t smem = 1024 + T::stages * T::stage + T::extra + 8 * (4 * T::stages + 8) + 24 + 4 * 2 * (size_t)(p.E + 1);
+    const size_t smem = 1024 + T::stages * T::stage + 8 * (4 * T::stages + 4 + 2 * kAhead) + 4 * kAhead + 16 + 4 * 2 * (size_t)(p.E + 1);
     static SharedMemoryLimit limit;
     const cudaError_t e = limit.raise(kern, smem);
     if (e != cudaSuccess) return e;
@@ -524,18 +500,18 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
     // long as all clusters run at once.
     p.split = 1;
     if (CG == 1 && !WG)
-        while (p.split < 8 && p.R >= 4 * kStep * p.split && max_units <= clusters.get(kern, 2 * p.split, kThreadsG, smem))
+        while (p.split < 8 && p.R >= 4 * kStep * p.split && max_units <= clusters.get(kern, 2 * p.split, T::threads, smem))
             p.split *= 2;
-    int64_t grid = p.split > 1 ? max_units : clusters.get(kern, CG, kThreadsG, smem);
+    int64_t grid = p.split > 1 ? max_units : clusters.get(kern, CG, T::threads, smem);
     if (max_units < grid) grid = max_units;
     if (grid < 1) grid = 1;
-    if (WG && p.E > 1 && max_units > 4 * grid) {  // units of unlike cost, several each
+    if (WG && CG == 2 && p.E > 1 && max_units > 4 * grid) {  // units of unlike cost, several each
         const cudaError_t me = cudaMemsetAsync(p.status + 16, 0, sizeof(int), s);
         if (me != cudaSuccess) return me;
         p.counter = p.status + 16;
     }
     const int cluster = CG * p.split;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(kThreadsG), smem, cluster, s, maps[0],
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(T::threads), smem, cluster, s, maps[0],
                                           maps[1], p);
     if (le != cudaSuccess) return le;
     count_launches(1);
@@ -565,8 +541,8 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     p.status = g.status;
     injected_stall(&p.wait_ns, &p.skip_producer);
     const bool wg = g.form == kGroupWgrad, fw = g.form == kGroupForward;
-    p.M = g.form == kGroupDgrad ? g.K : g.N;
-    p.N = g.K;
+    p.M = fw ? g.N : g.K;
+    p.N = g.N;
     p.R = fw ? g.K : g.N;
     // The tile's extent along the rows, by the rows per expert that has any. Measured on 256 experts
     // of 1024 x 2048 (forward, us, with 32 / 128 / 256 = a pair of CTAs): 12 rows 162 / 165 / 165, 32
@@ -580,9 +556,9 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap maps[2];
     bool ok;
-    if (wg) {  // A: dy [P][N] read along n; B: x [P][K] read along k
-        ok = make_tensor_map_2d(&maps[0], bf, g.dy, g.N, g.P, 2 * (uint64_t)g.ld_dy, 64, kStep, sw) &&
-             make_tensor_map_2d(&maps[1], bf, g.x, g.K, g.P, 2 * (uint64_t)g.ld_x, 64, kStep, sw);
+    if (wg) {  // A: x [P][K] read along k; B: dy [P][N] read along n
+        ok = make_tensor_map_2d(&maps[0], bf, g.x, g.K, g.P, 2 * (uint64_t)g.ld_x, 64, kStep, sw) &&
+             make_tensor_map_2d(&maps[1], bf, g.dy, g.N, g.P, 2 * (uint64_t)g.ld_dy, 64, kStep, sw);
     } else {   // A: w [E][N][K]; B: x [P][K] or dy [P][N]
         ok = make_tensor_map_3d(&maps[0], bf, g.w, g.K, g.N, g.E, 2 * (uint64_t)g.K, 2 * (uint64_t)g.K * g.N, 64,
                                 fw ? kTileM : kStep, sw) &&

@@ -269,12 +269,13 @@ def test_runs_are_bitwise_equal_and_capture(ft):
     assert all(torch.equal(a, b) for a, b in zip(first, (y, dx, dw)))
 
 
+@pytest.mark.parametrize("N,K", [(512, 512), (64, 1024)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
-def test_wgrad_of_many_units_is_bitwise_equal_and_captures(ft, out):
+def test_wgrad_of_many_units_is_bitwise_equal_and_captures(ft, out, N, K):
     """Enough units that they are handed out by a counter: which CTA computes a unit must not show."""
     sizes = [(37 * i) % 150 for i in range(200)] + [0, 900, 1, 2000]
     gen = torch.Generator(device="cuda").manual_seed(14)
-    P, E, N, K = sum(sizes), len(sizes), 512, 512
+    P, E = sum(sizes), len(sizes)
     x, dy, offs = _randn(gen, P, K), _randn(gen, P, N), _offs(sizes)
     got, ref, mag = _forms(ft, "wgrad", x, torch.empty((E, N, K), device="cuda"), dy, offs, sizes, out)
     _close(got, ref, mag, 2000, out)
