@@ -298,6 +298,11 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
                     if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
+            // The last stages' MMAs also arrive in the other CTA: neither leaves before all have.
+            for (int i = 0; CG == 2 && i < S && !dead; ++i) {
+                if (!warp_wait(empty + s, ph, abort_flag, wl)) dead = true;
+                if (++s == S) { s = 0; ph ^= 1; }
+            }
             if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
             if (dead && leader)  // every issued copy lands before the exit (normally the MMAs have waited for them)
                 for (int i = 0; i < S && i < it; ++i) {
