@@ -249,22 +249,6 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
-// The dynamic shared memory that one kernel may be launched with (a static per kernel), raised when
-// a launch needs more than an earlier one did on the same device.
-struct SharedMemoryLimit {
-    size_t raised[64] = {};
-    template <typename Kernel>
-    cudaError_t raise(Kernel *kern, size_t bytes)
-    {
-        int dev = 0;
-        const cudaError_t de = cudaGetDevice(&dev);
-        if (de != cudaSuccess) return de;
-        if (dev >= 0 && dev < 64 && raised[dev] >= bytes) return cudaSuccess;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e == cudaSuccess && dev >= 0 && dev < 64) raised[dev] = bytes;
-        return e;
-    }
-};
 // Clusters of `cluster` CTAs (up to 8) of a kernel that can run at once: the grid of a persistent
 // kernel. A die's SMs need not divide into whole clusters, and a cluster beyond this number would
 // start only when another one ends: 152 SMs hold 76 pairs, but 36 clusters of four and 15 of eight.

@@ -497,8 +497,7 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
     using T = Ring<CG, BN, WG>;
     auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32>;
     const size_t smem = 1024 + T::stages * T::stage + 8 * (4 * T::stages + 4 + 2 * kAhead) + 4 * kAhead + 16 + 4 * 2 * (size_t)(p.E + 1);
-    static SharedMemoryLimit limit;
-    const cudaError_t e = limit.raise(kern, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     static ClusterLimit clusters;
     // Few units: the CTAs of a cluster share one unit's contraction, at least two stages each, as

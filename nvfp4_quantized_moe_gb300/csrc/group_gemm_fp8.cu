@@ -652,8 +652,7 @@ cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p,
     auto kern = group_gemm_fp8_kernel<BN, F32>;
     const size_t smem = 1024 + T::stages * T::stage + 4 * T::slots * BN +
                         8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) + 16 + 4 * 2 * (size_t)(p.E + 1);
-    static SharedMemoryLimit limit;
-    const cudaError_t e = limit.raise(kern, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t m_tiles = (p.N + kTileM - 1) / kTileM;
     const int64_t units = m_tiles * (p.P / BN + (p.E < p.P ? p.E : p.P));  // at most
@@ -677,8 +676,7 @@ cudaError_t launch_wide(const CUtensorMap &w, const CUtensorMap &x, const Group8
     using T = RingW;
     auto kern = group_gemm_fp8_wide_kernel<F32>;
     const size_t smem = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 8) + 16 + 4 * 2 * (size_t)(p.E + 1);
-    static SharedMemoryLimit limit;
-    const cudaError_t e = limit.raise(kern, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)((p.N + T::BN - 1) / T::BN) * (p.P / (2 * kTileM) + (p.E < p.P ? p.E : p.P));  // at most
     static ClusterLimit clusters;
