@@ -37,7 +37,7 @@ using namespace grp;
 constexpr int kStep = 64;       // contraction steps per stage
 // Long sums into fp32 outputs are cut into parts of this many stages, added in registers: the
 // tensor cores truncate where an fp32 addition rounds, so that the error of one long
-// accumulation grows with its length (5e-6 relative over 8192 steps, against 2e-7 for sums in
+// accumulation grows with its length (5e-6 relative over 8192 steps, against 4.4e-7 for sums in
 // parts of 512). A bf16 output rounds 300 times coarser and keeps one accumulation.
 constexpr int kPartStages = 8;
 // wgrad: units handed out ahead of the epilogue. Small units need the distance to keep loads in
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
     using T = Ring<CG, BN, WG>;
     constexpr int S = T::stages;
     constexpr int kGran = WG ? 64 : 16;        // N indices per CTA come in multiples of this
-    constexpr bool kSplit = CG == 1 && !WG;
+    constexpr bool kSplit = CG == 1;
     constexpr int HC = BN / 2;                 // columns of one half's epilogue warps
     constexpr int W = HC < 32 ? HC : 32;       // columns per tensor-memory load
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
                     const int k0 = b * kStep;
                     // a stage with tail rows is completed by the tail warp
-                    const bool tails = WG && b == nb - 1 && (x.R & 15);
+                    const bool tails = WG && (b + 1) * kStep >= x.R && (x.R & 15);
                     const uint32_t bar = tails ? smem_u32(tail + s) : CG == 2 ? map_rank(full + s, 0) : smem_u32(full + s);
                     if (one) {
                         // the leader expects both CTAs' bytes (equally many); the other's may land first
@@ -357,10 +357,10 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
         uint32_t phases = 0;  // bit s: parity of tail[s]
         for (int u; (u = next_unit()) >= 0 && !dead;) {
             const Unit x = unit_of(u);
-            const int nb = (x.R + kStep - 1) / kStep;
-            if (nb == 0) continue;
-            s = (s + nb - 1) % S;  // the unit's last stage
-            if (x.R & 15) {
+            const int nb = last_stage(x.R), n = nb - first_stage(x.R);
+            if (n == 0) continue;
+            s = (s + n - 1) % S;  // the unit's last stage here
+            if (nb * kStep >= x.R && (x.R & 15)) {
                 const uint32_t parity = (phases >> s) & 1;
                 if (!warp_wait(tail + s, parity, abort_flag, wl)) { dead = true; break; }
                 phases ^= 1u << s;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
             const Unit x = unit_of(u);
             const int nb = last_stage(x.R) - first_stage(x.R);
             const int parts = F32 ? (nb + kPartStages - 1) / kPartStages : nb > 0;
-            if (WG && parts == 0 && p.accumulate) continue;
+            if (WG && parts == 0 && p.accumulate && split == 1) continue;
             const int mine = min(max(x.cols - h * HC, 0), HC);  // columns of this half in use
             const int m = x.m0 + 32 * q + lane;
 
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
             // axis of out, so that a store instruction writes a whole line without a detour
             const int64_t row0 = (WG ? (int64_t)x.e * p.N : 0) + x.col0 + h * HC;
             auto emit = [&](int c, const float (&v)[W]) {
-                if (WG && F32 && p.accumulate) {
+                if (WG && F32 && p.accumulate && split == 1) {
                     const int n = m < p.M ? mine - c : 0;
                     float *o = static_cast<float *>(p.out) + (row0 + c) * p.ld + m;
 #pragma unroll
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
             cluster_sync();
             if (u0 < units) {
                 const Unit x = unit_of(u0);
-                add_parts<F32>(reinterpret_cast<const float *>(smem), x.cols, x.m0, p.M, x.col0, p.out, p.ld, split, part);
+                add_parts<F32>(reinterpret_cast<const float *>(smem), x.cols, x.m0, p.M, (WG ? (int64_t)x.e * p.N : 0) + x.col0,
+                               p.out, p.ld, split, part, WG && F32 && p.accumulate);
             }
             cluster_sync();
         }
@@ -500,11 +501,12 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     static ClusterLimit clusters;
-    // Few units: the CTAs of a cluster share one unit's contraction, at least two stages each, as
-    // long as all clusters run at once.
+    // Few units: the CTAs of a cluster share one unit's contraction (wgrad: an expert's rows), at least
+    // two stages each, as long as all clusters run at once.
     p.split = 1;
-    if (CG == 1 && !WG)
-        while (p.split < 8 && p.R >= 4 * kStep * p.split && max_units <= clusters.get(kern, 2 * p.split, T::threads, smem))
+    const int64_t steps = WG ? p.P / p.E : p.R;
+    if (CG == 1)
+        while (p.split < 8 && steps >= 4 * kStep * p.split && max_units <= clusters.get(kern, 2 * p.split, T::threads, smem))
             p.split *= 2;
     int64_t grid = p.split > 1 ? max_units : clusters.get(kern, CG, T::threads, smem);
     if (max_units < grid) grid = max_units;
@@ -570,8 +572,14 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
                                 bn <= 32 ? Ring<1, 32, false>::box_rows : Ring<1, 128, false>::box_rows, sw);
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (wg)
-        return p.M > kTileM ? launch_typed<2, 256, true, true>(g, maps, p, s) : launch_typed<1, 256, true, true>(g, maps, p, s);
+    if (wg) {
+        // Pairs, unless their tiles leave more than half of the SMs idle: then single CTAs that share
+        // the rows (fp32, pairs / shared, us: one expert of 256 x 2048 with 8192 rows 53.6 / 22.2, 1024
+        // x 2048 with 1999 rows 19.2 / 17.0; 8 of 512 x 512 with 128 rows each, too few to share, 7.6 / 7.3).
+        const int64_t tiles = (int64_t)g.E * ((g.N + 255) / 256) * ((g.K + 255) / 256);
+        return p.M > kTileM && 4 * tiles >= sm_count() ? launch_typed<2, 256, true, true>(g, maps, p, s)
+                                                       : launch_typed<1, 256, true, true>(g, maps, p, s);
+    }
     if (fw) {
         if (bn == 32) return launch_typed<1, 32, false, false>(g, maps, p, s);
         if (bn == 128) return launch_typed<1, 128, false, false>(g, maps, p, s);

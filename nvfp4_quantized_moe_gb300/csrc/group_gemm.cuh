@@ -245,11 +245,11 @@ __device__ __forceinline__ void store_rows(const float (&v)[W], int m, int M, in
 }
 
 // The sums of a tile whose contraction the `split` CTAs of a cluster shared: each left its part in
-// its own `red` [cols][128]; the CTAs add and store a share of the elements each, parts always in
-// the same order. Between two cluster barriers, by all threads.
+// its own `red` [cols][128]; the CTAs add and store a share of the elements each (or add them to
+// out), parts always in the same order. Between two cluster barriers, by all threads.
 template <bool F32>
 __device__ __forceinline__ void add_parts(const float *red, int cols, int m0, int M, int64_t row0, void *out, int64_t ld,
-                                          int split, int part)
+                                          int split, int part, bool accumulate = false)
 {
     constexpr int kMax = 8;
     // four neighbours of one row at a time, all parts' loads in flight together
@@ -272,7 +272,7 @@ __device__ __forceinline__ void add_parts(const float *red, int cols, int m0, in
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (m + j < M) {
-                if constexpr (F32) static_cast<float *>(out)[at + j] = o[j];
+                if constexpr (F32) static_cast<float *>(out)[at + j] = accumulate ? static_cast<float *>(out)[at + j] + o[j] : o[j];
                 else static_cast<__nv_bfloat16 *>(out)[at + j] = __float2bfloat16_rn(o[j]);
             }
     }

@@ -294,6 +294,37 @@ def test_wgrad_of_many_units_is_bitwise_equal_and_captures(ft, out, N, K):
         assert torch.equal(dw, got)
 
 
+@pytest.mark.parametrize("out,accumulate", ((torch.bfloat16, False), (torch.float32, False), (torch.float32, True)))
+@pytest.mark.parametrize("sizes,N,K", (([1000], 256, 200), ([4099], 40, 1000), ([2048], 256, 256), ([700, 0, 1], 128, 136),
+                                       ([0, 64, 3000, 5], 64, 128)))
+def test_wgrad_of_few_tiles_shares_the_rows(ft, sizes, N, K, accumulate, out):
+    """Few tiles and many rows: several thread blocks share an expert's rows, some without any."""
+    P, E = sum(sizes), len(sizes)
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    x, dy, offs = _randn(gen, P, K), _randn(gen, P, N), _offs(sizes)
+    base = torch.randn((E, N, K), generator=gen, device="cuda")
+    _, ref, mag = _forms(ft, "wgrad", x, base.bfloat16(), dy, offs, sizes, torch.float32)
+    dw, ws = base.to(out, copy=True), _ws(ft, E, P, N, K)
+    ft.ft_moe_group_gemm_wgrad(dy, x, offs, dw, ws, accumulate=accumulate)
+    if accumulate:
+        ref, mag = ref + base.double(), mag + base.double().abs()
+    _close(dw, ref, mag, max(sizes) + accumulate, out)
+    again = base.to(out, copy=True)
+    ft.ft_moe_group_gemm_wgrad(dy, x, offs, again, ws, accumulate=accumulate)
+    assert torch.equal(dw, again)
+
+
+def test_wgrad_shared_rows_keep_to_their_expert(ft):
+    """Rows of the next expert that are not finite, behind a last stage that several blocks' parts end in."""
+    sizes, N, K = [1003, 500], 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    x, dy = _randn(gen, 1503, K), _randn(gen, 1503, N)
+    x[1003:], dy[1003:] = float("nan"), float("inf")
+    dw = torch.empty((2, N, K), device="cuda")
+    ft.ft_moe_group_gemm_wgrad(dy, x, _offs(sizes), dw, _ws(ft, 2, 1503, N, K))
+    assert torch.isfinite(dw[0]).all() and not torch.isfinite(dw[1]).any()
+
+
 def test_one_row_of_any_stride(ft):
     """A single row has no stride: one cut out of an odd-sized buffer is as good as any."""
     buf = torch.ones((3, 64 + 5), dtype=torch.bfloat16, device="cuda")
