@@ -24,6 +24,10 @@
 //   - wgrad: the output. fp32 dw [256, 1024, 2048] (2.1 GB) of 65536 rows takes 394 us with 256 rows
 //     per expert (6.5 TB/s read and written) and 510 us with Zipf-distributed ones, where the large
 //     experts' MMAs and the small ones' stores add up in each SM.
+//     Added to dw (4.3 GB read and written), 256 rows each take 801 us, as reductions that L2 carries
+//     out; read, added and stored by the warps, each value's latency waited for, 2525 us.
+//   - wgrad of few tiles: the rows of an expert, shared by a cluster. One expert of 256 x 2048 with
+//     8192 rows takes 22 us (not shared 54).
 #include <cuda_bf16.h>
 
 #include "group_gemm.cuh"
@@ -71,7 +75,6 @@ struct GroupParams {
     int R;                // forward, dgrad: contraction length
     void *out;            // forward, dgrad: [P][ld]; wgrad: [E][N][ld]
     int64_t ld;
-    int accumulate;       // wgrad, fp32: add to what dw holds
     int split;            // CTAs (one cluster) that share a unit's contraction
     int *counter;         // units handed out so far (zero at launch), or null: units go in turn
     int *status;
@@ -111,13 +114,16 @@ struct Unit {
 
 }  // namespace
 
-// WG: the wgrad form (both operands transposed, ragged contraction); A_MN: A transposed.
-template <int CG, int BN, bool A_MN, bool WG, bool F32>
+// WG: the wgrad form (both operands transposed, ragged contraction); A_MN: A transposed; ACC: wgrad
+// that adds to what dw holds (a kernel of its own: the branch in the stores cost the plain one 8%,
+// in registers: 256 experts of 1024 x 2048 with 256 rows each 396 and 426 us).
+template <int CG, int BN, bool A_MN, bool WG, bool F32, bool ACC>
 __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
     group_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ GroupParams p)
 {
     static_assert(!WG || A_MN, "wgrad reads both operands transposed");
+    static_assert(!ACC || (WG && F32), "only wgrad adds, in fp32");
     using T = Ring<CG, BN, WG>;
     constexpr int S = T::stages;
     constexpr int kGran = WG ? 64 : 16;        // N indices per CTA come in multiples of this
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
             const Unit x = unit_of(u);
             const int nb = last_stage(x.R) - first_stage(x.R);
             const int parts = F32 ? (nb + kPartStages - 1) / kPartStages : nb > 0;
-            if (WG && parts == 0 && p.accumulate && split == 1) continue;
+            if (ACC && parts == 0 && split == 1) continue;
             const int mine = min(max(x.cols - h * HC, 0), HC);  // columns of this half in use
             const int m = x.m0 + 32 * q + lane;
 
@@ -406,26 +412,13 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
             // axis of out, so that a store instruction writes a whole line without a detour
             const int64_t row0 = (WG ? (int64_t)x.e * p.N : 0) + x.col0 + h * HC;
             auto emit = [&](int c, const float (&v)[W]) {
-                if (WG && F32 && p.accumulate && split == 1) {
-                    const int n = m < p.M ? mine - c : 0;
-                    float *o = static_cast<float *>(p.out) + (row0 + c) * p.ld + m;
-#pragma unroll
-                    for (int j = 0; j < W; j += 4) {
-                        float was[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) was[i] = j + i < n ? o[i * p.ld] : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (j + i < n) o[i * p.ld] = was[i] + v[j + i];
-                        o += 4 * p.ld;
-                    }
-                } else if (kSplit && split > 1) {
+                if (kSplit && split > 1) {
                     // (every stage of the ring has been read by the time the last sums are complete)
                     float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
                     for (int j = 0; j < W; ++j) red[(h * HC + c + j) * kTileM + 32 * q + lane] = v[j];
                 } else {
-                    store_rows<F32, W>(v, m, p.M, row0 + c, mine - c, p.out, p.ld);
+                    store_rows<F32, W>(v, m, p.M, row0 + c, mine - c, p.out, p.ld, ACC);
                 }
             };
             float sum[F32 ? HC : 1];  // fp32 outputs: the parts' running sums
@@ -480,7 +473,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
             if (u0 < units) {
                 const Unit x = unit_of(u0);
                 add_parts<F32>(reinterpret_cast<const float *>(smem), x.cols, x.m0, p.M, (WG ? (int64_t)x.e * p.N : 0) + x.col0,
-                               p.out, p.ld, split, part, WG && F32 && p.accumulate);
+                               p.out, p.ld, split, part, ACC);
             }
             cluster_sync();
         }
@@ -492,11 +485,11 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
 
 namespace {
 
-template <int CG, int BN, bool A_MN, bool WG, bool F32>
+template <int CG, int BN, bool A_MN, bool WG, bool F32, bool ACC>
 cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_units, cudaStream_t s)
 {
     using T = Ring<CG, BN, WG>;
-    auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32>;
+    auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32, ACC>;
     const size_t smem = 1024 + T::stages * T::stage + 8 * (4 * T::stages + 4 + 2 * kAhead) + 4 * kAhead + 16 + 4 * 2 * (size_t)(p.E + 1);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -529,8 +522,10 @@ cudaError_t launch_typed(const GroupGemm &g, const CUtensorMap (&maps)[2], Group
 {
     const int64_t m_tiles = (p.M + kTileM * CG - 1) / (kTileM * CG);
     const int64_t tiles = WG ? (int64_t)g.E * ((p.N + BN - 1) / BN) : g.P / BN + (g.E < g.P ? g.E : g.P);
-    return g.out_f32 ? launch<CG, BN, A_MN, WG, true>(maps, p, m_tiles * tiles, s)
-                     : launch<CG, BN, A_MN, WG, false>(maps, p, m_tiles * tiles, s);
+    if constexpr (WG)
+        if (g.accumulate) return launch<CG, BN, A_MN, WG, true, true>(maps, p, m_tiles * tiles, s);
+    return g.out_f32 ? launch<CG, BN, A_MN, WG, true, false>(maps, p, m_tiles * tiles, s)
+                     : launch<CG, BN, A_MN, WG, false, false>(maps, p, m_tiles * tiles, s);
 }
 
 }  // namespace
@@ -543,7 +538,6 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     p.P = g.P;
     p.out = g.out;
     p.ld = g.ld_out;
-    p.accumulate = g.accumulate;
     p.status = g.status;
     injected_stall(&p.wait_ns, &p.skip_producer);
     const bool wg = g.form == kGroupWgrad, fw = g.form == kGroupForward;

@@ -209,19 +209,30 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 
 // ---------------------------------------------------------------- stores
 
+// *to += v, without waiting for what it holds. Each element gets one such addition in a launch, so
+// that there is no order to depend on.
+__device__ __forceinline__ void add_global(float *to, float v)
+{
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(v) : "memory");
+}
+
 // W columns of a tile whose lane is the M index m: columns are the rows row0, row0 + 1, ... of
 // `out` (`rows` of them at most), m (< M) is the place in the row. Called by whole warps.
 // bf16 rows with pairs (M even, every row 4-byte aligned): neighbouring lanes trade one value each,
 // so that a lane holds two neighbours of one row and a store covers two rows.
 template <bool F32, int W, bool PAIRS = true>
-__device__ __forceinline__ void store_rows(const float (&v)[W], int m, int M, int64_t row0, int rows, void *out, int64_t ld)
+__device__ __forceinline__ void store_rows(const float (&v)[W], int m, int M, int64_t row0, int rows, void *out, int64_t ld,
+                                           bool accumulate = false)
 {
     if constexpr (F32) {
         const int n = m < M ? rows : 0;
         float *o = static_cast<float *>(out) + row0 * ld + m;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            if (j < n) *o = v[j];
+            if (j < n) {
+                if (accumulate) add_global(o, v[j]);
+                else *o = v[j];
+            }
             o += ld;
         }
     } else if constexpr (PAIRS) {
@@ -272,8 +283,10 @@ __device__ __forceinline__ void add_parts(const float *red, int cols, int m0, in
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (m + j < M) {
-                if constexpr (F32) static_cast<float *>(out)[at + j] = accumulate ? static_cast<float *>(out)[at + j] + o[j] : o[j];
-                else static_cast<__nv_bfloat16 *>(out)[at + j] = __float2bfloat16_rn(o[j]);
+                if constexpr (F32) {
+                    if (accumulate) add_global(static_cast<float *>(out) + at + j, o[j]);
+                    else static_cast<float *>(out)[at + j] = o[j];
+                } else static_cast<__nv_bfloat16 *>(out)[at + j] = __float2bfloat16_rn(o[j]);
             }
     }
 }

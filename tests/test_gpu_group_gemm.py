@@ -314,6 +314,28 @@ def test_wgrad_of_few_tiles_shares_the_rows(ft, sizes, N, K, accumulate, out):
     assert torch.equal(dw, again)
 
 
+def test_wgrad_accumulates_over_many_units(ft):
+    """Twice into the same dw, units handed out by a counter; values that are not finite stay."""
+    sizes, N, K = [(37 * i) % 150 for i in range(200)] + [0, 900, 1, 2000], 200, 520
+    P, E = sum(sizes), len(sizes)
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    x, dy, offs = _randn(gen, P, K), _randn(gen, P, N), _offs(sizes)
+    base = torch.randn((E, N, K), generator=gen, device="cuda")
+    base[3, 5, 7], base[200, 0, 0] = float("inf"), float("nan")
+    _, ref, mag = _forms(ft, "wgrad", x, base.bfloat16(), dy, offs, sizes, torch.float32)
+    dw, ws = base.clone(), _ws(ft, E, P, N, K)
+    for _ in range(2):
+        ft.ft_moe_group_gemm_wgrad(dy, x, offs, dw, ws, accumulate=True)
+    again = base.clone()
+    for _ in range(2):
+        ft.ft_moe_group_gemm_wgrad(dy, x, offs, again, ws, accumulate=True)
+    assert torch.equal(dw.view(torch.int32), again.view(torch.int32))
+    assert torch.isinf(dw[3, 5, 7]) and torch.isnan(dw[200, 0, 0])
+    ok = torch.isfinite(base)
+    assert torch.equal(torch.isfinite(dw), ok)
+    _close(dw[ok], (2 * ref + base.double())[ok], (2 * mag + base.double().abs())[ok], 2001, torch.float32)
+
+
 def test_wgrad_shared_rows_keep_to_their_expert(ft):
     """Rows of the next expert that are not finite, behind a last stage that several blocks' parts end in."""
     sizes, N, K = [1003, 500], 64, 128
