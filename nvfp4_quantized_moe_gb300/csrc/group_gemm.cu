@@ -570,14 +570,17 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
         // Pairs, unless their tiles leave more than half of the SMs idle: then single CTAs that share
         // the rows (fp32, pairs / shared, us: one expert of 256 x 2048 with 8192 rows 53.6 / 22.2, 1024
         // x 2048 with 1999 rows 19.2 / 17.0; 8 of 512 x 512 with 128 rows each, too few to share, 7.6 / 7.3).
-        // Nor with one or two stages a unit, where a pair's shared operand saves little, and so few
-        // units that the counter and its memset are a tenth of the time (fp32, pairs / single, us: 128
-        // of 640 x 512 with 19 rows each 43.7 / 35.6, with 94 46.5 / 38.9; 256 of 264 x 320 with 36 45.6
-        // / 31.4; but 64 of 1024 x 1024, Zipf, 256 on average 89.2 / 103.7, and 256 of 1024 x 2048 with 16
-        // 350 / 371).
+        // Nor with one or two stages a unit, where a pair's shared operand saves little, if there are so
+        // few units that the counter and its memset are a tenth of the time (fp32, pairs / single, us:
+        // 128 of 640 x 512 with 19 rows each 43.7 / 35.6, with 94 46.5 / 38.9; 256 of 264 x 320 with 36
+        // 45.6 / 31.4; but 64 of 1024 x 1024, Zipf, 256 on average 89.2 / 103.7), or if the output is bf16,
+        // whose units are too short to hide a pair's handshakes (256 of 1024 x 2048 with 16 rows 246 /
+        // 214, with 64 263 / 230; fp32 350 / 371; nearly all experts empty, where the counter helps,
+        // bf16 85 / 101).
         const int64_t tiles = (int64_t)g.E * ((g.N + 255) / 256) * ((g.K + 255) / 256);
-        const bool few = 4 * tiles < sm_count(), small = g.P / g.E < 2 * kStep && tiles <= 8 * sm_count();
-        return p.M <= kTileM || few || small ? launch_typed<1, 256, true, true>(g, maps, p, s)
+        const bool few = 4 * tiles < sm_count(), small = g.P / g.E < 2 * kStep;
+        const bool quick = small && (tiles <= 8 * sm_count() || (!g.out_f32 && g.P / g.E >= 8));
+        return p.M <= kTileM || few || quick ? launch_typed<1, 256, true, true>(g, maps, p, s)
                                              : launch_typed<2, 256, true, true>(g, maps, p, s);
     }
     if (fw) {
