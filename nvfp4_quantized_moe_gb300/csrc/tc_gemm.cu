@@ -643,31 +643,41 @@ static EncodeTiledFn encode_fn()
     return fn;
 }
 
+// The encoder needs a current context, and a host thread has none before its first runtime call that
+// wants one: such a thread gets its device's context here. (Calls that launch another kernel first
+// never meet this; a call that begins with its tensor maps would fail in every new thread.)
+static bool encode(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const cuuint64_t *dims,
+                   const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swz, CUtensorMapL2promotion l2)
+{
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    auto once = [&]() {
+        return fn(map, dt, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swz, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (once()) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && once();
+}
+
 bool make_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t dims[2] = {inner, rows};
     const cuuint64_t strides[1] = {row_bytes};
     const cuuint32_t box[2] = {box_inner, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, dt, 2, base, dims, strides, box, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
 bool make_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t mats, uint64_t row_bytes, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_rows,
                         CUtensorMapSwizzle swz)
 {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t dims[3] = {inner, rows, mats};
     const cuuint64_t strides[2] = {row_bytes, mat_bytes};
     const cuuint32_t box[3] = {box_inner, box_rows, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, dt, 3, base, dims, strides, box, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 bool tc_shape_ok_fp8(int K, int rows_per_expert) { return K % 128 == 0 && K >= 128 && rows_per_expert % MT == 0; }
