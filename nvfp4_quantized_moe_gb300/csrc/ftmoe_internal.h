@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ft_moe.h"
 
 namespace ftmoe {
@@ -167,6 +169,7 @@ bool make_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *ba
 // A grouped bf16 product (group_gemm.cu). Forward uses x and w, dgrad dy and w, wgrad dy and x;
 // `out` is y, dx or dw. Pointers, strides and sizes are the entry points', already checked.
 enum { kGroupForward, kGroupDgrad, kGroupWgrad };
+constexpr int kGroupMaxExperts = 1024;
 struct GroupGemm {
     int form;
     const int *offs;             // [E + 1], or null (E = 1: all P rows)
@@ -252,16 +255,18 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
 // Clusters of `cluster` CTAs (up to 8) of a kernel that can run at once: the grid of a persistent
 // kernel. A die's SMs need not divide into whole clusters, and a cluster beyond this number would
 // start only when another one ends: 152 SMs hold 76 pairs, but 36 clusters of four and 15 of eight.
-// A static per kernel (and shared memory size); the answer is looked up once per device.
+// A static per kernel, always asked with the kernel's largest shared memory size; the answer is
+// looked up once per device (threads that look it up together find the same).
 struct ClusterLimit {
-    int found[64][9] = {};
+    std::atomic<int> found[64][9] = {};
     template <typename Kernel>
     int get(Kernel *kern, int cluster, int threads, size_t smem)
     {
         int dev = 0;
         if (cluster <= 1) return sm_count();
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || cluster > 8) return sm_count() / cluster;
-        if (found[dev][cluster] == 0) {
+        int n = found[dev][cluster].load(std::memory_order_relaxed);
+        if (n == 0) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(cluster * sm_count());
             cfg.blockDim = dim3(threads);
@@ -272,11 +277,11 @@ struct ClusterLimit {
             attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            int n = 0;
-            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = sm_count() / cluster;
-            found[dev][cluster] = n < sm_count() / cluster ? n : sm_count() / cluster;
+            const int all = sm_count() / cluster;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0 || n > all) n = all;
+            found[dev][cluster].store(n, std::memory_order_relaxed);
         }
-        return found[dev][cluster];
+        return n;
     }
 };
 // launch_pdl inside a function returning cudaError_t: return the launch error, if any.

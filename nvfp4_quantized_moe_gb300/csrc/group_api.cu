@@ -35,7 +35,7 @@ static ft_status check_sizes(int E, int P, int N, int K, int unit_n, int unit_k)
 {
     if (E <= 0 || P < 0 || N <= 0 || K <= 0)
         return reject(FT_ERR_INVALID_ARG, "need E, N, K > 0 and P >= 0 (got E %d, P %d, N %d, K %d)", E, P, N, K);
-    if (E > 1024 || P > kMaxRows || N > kMaxWidth || K > kMaxWidth)
+    if (E > kGroupMaxExperts || P > kMaxRows || N > kMaxWidth || K > kMaxWidth)
         return reject(FT_ERR_UNSUPPORTED, "need E <= 1024, P <= 2^25, N and K <= 65536");
     if (N % unit_n || K % unit_k)
         return reject(FT_ERR_UNSUPPORTED, "need N a multiple of %d and K a multiple of %d (got N %d, K %d)", unit_n, unit_k,

@@ -490,8 +490,10 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
 {
     using T = Ring<CG, BN, WG>;
     auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32, ACC>;
-    const size_t smem = 1024 + T::stages * T::stage + 8 * (4 * T::stages + 4 + 2 * kAhead) + 4 * kAhead + 16 + 4 * 2 * (size_t)(p.E + 1);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t fixed = 1024 + T::stages * T::stage + 8 * (4 * T::stages + 4 + 2 * kAhead) + 4 * kAhead + 16;
+    constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
+    static_assert(most <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     static ClusterLimit clusters;
     // Few units: the CTAs of a cluster share one unit's contraction (wgrad: an expert's rows), at least
@@ -499,9 +501,9 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
     p.split = 1;
     const int64_t steps = WG ? p.P / p.E : p.R;
     if (CG == 1)
-        while (p.split < 8 && steps >= 4 * kStep * p.split && max_units <= clusters.get(kern, 2 * p.split, T::threads, smem))
+        while (p.split < 8 && steps >= 4 * kStep * p.split && max_units <= clusters.get(kern, 2 * p.split, T::threads, most))
             p.split *= 2;
-    int64_t grid = p.split > 1 ? max_units : clusters.get(kern, CG, T::threads, smem);
+    int64_t grid = p.split > 1 ? max_units : clusters.get(kern, CG, T::threads, most);
     if (max_units < grid) grid = max_units;
     if (grid < 1) grid = 1;
     if (WG && CG == 2 && p.E > 1 && max_units > 4 * grid) {  // units of unlike cost, several each
@@ -510,8 +512,8 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
         p.counter = p.status + 16;
     }
     const int cluster = CG * p.split;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(T::threads), smem, cluster, s, maps[0],
-                                          maps[1], p);
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * cluster), dim3(T::threads), fixed + table_bytes(p.E), cluster, s,
+                                          maps[0], maps[1], p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();

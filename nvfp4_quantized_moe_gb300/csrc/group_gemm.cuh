@@ -24,6 +24,11 @@ constexpr int kTileM = 128;          // weight rows of one CTA's tile (TMEM lane
 constexpr int kChunkBytes = 128;     // bytes of the contraction axis per stage (the swizzle width)
 constexpr int kABytes = kTileM * kChunkBytes;
 
+// Shared memory of the experts' table. The limit of a kernel's shared memory belongs to the kernel,
+// not to a call: it is always set to what kGroupMaxExperts need, so that calls with unlike numbers of
+// experts, made by several threads at once, do not lower it for each other.
+constexpr size_t table_bytes(int E) { return 4 * 2 * ((size_t)E + 1); }
+
 // ---------------------------------------------------------------- issuing warps
 //
 // One thread issues the copies and the MMAs, but its whole warp runs the loop around them: their

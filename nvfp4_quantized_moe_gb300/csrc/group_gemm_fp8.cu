@@ -656,9 +656,10 @@ cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p,
 {
     using T = Ring8<BN>;
     auto kern = group_gemm_fp8_kernel<BN, F32>;
-    const size_t smem = 1024 + T::stages * T::stage + 4 * T::slots * BN +
-                        8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) + 16 + 4 * 2 * (size_t)(p.E + 1);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t fixed = 1024 + T::stages * T::stage + 4 * T::slots * BN + 8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) + 16;
+    constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
+    static_assert(most <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     const int64_t m_tiles = (p.N + kTileM - 1) / kTileM;
     const int64_t units = m_tiles * (p.P / BN + (p.E < p.P ? p.E : p.P));  // at most
@@ -666,11 +667,12 @@ cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p,
     // Few units: the CTAs of a cluster share one unit's contraction, at least two blocks each, as
     // long as all clusters run at once.
     p.split = 1;
-    while (p.split < 8 && p.K >= 4 * kStep8 * p.split && units <= clusters.get(kern, 2 * p.split, kThreads8, smem)) p.split *= 2;
+    while (p.split < 8 && p.K >= 4 * kStep8 * p.split && units <= clusters.get(kern, 2 * p.split, kThreads8, most)) p.split *= 2;
     int64_t grid = p.split > 1 ? units : sm_count();
     if (units < grid) grid = units;
     if (grid < 1) grid = 1;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * p.split), dim3(kThreads8), smem, p.split, s, w, x, p);
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * p.split), dim3(kThreads8), fixed + table_bytes(p.E), p.split, s, w,
+                                          x, p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
@@ -681,14 +683,16 @@ cudaError_t launch_wide(const CUtensorMap &w, const CUtensorMap &x, const Group8
 {
     using T = RingW;
     auto kern = group_gemm_fp8_wide_kernel<F32>;
-    const size_t smem = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 8) + 16 + 4 * 2 * (size_t)(p.E + 1);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t fixed = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 8) + 16;
+    constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
+    static_assert(most <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)((p.N + T::BN - 1) / T::BN) * (p.P / (2 * kTileM) + (p.E < p.P ? p.E : p.P));  // at most
     static ClusterLimit clusters;
-    int64_t grid = clusters.get(kern, 2, T::threads, smem);
+    int64_t grid = clusters.get(kern, 2, T::threads, most);
     if (units < grid) grid = units;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), smem, 2, s, w, x, p);
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), fixed + table_bytes(p.E), 2, s, w, x, p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();

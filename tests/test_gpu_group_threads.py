@@ -1,5 +1,8 @@
 """The expert products called from other host threads than the first, each with its own stream and
 workspace: in a thread that has made no CUDA call before, and in several at once."""
+import os
+import shutil
+import subprocess
 import threading
 
 import pytest
@@ -64,3 +67,15 @@ def test_first_call_of_a_thread(ft, which):
     torch.cuda.synchronize()
     assert not failed, failed
     assert ft.ft_moe_read_status(ws) == 0 and torch.equal(outs[which], first)
+
+
+def test_threads_with_unlike_numbers_of_experts(ft, tmp_path):
+    """From C++, where nothing serialises the calls (gpu_probes/unlike_threads.cpp)."""
+    here, lib = os.path.dirname(os.path.abspath(__file__)), os.path.abspath(ft.LIB_PATH)
+    exe = str(tmp_path / "unlike_threads")
+    subprocess.check_call([shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc", "-O2", "-std=c++17", "-I",
+                           os.path.join(os.path.dirname(here), "include"), "-o", exe,
+                           os.path.join(here, "gpu_probes", "unlike_threads.cpp"), lib, "-Xlinker",
+                           "-rpath=" + os.path.dirname(lib)])
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
