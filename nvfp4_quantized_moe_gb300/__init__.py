@@ -259,7 +259,8 @@ def ft_moe_quantize_nvfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.
 
 
 # The expert products and row kernels are short calls: what follows checks what the C call cannot
-# see (types, shapes, layouts) and passes plain integers.
+# see (types, shapes, layouts, and that all tensors lie on the first one's device) and passes plain
+# integers.
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _OUT, _E4M3 = (torch.bfloat16, torch.float32), (torch.uint8, torch.float8_e4m3fn)
 _OUT_CODE = {torch.bfloat16: FT_DTYPE_BF16, torch.float32: FT_DTYPE_F32}
@@ -267,12 +268,12 @@ _OUT_CODE = {torch.bfloat16: FT_DTYPE_BF16, torch.float32: FT_DTYPE_F32}
 
 def _refuse(name, t, dtypes, shape):
     raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))} of shape {tuple(shape)} with contiguous "
-                     f"elements, got {t.dtype} {tuple(t.shape)} (strides {t.stride()})")
+                     f"elements on the first operand's device, got {t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
-def _rows(name, t, dtypes, rows, cols):
+def _rows(name, t, dev, dtypes, rows, cols):
     """Row stride of a [rows, cols] tensor whose rows are contiguous (a single row's does not matter)."""
-    if t.dtype not in dtypes or t.shape != (rows, cols):
+    if t.dtype not in dtypes or t.shape != (rows, cols) or t.get_device() != dev:
         _refuse(name, t, dtypes, (rows, cols))
     ld, step = t.stride()
     if step != 1 and cols > 1:
@@ -280,13 +281,21 @@ def _rows(name, t, dtypes, rows, cols):
     return ld if rows > 1 else cols
 
 
-def _whole(name, t, dtypes, shape):
+def _whole(name, t, dev, dtypes, shape):
     """Address of a contiguous tensor of the given shape (None, where it may be left out, stays None)."""
     if t is None:
         return None
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         _refuse(name, t, dtypes, shape)
     return t.data_ptr()
+
+
+def _scratch(t, dev):
+    """Address and bytes of a workspace."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on the first operand's device, got strides "
+                         f"{t.stride()} on {t.device}")
+    return t.data_ptr(), t.nbytes
 
 
 def _dims(name, t, n):
@@ -295,19 +304,19 @@ def _dims(name, t, n):
     return t.shape
 
 
-def _stream_of(stream, t):
-    """The stream to launch on, as an integer: the one given, or the current one of t's device."""
-    if not t.is_cuda:
+def _stream_of(stream, dev):
+    """The stream to launch on, as an integer: the one given, or the device's current one."""
+    if dev < 0:
         raise ValueError("expected tensors on the GPU")
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _offsets(offs, E):
+def _offsets(offs, dev, E):
     if offs is None and E != 1:
         raise ValueError("offs may be None for one expert only")
-    return _whole("offs", offs, _I32, (E + 1,))
+    return _whole("offs", offs, dev, _I32, (E + 1,))
 
 
 def ft_moe_group_workspace_size(E: int, P: int, N: int, K: int) -> int:
@@ -321,11 +330,11 @@ def ft_moe_group_workspace_size(E: int, P: int, N: int, K: int) -> int:
 def ft_moe_group_gemm(x: torch.Tensor, w: torch.Tensor, offs, y: torch.Tensor, workspace: torch.Tensor, stream=None):
     """y[p] = w[e] . x[p] for the rows p of every expert e (w bf16 [E, N, K]; y bf16 or fp32)."""
     E, N, K = _dims("w", w, 3)
-    P = _dims("x", x, 2)[0]
+    P, dev = _dims("x", x, 2)[0], x.get_device()
     status = (_lib or load()).ft_moe_group_gemm(
-        x.data_ptr(), _rows("x", x, _BF16, P, K), _whole("w", w, _BF16, (E, N, K)), _offsets(offs, E), E, P, N, K,
-        y.data_ptr(), _rows("y", y, _OUT, P, N), _OUT_CODE[y.dtype], workspace.data_ptr(), workspace.nbytes,
-        _stream_of(stream, x))
+        x.data_ptr(), _rows("x", x, dev, _BF16, P, K), _whole("w", w, dev, _BF16, (E, N, K)), _offsets(offs, dev, E), E, P,
+        N, K, y.data_ptr(), _rows("y", y, dev, _OUT, P, N), _OUT_CODE[y.dtype], *_scratch(workspace, dev),
+        _stream_of(stream, dev))
     if status:
         _check(status)
 
@@ -334,11 +343,11 @@ def ft_moe_group_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, offs, dx: torch.T
                             stream=None):
     """dx[p] = w[e]^T . dy[p]: the gradient of ft_moe_group_gemm's rows (dx bf16 or fp32)."""
     E, N, K = _dims("w", w, 3)
-    P = _dims("dy", dy, 2)[0]
+    P, dev = _dims("dy", dy, 2)[0], dy.get_device()
     status = (_lib or load()).ft_moe_group_gemm_dgrad(
-        dy.data_ptr(), _rows("dy", dy, _BF16, P, N), _whole("w", w, _BF16, (E, N, K)), _offsets(offs, E), E, P, N, K,
-        dx.data_ptr(), _rows("dx", dx, _OUT, P, K), _OUT_CODE[dx.dtype], workspace.data_ptr(), workspace.nbytes,
-        _stream_of(stream, dy))
+        dy.data_ptr(), _rows("dy", dy, dev, _BF16, P, N), _whole("w", w, dev, _BF16, (E, N, K)), _offsets(offs, dev, E), E,
+        P, N, K, dx.data_ptr(), _rows("dx", dx, dev, _OUT, P, K), _OUT_CODE[dx.dtype], *_scratch(workspace, dev),
+        _stream_of(stream, dev))
     if status:
         _check(status)
 
@@ -347,11 +356,11 @@ def ft_moe_group_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, offs, dw: torch.T
                             accumulate: bool = False, stream=None):
     """dw[e] = sum of dy[p] x[p]^T over expert e's rows (dw bf16 or fp32 [E, N, K]); accumulate adds to an fp32 dw."""
     E, N, K = _dims("dw", dw, 3)
-    P = _dims("dy", dy, 2)[0]
+    P, dev = _dims("dy", dy, 2)[0], dy.get_device()
     status = (_lib or load()).ft_moe_group_gemm_wgrad(
-        dy.data_ptr(), _rows("dy", dy, _BF16, P, N), x.data_ptr(), _rows("x", x, _BF16, P, K), _offsets(offs, E), E, P,
-        N, K, _whole("dw", dw, _OUT, (E, N, K)), _OUT_CODE[dw.dtype], 1 if accumulate else 0, workspace.data_ptr(),
-        workspace.nbytes, _stream_of(stream, dy))
+        dy.data_ptr(), _rows("dy", dy, dev, _BF16, P, N), x.data_ptr(), _rows("x", x, dev, _BF16, P, K),
+        _offsets(offs, dev, E), E, P, N, K, _whole("dw", dw, dev, _OUT, (E, N, K)), _OUT_CODE[dw.dtype],
+        1 if accumulate else 0, *_scratch(workspace, dev), _stream_of(stream, dev))
     if status:
         _check(status)
 
@@ -361,56 +370,56 @@ def ft_moe_group_gemm_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tenso
     """ft_moe_group_gemm on e4m3 codes (uint8 or float8_e4m3fn) with fp32 scales: x_scale [ceil(K/128), P],
     w_scale [E, ceil(N/128), ceil(K/128)]."""
     E, N, K = _dims("w", w, 3)
-    P = _dims("x", x, 2)[0]
+    P, dev = _dims("x", x, 2)[0], x.get_device()
     nb = (K + 127) // 128
     status = (_lib or load()).ft_moe_group_gemm_fp8(
-        x.data_ptr(), _rows("x", x, _E4M3, P, K), x_scale.data_ptr(), _rows("x_scale", x_scale, _F32, nb, P),
-        _whole("w", w, _E4M3, (E, N, K)), _whole("w_scale", w_scale, _F32, (E, (N + 127) // 128, nb)),
-        _offsets(offs, E), E, P, N, K, y.data_ptr(), _rows("y", y, _OUT, P, N), _OUT_CODE[y.dtype],
-        workspace.data_ptr(), workspace.nbytes, _stream_of(stream, x))
+        x.data_ptr(), _rows("x", x, dev, _E4M3, P, K), x_scale.data_ptr(), _rows("x_scale", x_scale, dev, _F32, nb, P),
+        _whole("w", w, dev, _E4M3, (E, N, K)), _whole("w_scale", w_scale, dev, _F32, (E, (N + 127) // 128, nb)),
+        _offsets(offs, dev, E), E, P, N, K, y.data_ptr(), _rows("y", y, dev, _OUT, P, N), _OUT_CODE[y.dtype],
+        *_scratch(workspace, dev), _stream_of(stream, dev))
     if status:
         _check(status)
 
 
 def ft_moe_quantize_fp8(src: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
     """e4m3 codes [rows, K] and scales [ceil(K/128), rows] of bf16 or fp32 rows."""
-    rows, K = _dims("src", src, 2)
+    (rows, K), dev = _dims("src", src, 2), src.get_device()
     status = (_lib or load()).ft_moe_quantize_fp8(
-        src.data_ptr(), _OUT_CODE.get(src.dtype, 0), _rows("src", src, _OUT, rows, K), rows, K, codes.data_ptr(),
-        _rows("codes", codes, _E4M3, rows, K), scales.data_ptr(),
-        _rows("scales", scales, _F32, (K + 127) // 128, rows), _stream_of(stream, src))
+        src.data_ptr(), _OUT_CODE.get(src.dtype, 0), _rows("src", src, dev, _OUT, rows, K), rows, K, codes.data_ptr(),
+        _rows("codes", codes, dev, _E4M3, rows, K), scales.data_ptr(),
+        _rows("scales", scales, dev, _F32, (K + 127) // 128, rows), _stream_of(stream, dev))
     if status:
         _check(status)
 
 
 def ft_moe_swiglu(gu: torch.Tensor, w, h: torch.Tensor, stream=None):
     """h = w * silu(gate) * up of rows gu = [gate, up] (w: one fp32 weight per row, or None)."""
-    rows, I = _dims("h", h, 2)
+    (rows, I), dev = _dims("h", h, 2), gu.get_device()
     status = (_lib or load()).ft_moe_swiglu(
-        gu.data_ptr(), _rows("gu", gu, _BF16, rows, 2 * I), _whole("w", w, _F32, (rows,)), rows, I, h.data_ptr(),
-        _rows("h", h, _BF16, rows, I), _stream_of(stream, gu))
+        gu.data_ptr(), _rows("gu", gu, dev, _BF16, rows, 2 * I), _whole("w", w, dev, _F32, (rows,)), rows, I,
+        h.data_ptr(), _rows("h", h, dev, _BF16, rows, I), _stream_of(stream, dev))
     if status:
         _check(status)
 
 
 def ft_moe_swiglu_quantize_fp8(gu: torch.Tensor, w, codes: torch.Tensor, scales: torch.Tensor, stream=None):
     """ft_moe_swiglu stored as e4m3 codes [rows, I] and scales [ceil(I/128), rows]."""
-    rows, I = _dims("codes", codes, 2)
+    (rows, I), dev = _dims("codes", codes, 2), gu.get_device()
     status = (_lib or load()).ft_moe_swiglu_quantize_fp8(
-        gu.data_ptr(), _rows("gu", gu, _BF16, rows, 2 * I), _whole("w", w, _F32, (rows,)), rows, I, codes.data_ptr(),
-        _rows("codes", codes, _E4M3, rows, I), scales.data_ptr(),
-        _rows("scales", scales, _F32, (I + 127) // 128, rows), _stream_of(stream, gu))
+        gu.data_ptr(), _rows("gu", gu, dev, _BF16, rows, 2 * I), _whole("w", w, dev, _F32, (rows,)), rows, I,
+        codes.data_ptr(), _rows("codes", codes, dev, _E4M3, rows, I), scales.data_ptr(),
+        _rows("scales", scales, dev, _F32, (I + 127) // 128, rows), _stream_of(stream, dev))
     if status:
         _check(status)
 
 
 def ft_moe_swiglu_backward(gu: torch.Tensor, w, dh: torch.Tensor, dgu: torch.Tensor, dw=None, stream=None):
     """Gradients of ft_moe_swiglu: dgu = [d gate, d up] and, where dw is given, the row weights'."""
-    rows, I = _dims("dh", dh, 2)
+    (rows, I), dev = _dims("dh", dh, 2), gu.get_device()
     status = (_lib or load()).ft_moe_swiglu_backward(
-        gu.data_ptr(), _rows("gu", gu, _BF16, rows, 2 * I), _whole("w", w, _F32, (rows,)), dh.data_ptr(),
-        _rows("dh", dh, _BF16, rows, I), rows, I, dgu.data_ptr(), _rows("dgu", dgu, _BF16, rows, 2 * I),
-        _whole("dw", dw, _F32, (rows,)), _stream_of(stream, gu))
+        gu.data_ptr(), _rows("gu", gu, dev, _BF16, rows, 2 * I), _whole("w", w, dev, _F32, (rows,)), dh.data_ptr(),
+        _rows("dh", dh, dev, _BF16, rows, I), rows, I, dgu.data_ptr(), _rows("dgu", dgu, dev, _BF16, rows, 2 * I),
+        _whole("dw", dw, dev, _F32, (rows,)), _stream_of(stream, dev))
     if status:
         _check(status)
 
