@@ -39,11 +39,19 @@ namespace {
 using namespace grp;
 
 constexpr int kStep = 64;       // contraction steps per stage
-// Long sums into fp32 outputs are cut into parts of this many stages, added in registers: the
-// tensor cores truncate where an fp32 addition rounds, so that the error of one long
-// accumulation grows with its length (5e-6 relative over 8192 steps, against 4.4e-7 for sums in
-// parts of 512). A bf16 output rounds 300 times coarser and keeps one accumulation.
+// Long sums are cut into parts of this many stages, added in registers: the tensor cores truncate
+// where an fp32 addition rounds, so that the error of one long accumulation grows with its length
+// (fp32 outputs: 5e-6 relative over 8192 steps, against 4.4e-7 for sums in parts of 512).
 constexpr int kPartStages = 8;
+// bf16 outputs round at 2^-9 (2e-3) on average and keep one accumulation over up to kLongRows steps. With
+// products of one sign, whose losses add up, it is 5e-5 low after 8192 steps and 4e-4 after 65536, the
+// widest contraction of forward and dgrad; but 0.6% after a million and 2.6% after four, and an expert
+// may have that many rows. wgrad of more than kLongRows rows adds up parts of kLongStages too (256
+// steps 2^-23 each are lost in a part, 3e-5 at most). Its epilogue holds 128 running sums a thread, which costs
+// a wgrad of few stages a unit the more (256 experts of 1024 x 2048, us without / with: 256 rows each 294 / 354,
+// 512 443 / 456, 1024 764 / 788; one of 256 x 256 with 2^21 rows 1676 / 1682).
+constexpr int kLongRows = 65536;
+constexpr int kLongStages = 64;
 // wgrad: units handed out ahead of the epilogue. Small units need the distance to keep loads in
 // flight, and a large one in between makes those behind it wait (Zipf-distributed rows, fp32 dw
 // [256, 1024, 2048]: 2 ahead 524 us, 3 502, 4 513, 6 534).
@@ -116,14 +124,18 @@ struct Unit {
 
 // WG: the wgrad form (both operands transposed, ragged contraction); A_MN: A transposed; ACC: wgrad
 // that adds to what dw holds (a kernel of its own: the branch in the stores cost the plain one 8%,
-// in registers: 256 experts of 1024 x 2048 with 256 rows each 396 and 426 us).
-template <int CG, int BN, bool A_MN, bool WG, bool F32, bool ACC>
+// in registers: 256 experts of 1024 x 2048 with 256 rows each 396 and 426 us); LONG: wgrad into bf16
+// of more than kLongRows rows.
+template <int CG, int BN, bool A_MN, bool WG, bool F32, bool ACC, bool LONG>
 __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
     group_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ GroupParams p)
 {
     static_assert(!WG || A_MN, "wgrad reads both operands transposed");
     static_assert(!ACC || (WG && F32), "only wgrad adds, in fp32");
+    static_assert(!LONG || (WG && !F32), "fp32 outputs always add up parts");
+    constexpr bool kSums = F32 || LONG;        // parts and their running sums
+    constexpr int kPart = F32 ? kPartStages : kLongStages;
     using T = Ring<CG, BN, WG>;
     constexpr int S = T::stages;
     constexpr int kGran = WG ? 64 : 16;        // N indices per CTA come in multiples of this
@@ -328,8 +340,8 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
                 const uint32_t idesc = idesc_bf16(kTileM * CG, x.half * CG, A_MN, WG);
                 // (an expert without rows has no stages: the epilogue writes zeros on its own)
                 for (int b = b0; b < nb; ++b) {
-                    const bool starts = F32 ? (b - b0) % kPartStages == 0 : b == b0;
-                    const bool ends = b == nb - 1 || (F32 && (b - b0) % kPartStages == kPartStages - 1);
+                    const bool starts = kSums ? (b - b0) % kPart == 0 : b == b0;
+                    const bool ends = b == nb - 1 || (kSums && (b - b0) % kPart == kPart - 1);
                     if (starts && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) { dead = true; break; }
                     if (!warp_wait(full + s, ph, abort_flag, wl)) { dead = true; break; }
                     tc::fence_after_sync();
@@ -403,7 +415,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
         for (int u; (u = next_unit()) >= 0 && !dead;) {
             const Unit x = unit_of(u);
             const int nb = last_stage(x.R) - first_stage(x.R);
-            const int parts = F32 ? (nb + kPartStages - 1) / kPartStages : nb > 0;
+            const int parts = kSums ? (nb + kPart - 1) / kPart : nb > 0;
             if (ACC && parts == 0 && split == 1) continue;
             const int mine = min(max(x.cols - h * HC, 0), HC);  // columns of this half in use
             const int m = x.m0 + 32 * q + lane;
@@ -421,7 +433,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
                     store_rows<F32, W>(v, m, p.M, row0 + c, mine - c, p.out, p.ld, ACC);
                 }
             };
-            float sum[F32 ? HC : 1];  // fp32 outputs: the parts' running sums
+            float sum[kSums ? HC : 1];  // the parts' running sums
             for (int t = 0; t < parts; ++t, ++ac) {
                 if (!warp_wait(acc_full + (ac & 1), (ac >> 1) & 1, abort_flag, wl)) { dead = true; break; }
                 tc::fence_after_sync();
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
                     uint32_t v[W];
                     tmem_ld<W>(addr + c, v);
                     tc::wait_ld();
-                    if constexpr (F32) {
+                    if constexpr (kSums) {
 #pragma unroll
                         for (int j = 0; j < W; ++j) sum[c + j] = t ? sum[c + j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
                     } else {
@@ -450,13 +462,13 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
                 }
             }
             if (dead) break;
-            if (F32 || parts == 0) {
+            if (kSums || parts == 0) {
 #pragma unroll
                 for (int c = 0; c < HC; c += W) {
                     if (c >= mine) break;
                     float f[W];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) f[j] = F32 && parts ? sum[F32 ? c + j : 0] : 0.f;
+                    for (int j = 0; j < W; ++j) f[j] = kSums && parts ? sum[kSums ? c + j : 0] : 0.f;
                     emit(c, f);
                 }
             }
@@ -485,11 +497,11 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
 
 namespace {
 
-template <int CG, int BN, bool A_MN, bool WG, bool F32, bool ACC>
+template <int CG, int BN, bool A_MN, bool WG, bool F32, bool ACC, bool LONG>
 cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_units, cudaStream_t s)
 {
     using T = Ring<CG, BN, WG>;
-    auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32, ACC>;
+    auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32, ACC, LONG>;
     constexpr size_t fixed = 1024 + T::stages * T::stage + 8 * (4 * T::stages + 4 + 2 * kAhead) + 4 * kAhead + 16;
     constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
     static_assert(most <= 227 * 1024, "shared memory");
@@ -524,10 +536,12 @@ cudaError_t launch_typed(const GroupGemm &g, const CUtensorMap (&maps)[2], Group
 {
     const int64_t m_tiles = (p.M + kTileM * CG - 1) / (kTileM * CG);
     const int64_t tiles = WG ? (int64_t)g.E * ((p.N + BN - 1) / BN) : g.P / BN + (g.E < g.P ? g.E : g.P);
-    if constexpr (WG)
-        if (g.accumulate) return launch<CG, BN, A_MN, WG, true, true>(maps, p, m_tiles * tiles, s);
-    return g.out_f32 ? launch<CG, BN, A_MN, WG, true, false>(maps, p, m_tiles * tiles, s)
-                     : launch<CG, BN, A_MN, WG, false, false>(maps, p, m_tiles * tiles, s);
+    if constexpr (WG) {
+        if (g.accumulate) return launch<CG, BN, A_MN, WG, true, true, false>(maps, p, m_tiles * tiles, s);
+        if (!g.out_f32 && g.P > kLongRows) return launch<CG, BN, A_MN, WG, false, false, true>(maps, p, m_tiles * tiles, s);
+    }
+    if (g.out_f32) return launch<CG, BN, A_MN, WG, true, false, false>(maps, p, m_tiles * tiles, s);
+    return launch<CG, BN, A_MN, WG, false, false, false>(maps, p, m_tiles * tiles, s);
 }
 
 }  // namespace
