@@ -204,7 +204,8 @@ cudaError_t launch_swiglu_backward(const void *gu, int64_t ld_gu, const float *w
                                    int I, void *dgu, int64_t ld_dgu, float *dw, cudaStream_t s);
 
 // While one exists, the fault injection armed on this thread applies to the launches made; its
-// end disarms it.
+// end disarms it. (A call makes one when its arguments are checked: a refused call launches
+// nothing and leaves the injection armed.)
 struct StallScope {
     StallScope();
     ~StallScope();

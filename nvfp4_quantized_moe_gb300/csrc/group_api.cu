@@ -101,7 +101,6 @@ ft_status ft_moe_group_gemm(const void *x, int64_t ld_x, const void *w, const in
                             size_t workspace_bytes, void *stream)
 {
     FT_NVTX_RANGE("ft_moe_group_gemm");
-    const StallScope stall;
     FT_TRY(check_sizes(E, P, N, K, 8, 8));
     FT_TRY(check_out_dtype(y_dtype));
     FT_TRY(check_group(offs, E, workspace, workspace_bytes));
@@ -115,6 +114,7 @@ ft_status ft_moe_group_gemm(const void *x, int64_t ld_x, const void *w, const in
     g.x = x; g.ld_x = ld_x; g.w = w;
     g.out = y; g.ld_out = ld_y; g.out_f32 = y_dtype == FT_DTYPE_F32;
     g.status = static_cast<int *>(workspace);
+    const StallScope stall;
     return finish(launch_group_gemm(g, static_cast<cudaStream_t>(stream)), "grouped product launch");
 }
 
@@ -123,7 +123,6 @@ ft_status ft_moe_group_gemm_dgrad(const void *dy, int64_t ld_dy, const void *w, 
                                   size_t workspace_bytes, void *stream)
 {
     FT_NVTX_RANGE("ft_moe_group_gemm_dgrad");
-    const StallScope stall;
     FT_TRY(check_sizes(E, P, N, K, 8, 8));
     FT_TRY(check_out_dtype(dx_dtype));
     FT_TRY(check_group(offs, E, workspace, workspace_bytes));
@@ -137,6 +136,7 @@ ft_status ft_moe_group_gemm_dgrad(const void *dy, int64_t ld_dy, const void *w, 
     g.dy = dy; g.ld_dy = ld_dy; g.w = w;
     g.out = dx; g.ld_out = ld_dx; g.out_f32 = dx_dtype == FT_DTYPE_F32;
     g.status = static_cast<int *>(workspace);
+    const StallScope stall;
     return finish(launch_group_gemm(g, static_cast<cudaStream_t>(stream)), "grouped input-gradient launch");
 }
 
@@ -145,7 +145,6 @@ ft_status ft_moe_group_gemm_wgrad(const void *dy, int64_t ld_dy, const void *x, 
                                   void *workspace, size_t workspace_bytes, void *stream)
 {
     FT_NVTX_RANGE("ft_moe_group_gemm_wgrad");
-    const StallScope stall;
     FT_TRY(check_sizes(E, P, N, K, 8, 8));
     FT_TRY(check_out_dtype(dw_dtype));
     if (accumulate != 0 && accumulate != 1) return reject(FT_ERR_INVALID_ARG, "accumulate must be 0 or 1");
@@ -170,6 +169,7 @@ ft_status ft_moe_group_gemm_wgrad(const void *dy, int64_t ld_dy, const void *x, 
     g.dy = dy; g.ld_dy = ld_dy; g.x = x; g.ld_x = ld_x;
     g.out = dw; g.ld_out = K; g.out_f32 = dw_dtype == FT_DTYPE_F32; g.accumulate = accumulate;
     g.status = static_cast<int *>(workspace);
+    const StallScope stall;
     return finish(launch_group_gemm(g, s), "grouped weight-gradient launch");
 }
 
@@ -178,7 +178,6 @@ ft_status ft_moe_group_gemm_fp8(const void *x, int64_t ld_x, const float *x_scal
                                 int64_t ld_y, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream)
 {
     FT_NVTX_RANGE("ft_moe_group_gemm_fp8");
-    const StallScope stall;
     FT_TRY(check_sizes(E, P, N, K, 1, 16));
     FT_TRY(check_out_dtype(y_dtype));
     FT_TRY(check_group(offs, E, workspace, workspace_bytes));
@@ -195,6 +194,7 @@ ft_status ft_moe_group_gemm_fp8(const void *x, int64_t ld_x, const float *x_scal
     g.w = w; g.ws = w_scale;
     g.out = y; g.ld_out = ld_y; g.out_f32 = y_dtype == FT_DTYPE_F32;
     g.status = static_cast<int *>(workspace);
+    const StallScope stall;
     return finish(launch_group_gemm_fp8(g, static_cast<cudaStream_t>(stream)), "grouped 8-bit product launch");
 }
 
