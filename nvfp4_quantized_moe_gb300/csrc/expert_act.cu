@@ -8,7 +8,7 @@
 //   backward   dg = w dh u s (1 + g (1 - s)),  du = w dh g s,  dw = sum dh g s u
 //
 // Measured on one GB300 (copy bandwidth 6.78 TB/s), 65536 rows: SwiGLU forward (512 columns) 29.1 us,
-// 6.9 TB/s; backward 53.2 us, 6.3 TB/s; in 8 bits 31.5 us, 5.3 TB/s (two special functions and the
+// 6.9 TB/s; backward 53.8 us, 6.2 TB/s; in 8 bits 29.1 us, 5.8 TB/s (two special functions and the
 // scaling per value); quantizer (2048 columns) 67.6 us, 6.0 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -84,9 +84,19 @@ __device__ __forceinline__ uint2 block_codes(const float (&v)[8], float scale)
     return make_uint2(e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
 }
 
-// s = 1 / (1 + e^-g): the fast exponential and division, a few 1e-7 relative, far below the
-// rounding of the stored results; e^-g = inf gives 0.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// s = 1 / (1 + e^-g) as (1/4) / (1/4 + e^-g / 4), with e^-g / 4 = 2^(-g log2(e) - 2): one multiply-add before the
+// power of two, and a divisor that stays below 2^126 where s is 1e-38 and g s u may be of any size (the fast
+// reciprocal gives zero above 2^126, which 1 + e^-g passes below g = -87.3). s is 0 below -88.7. The exponent is
+// off by |g| 2^-23 at most and the power by 2^-22: s is within 2^-21 near zero and 1e-5 at g = -88, relative; the
+// stores round to 2^-9 (bf16) or 2^-5 (8 bits) on average. (From e^-|g|, 65536 x 512 in 8 bits take 32.7 us, backward
+// 55.8; as here 29.1 and 53.8.)
+__device__ __forceinline__ float sigmoid(float g)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.4426950408889634f, -2.0f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0.25f + e));
+    return 0.25f * r;
+}
 
 constexpr int kActThreads = 256;
 // Quantizing kernels: 16 lanes per row and block of 128; 8 rows per CTA, so that the scales of a block
