@@ -449,6 +449,15 @@ ft_status ft_moe_set_stage_events(void *const *events);
  * Errors: FT_ERR_INVALID_ARG (skip_producer not 0/1, limit out of range). Host-only. */
 ft_status ft_moe_debug_inject_stall(uint64_t wait_limit_ns, int32_t skip_producer);
 
+/* The kernel that a grouped product of these sizes takes on the current device, without launching it, so that
+ * a test can say which one it is about. plan (out): CTAs that share an output tile (1 or 2), the tile's extent
+ * along the rows (wgrad: along N), CTAs that share a tile's contraction, and whether tiles are handed out
+ * by a counter (1) or in turn (0). P >= 1; out_dtype and accumulate as in the calls (accumulate: wgrad
+ * into fp32 only). Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED, FT_ERR_CUDA. */
+enum { FT_GROUP_FORWARD = 0, FT_GROUP_DGRAD, FT_GROUP_WGRAD, FT_GROUP_FP8 };
+ft_status ft_moe_debug_group_plan(int32_t product, int32_t E, int32_t P, int32_t N, int32_t K, int32_t out_dtype,
+                                  int32_t accumulate, int32_t plan[4]);
+
 /* Number of kernels this library has launched (or captured into a graph) from the
  * calling thread since it was loaded. */
 int64_t ft_moe_launch_count(void);

@@ -22,7 +22,8 @@ __all__ = [
     "FT_NSTAGES", "STAGES", "ft_moe_debug_inject_stall", "ft_moe_workspace_size_w4a4", "ft_moe_forward_w4a4",
     "ft_moe_quantize_nvfp4", "ft_moe_group_workspace_size", "ft_moe_group_gemm", "ft_moe_group_gemm_dgrad",
     "ft_moe_group_gemm_wgrad", "ft_moe_group_gemm_fp8", "ft_moe_quantize_fp8", "ft_moe_swiglu",
-    "ft_moe_swiglu_quantize_fp8", "ft_moe_swiglu_backward",
+    "ft_moe_swiglu_quantize_fp8", "ft_moe_swiglu_backward", "ft_moe_debug_group_plan", "FT_GROUP_FORWARD",
+    "FT_GROUP_DGRAD", "FT_GROUP_WGRAD", "FT_GROUP_FP8",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libftmoe.so")
@@ -42,7 +43,8 @@ EXPORTS = ("ft_moe_layout", "ft_moe_pack", "ft_moe_route", "ft_moe_route_gemm", 
            "ft_moe_debug_inject_stall", "ft_moe_workspace_size_w4a4", "ft_moe_forward_w4a4", "ft_moe_quantize_nvfp4",
            "ft_moe_group_workspace_size", "ft_moe_group_gemm", "ft_moe_group_gemm_dgrad", "ft_moe_group_gemm_wgrad",
            "ft_moe_group_gemm_fp8", "ft_moe_quantize_fp8", "ft_moe_swiglu", "ft_moe_swiglu_quantize_fp8",
-           "ft_moe_swiglu_backward")
+           "ft_moe_swiglu_backward", "ft_moe_debug_group_plan")
+FT_GROUP_FORWARD, FT_GROUP_DGRAD, FT_GROUP_WGRAD, FT_GROUP_FP8 = range(4)
 FT_NSTAGES = 6
 STAGES = ("align", "gate_up", "shared_gate_up", "down", "shared_down", "combine")
 
@@ -119,6 +121,7 @@ def load():
             "ft_moe_quantize_fp8": [P, I32, I64, I32, I32, P, I64, P, I64, P],
             "ft_moe_swiglu": [P, I64, P, I32, I32, P, I64, P],
             "ft_moe_swiglu_quantize_fp8": [P, I64, P, I32, I32, P, I64, P, I64, P],
+            "ft_moe_debug_group_plan": [I32, I32, I32, I32, I32, I32, I32, P],
             "ft_moe_swiglu_backward": [P, I64, P, P, I64, I32, I32, P, I64, P, P],
         }
         for name, args in sigs.items():
@@ -379,6 +382,14 @@ def ft_moe_group_gemm_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tenso
         *_scratch(workspace, dev), _stream_of(stream, dev))
     if status:
         _check(status)
+
+
+def ft_moe_debug_group_plan(product: int, E: int, P: int, N: int, K: int, out_dtype=torch.bfloat16,
+                            accumulate: bool = False) -> tuple:
+    """(CTAs per tile, tile extent, CTAs per contraction, counted) of the kernel that a grouped product takes."""
+    plan = (ctypes.c_int32 * 4)()
+    _check(load().ft_moe_debug_group_plan(product, E, P, N, K, _OUT_CODE.get(out_dtype, 0), int(accumulate), plan))
+    return tuple(plan)
 
 
 def ft_moe_quantize_fp8(src: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):

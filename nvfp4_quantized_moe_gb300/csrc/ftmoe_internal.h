@@ -179,7 +179,16 @@ struct GroupGemm {
     void *out;
     int out_f32, accumulate;
     int *status;
+    int32_t *plan;               // not null: nothing is launched, the kernel's choice goes here
 };
+// What ft_moe_debug_group_plan reports.
+inline void write_plan(int32_t *plan, int ctas, int tile, int split, bool counted)
+{
+    plan[0] = ctas;
+    plan[1] = tile;
+    plan[2] = split;
+    plan[3] = counted;
+}
 cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s);
 // A grouped e4m3 product with block scales (group_gemm_fp8.cu).
 struct GroupGemm8 {
@@ -191,6 +200,7 @@ struct GroupGemm8 {
     void *out;
     int out_f32;
     int *status;
+    int32_t *plan;               // as in GroupGemm
 };
 cudaError_t launch_group_gemm_fp8(const GroupGemm8 &g, cudaStream_t s);
 // expert_act.cu. Strides in elements; scales are [ceil(columns / 128)][ld_scales].

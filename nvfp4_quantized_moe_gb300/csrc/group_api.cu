@@ -198,6 +198,30 @@ ft_status ft_moe_group_gemm_fp8(const void *x, int64_t ld_x, const float *x_scal
     return finish(launch_group_gemm_fp8(g, static_cast<cudaStream_t>(stream)), "grouped 8-bit product launch");
 }
 
+ft_status ft_moe_debug_group_plan(int32_t product, int32_t E, int32_t P, int32_t N, int32_t K, int32_t out_dtype,
+                                  int32_t accumulate, int32_t *plan)
+{
+    if (product < FT_GROUP_FORWARD || product > FT_GROUP_FP8 || P < 1 || !plan || accumulate < 0 ||
+        accumulate > (product == FT_GROUP_WGRAD && out_dtype == FT_DTYPE_F32))
+        return reject(FT_ERR_INVALID_ARG, "need a product, P >= 1, accumulate for a wgrad into fp32 only, and room for the plan");
+    const bool fp8 = product == FT_GROUP_FP8;
+    FT_TRY(check_sizes(E, P, N, K, fp8 ? 1 : 8, fp8 ? 16 : 8));
+    FT_TRY(check_out_dtype(out_dtype));
+    if (fp8) {
+        GroupGemm8 g = {};
+        g.E = E; g.P = P; g.N = N; g.K = K;
+        g.out_f32 = out_dtype == FT_DTYPE_F32;
+        g.plan = plan;
+        return finish(launch_group_gemm_fp8(g, nullptr), "plan of a grouped 8-bit product");
+    }
+    GroupGemm g = {};
+    g.form = product == FT_GROUP_FORWARD ? kGroupForward : product == FT_GROUP_DGRAD ? kGroupDgrad : kGroupWgrad;
+    g.E = E; g.P = P; g.N = N; g.K = K;
+    g.out_f32 = out_dtype == FT_DTYPE_F32; g.accumulate = accumulate;
+    g.plan = plan;
+    return finish(launch_group_gemm(g, nullptr), "plan of a grouped product");
+}
+
 // Rows and columns of the row kernels.
 static ft_status check_rows(int rows, int cols, int unit)
 {

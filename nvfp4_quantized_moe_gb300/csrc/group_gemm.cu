@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
 namespace {
 
 template <int CG, int BN, bool A_MN, bool WG, bool F32, bool ACC, bool LONG>
-cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_units, cudaStream_t s)
+cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_units, int32_t *plan, cudaStream_t s)
 {
     using T = Ring<CG, BN, WG>;
     auto kern = group_gemm_kernel<CG, BN, A_MN, WG, F32, ACC, LONG>;
@@ -518,7 +518,12 @@ cudaError_t launch(const CUtensorMap (&maps)[2], GroupParams &p, int64_t max_uni
     int64_t grid = p.split > 1 ? max_units : clusters.get(kern, CG, T::threads, most);
     if (max_units < grid) grid = max_units;
     if (grid < 1) grid = 1;
-    if (WG && CG == 2 && p.E > 1 && max_units > 4 * grid) {  // units of unlike cost, several each
+    const bool counted = WG && CG == 2 && p.E > 1 && max_units > 4 * grid;  // units of unlike cost, several each
+    if (plan) {
+        write_plan(plan, CG, BN, p.split, counted);
+        return cudaSuccess;
+    }
+    if (counted) {
         const cudaError_t me = cudaMemsetAsync(p.status + 16, 0, sizeof(int), s);
         if (me != cudaSuccess) return me;
         p.counter = p.status + 16;
@@ -537,11 +542,11 @@ cudaError_t launch_typed(const GroupGemm &g, const CUtensorMap (&maps)[2], Group
     const int64_t m_tiles = (p.M + kTileM * CG - 1) / (kTileM * CG);
     const int64_t tiles = WG ? (int64_t)g.E * ((p.N + BN - 1) / BN) : g.P / BN + (g.E < g.P ? g.E : g.P);
     if constexpr (WG) {
-        if (g.accumulate) return launch<CG, BN, A_MN, WG, true, true, false>(maps, p, m_tiles * tiles, s);
-        if (!g.out_f32 && g.P > kLongRows) return launch<CG, BN, A_MN, WG, false, false, true>(maps, p, m_tiles * tiles, s);
+        if (g.accumulate) return launch<CG, BN, A_MN, WG, true, true, false>(maps, p, m_tiles * tiles, g.plan, s);
+        if (!g.out_f32 && g.P > kLongRows) return launch<CG, BN, A_MN, WG, false, false, true>(maps, p, m_tiles * tiles, g.plan, s);
     }
-    if (g.out_f32) return launch<CG, BN, A_MN, WG, true, false, false>(maps, p, m_tiles * tiles, s);
-    return launch<CG, BN, A_MN, WG, false, false, false>(maps, p, m_tiles * tiles, s);
+    if (g.out_f32) return launch<CG, BN, A_MN, WG, true, false, false>(maps, p, m_tiles * tiles, g.plan, s);
+    return launch<CG, BN, A_MN, WG, false, false, false>(maps, p, m_tiles * tiles, g.plan, s);
 }
 
 }  // namespace
@@ -571,8 +576,9 @@ cudaError_t launch_group_gemm(const GroupGemm &g, cudaStream_t s)
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap maps[2];
-    bool ok;
-    if (wg) {  // A: x [P][K] read along k; B: dy [P][N] read along n
+    bool ok = true;
+    if (g.plan) {  // nothing to read
+    } else if (wg) {  // A: x [P][K] read along k; B: dy [P][N] read along n
         ok = make_tensor_map_2d(&maps[0], bf, g.x, g.K, g.P, 2 * (uint64_t)g.ld_x, 64, kStep, sw) &&
              make_tensor_map_2d(&maps[1], bf, g.dy, g.N, g.P, 2 * (uint64_t)g.ld_dy, 64, kStep, sw);
     } else {   // A: w [E][N][K]; B: x [P][K] or dy [P][N]

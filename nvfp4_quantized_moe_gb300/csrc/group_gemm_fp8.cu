@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(RingW::threads, 1)
 namespace {
 
 template <int BN, bool F32>
-cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p, cudaStream_t s)
+cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p, int32_t *plan, cudaStream_t s)
 {
     using T = Ring8<BN>;
     auto kern = group_gemm_fp8_kernel<BN, F32>;
@@ -668,6 +668,10 @@ cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p,
     // long as all clusters run at once.
     p.split = 1;
     while (p.split < 8 && p.K >= 4 * kStep8 * p.split && units <= clusters.get(kern, 2 * p.split, kThreads8, most)) p.split *= 2;
+    if (plan) {
+        write_plan(plan, 1, BN, p.split, false);
+        return cudaSuccess;
+    }
     int64_t grid = p.split > 1 ? units : sm_count();
     if (units < grid) grid = units;
     if (grid < 1) grid = 1;
@@ -725,15 +729,20 @@ cudaError_t launch_group_gemm_fp8(const GroupGemm8 &g, cudaStream_t s)
     const int64_t per = g.P / (g.E < g.P ? g.E : g.P);
     const int64_t pairs = (int64_t)(g.N + 255) / 256 * (g.P / 256 + (g.E < g.P ? g.E : g.P));
     const int bn = per <= 24 ? 32 : per < 128 || g.N <= kTileM || 4 * pairs < sm_count() ? 128 : 256;
+    if (g.plan && bn == 256) {
+        write_plan(g.plan, 2, bn, 1, false);
+        return cudaSuccess;
+    }
     CUtensorMap w, x;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    if (!make_tensor_map_3d(&w, u8, g.w, g.K, g.N, g.E, g.K, (uint64_t)g.K * g.N, kStep8, bn == 256 ? 64 : kTileM,
+    if (g.plan) {  // nothing to read
+    } else if (!make_tensor_map_3d(&w, u8, g.w, g.K, g.N, g.E, g.K, (uint64_t)g.K * g.N, kStep8, bn == 256 ? 64 : kTileM,
                             CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_tensor_map_2d(&x, u8, g.x, g.K, g.P, g.ld_x, kStep8, bn == 32 ? Ring8<32>::box_rows : Ring8<128>::box_rows,
                             CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    if (bn == 32) return g.out_f32 ? launch8<32, true>(w, x, p, s) : launch8<32, false>(w, x, p, s);
-    if (bn == 128) return g.out_f32 ? launch8<128, true>(w, x, p, s) : launch8<128, false>(w, x, p, s);
+    if (bn == 32) return g.out_f32 ? launch8<32, true>(w, x, p, g.plan, s) : launch8<32, false>(w, x, p, g.plan, s);
+    if (bn == 128) return g.out_f32 ? launch8<128, true>(w, x, p, g.plan, s) : launch8<128, false>(w, x, p, g.plan, s);
     return g.out_f32 ? launch_wide<true>(w, x, p, s) : launch_wide<false>(w, x, p, s);
 }
 

@@ -111,3 +111,14 @@ def test_binding_refuses_what_it_cannot_pass(ft):
     for call in bad:
         with pytest.raises(ValueError):
             call()
+
+
+def test_plan_refusals(ft):
+    plan = (ctypes.c_int32 * 4)()
+    call = ft.load().ft_moe_debug_group_plan
+    good = dict(product=2, E=2, P=8, N=128, K=64, dtype=2, accumulate=1, plan=plan)
+    for change, code in ((dict(product=-1), 1), (dict(product=4), 1), (dict(P=0), 1), (dict(plan=None), 1), (dict(accumulate=2), 1),
+                         (dict(dtype=3), 1), (dict(product=0), 1), (dict(dtype=0, accumulate=0), 1), (dict(E=0), 1),
+                         (dict(N=12), 3), (dict(product=3, accumulate=0, K=72), 3), (dict(E=1025), 3)):
+        assert call(*dict(good, **change).values()) == code, change
+        assert ft.ft_last_error()
