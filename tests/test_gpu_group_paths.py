@@ -206,3 +206,16 @@ def test_the_counter_runs_where_the_plan_says(ft, out, accumulate):
         left = int(ws[64:68].view(torch.int32)[0])
         units = E * ((N + 255) // 256) * ((K + 255) // 256)
         assert left == -1 if not counted else units - 100 <= left <= units
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_rows_of_no_expert(ft, name):
+    """Every expert is empty although there are rows: nothing is written but the zeros of a weight gradient."""
+    case = Case(ft, name)
+    case.offs.fill_(case.P // 2)
+    out = case.run(case.base.clone())
+    assert case.status() == "FT_OK"
+    if case.product == WGRAD and not case.accumulate:
+        assert not out.any()
+    else:
+        assert torch.equal(_bits(out), _bits(case.base))
