@@ -35,6 +35,7 @@
  *   - All device memory is owned by the caller. The library allocates nothing on
  *     the device and keeps no per-call state; sizes come from ft_moe_layout and
  *     ft_moe_workspace_size.
+ *   - Any host thread may call; calls that may run at once need workspaces and outputs of their own.
  *   - Every call that takes a stream is asynchronous on that stream (cudaStream_t,
  *     passed as void*; NULL is the legacy default stream). Argument and geometry
  *     errors are detected on the host and returned before anything is launched.
@@ -287,16 +288,20 @@ ft_status ft_moe_quantize_nvfp4(const void *src, int32_t src_dtype, int32_t rows
  *   forward  y[p, n]     = sum_k x[p, k]  * w[e, n, k]
  *   dgrad    dx[p, k]    = sum_n dy[p, n] * w[e, n, k]
  *   wgrad    dw[e, n, k] = sum_p dy[p, n] * x[p, k]     (zero for an expert without rows)
- * Sums are fp32, rounded once when stored. Every output depends on its own expert's rows alone:
+ * Sums are fp32, however long, rounded once when stored. Every output depends on its own expert's rows alone:
  * a value that is not finite stays inside the rows (or weights) that it belongs to. Results do
  * not change from run to run.
  *   x, dy, y, dx  device rows, ld_* elements apart (a multiple of 8), 16-byte aligned; inputs are
  *                 bf16, outputs bf16 or fp32 (*_dtype)
  *   w             device bf16 [E, N, K], contiguous, 16-byte aligned
- *   dw            device bf16 or fp32 [E, N, K], contiguous; accumulate = 1 (fp32 only) adds to it
+ *   dw            device bf16 or fp32 [E, N, K], contiguous; accumulate = 1 (fp32 only) adds to it, one
+ *                 fp32 addition per element, made in L2: it takes what dw holds below 2^-126 for zero, and
+ *                 gives zero for sums below that
  *   workspace     device, >= ft_moe_group_workspace_size bytes, 256-byte aligned; its first bytes
- *                 hold the status word (ft_moe_read_status): FT_ERR_INVALID_ROUTING when offs
- *                 decreases or leaves [0, P] (its rows are then clamped and the results undefined)
+ *                 hold the last call's status word (ft_moe_read_status): FT_ERR_INVALID_ROUTING when offs
+ *                 decreases or leaves [0, P] (its rows are then clamped and the results undefined).
+ *                 One call at a time: wgrad counts the tiles it hands out there, so that calls that may run
+ *                 at once, on two streams, need a workspace each (with one, tiles of dw would be left out)
  * N and K are multiples of 8, at most 65536; E <= 1024; P <= 2^25. P = 0 computes nothing (wgrad
  * then clears dw, or leaves it when accumulating). Errors: FT_ERR_INVALID_ARG,
  * FT_ERR_UNSUPPORTED (sizes outside these limits), FT_ERR_WORKSPACE, FT_ERR_CUDA. */

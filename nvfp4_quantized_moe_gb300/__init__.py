@@ -261,6 +261,7 @@ def ft_moe_quantize_nvfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.
                                         _stream(stream, src)))
 
 
+# A workspace belongs to one call at a time: calls on two streams need one each.
 # The expert products and row kernels are short calls: what follows checks what the C call cannot
 # see (types, shapes, layouts, and that all tensors lie on the first one's device) and passes plain
 # integers.

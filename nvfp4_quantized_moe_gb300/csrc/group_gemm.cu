@@ -16,9 +16,12 @@
 //   - many rows per expert: the tensor cores. Dense 4864 x 4096 x 4096 takes 84 us, 1940 TFLOP/s
 //     (cuBLAS 82). Tiles of 256 x 256 by pairs of CTAs: one CTA alone would have to load 48 KB per
 //     stage that its MMAs finish in a quarter of a microsecond.
-//   - few rows: the weights' one pass through memory. 64 tokens over 256 experts of 1024 x 2048
-//     (0.93 GB) take 139 us, 6.7 TB/s; 4096 tokens over 256 experts of 4096 x 4096 (dgrad, 8.9 GB)
-//     1.18 ms, 7.6 TB/s. DRAM traffic equals what the operands hold.
+//   - few rows: the weights' one pass through memory. 64 tokens that reach 222 of 256 experts of 1024 x 2048
+//     (0.93 GB) take 139 us, 6.7 TB/s; 2560 rows over 256 experts of 4096 x 4096 (8.6 GB) 1.20 ms in dgrad,
+//     7.2 TB/s. DRAM traffic equals what the operands hold.
+//   - both at once, where a few experts have most rows: the weights of the others, then the MMAs of these.
+//     4096 Zipf-distributed tokens that reach 165 of those 256 experts of 4096 x 4096 (dgrad, 6.1 GB) take
+//     1.16 ms, 5.2 TB/s; its 133 experts below 128 rows alone 0.68, the others alone 0.59.
 //   - a handful of rows: the chain of latencies from launch to store. One token over 8 of 256
 //     experts (2048 x 512) takes 6.7 us, one expert of 2048 x 2048 with 4 rows 7.0 us.
 //   - wgrad: the output. fp32 dw [256, 1024, 2048] (2.1 GB) of 65536 rows takes 394 us with 256 rows
@@ -41,15 +44,17 @@ using namespace grp;
 constexpr int kStep = 64;       // contraction steps per stage
 // Long sums are cut into parts of this many stages, added in registers: the tensor cores truncate
 // where an fp32 addition rounds, so that the error of one long accumulation grows with its length
-// (fp32 outputs: 5e-6 relative over 8192 steps, against 4.4e-7 for sums in parts of 512).
+// (fp32 outputs: 5e-6 relative over 8192 steps, against 4.4e-7 for sums in parts of 512; elementary
+// operations in fp32 have 1.7e-7).
 constexpr int kPartStages = 8;
-// bf16 outputs round at 2^-9 (2e-3) on average and keep one accumulation over up to kLongRows steps. With
-// products of one sign, whose losses add up, it is 5e-5 low after 8192 steps and 4e-4 after 65536, the
-// widest contraction of forward and dgrad; but 0.6% after a million and 2.6% after four, and an expert
-// may have that many rows. wgrad of more than kLongRows rows adds up parts of kLongStages too (256
-// steps 2^-23 each are lost in a part, 3e-5 at most). Its epilogue holds 128 running sums a thread, which costs
-// a wgrad of few stages a unit the more (256 experts of 1024 x 2048, us without / with: 256 rows each 294 / 354,
-// 512 443 / 456, 1024 764 / 788; one of 256 x 256 with 2^21 rows 1676 / 1682).
+// bf16 outputs round at 2^-9 (2e-3) on average and keep one accumulation over up to kLongRows steps. Over 4096
+// steps single roundings then fall to the other side than with fp32 sums, 1e-4 in norm, and the error against
+// 64 bits is the same. Products of one sign, whose losses add up, come out 3e-5 low after 8192 steps and 4e-4
+// after 65536, the widest contraction of forward and dgrad; after a million it is 0.6%, after four 2.6%, and
+// an expert may have that many rows: wgrad of more than kLongRows rows adds up parts of kLongStages
+// too, which lose 3e-5 at most (256 truncations of 2^-23). Its epilogue holds 128 running sums a thread, at a
+// cost where units are short (256 experts of 1024 x 2048, us without / with: 256 rows each 294 / 354, 512
+// 443 / 455, 1024 764 / 771; one of 256 x 256 with 2^21 rows 1676 / 1682).
 constexpr int kLongRows = 65536;
 constexpr int kLongStages = 64;
 // wgrad: units handed out ahead of the epilogue. Small units need the distance to keep loads in

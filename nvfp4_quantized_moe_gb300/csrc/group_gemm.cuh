@@ -215,7 +215,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 // ---------------------------------------------------------------- stores
 
 // *to += v, without waiting for what it holds. Each element gets one such addition in a launch, so
-// that there is no order to depend on.
+// that there is no order to depend on. (The addition in L2 takes subnormal values for zero.)
 __device__ __forceinline__ void add_global(float *to, float v)
 {
     asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(v) : "memory");

@@ -656,7 +656,8 @@ cudaError_t launch8(const CUtensorMap &w, const CUtensorMap &x, Group8Params &p,
 {
     using T = Ring8<BN>;
     auto kern = group_gemm_fp8_kernel<BN, F32>;
-    constexpr size_t fixed = 1024 + T::stages * T::stage + 4 * T::slots * BN + 8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) + 16;
+    constexpr size_t fixed = 1024 + T::stages * T::stage + 4 * T::slots * BN +
+                             8 * (2 * T::stages + 2 * T::acc + 2 * T::slots) + 16;
     constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
     static_assert(most <= 227 * 1024, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
@@ -696,7 +697,8 @@ cudaError_t launch_wide(const CUtensorMap &w, const CUtensorMap &x, const Group8
     static ClusterLimit clusters;
     int64_t grid = clusters.get(kern, 2, T::threads, most);
     if (units < grid) grid = units;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), fixed + table_bytes(p.E), 2, s, w, x, p);
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), fixed + table_bytes(p.E), 2, s, w, x,
+                                          p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
