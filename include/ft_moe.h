@@ -360,6 +360,122 @@ ft_status ft_moe_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float 
 ft_status ft_moe_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, const void *dh, int64_t ld_dh, int32_t rows,
                                  int32_t I, void *dgu, int64_t ld_dgu, float *dw, void *stream);
 
+/* ---- microscaled 4-bit products (MXFP4) ---------------------------------------- */
+
+/* The forward product with both operands in MXFP4: e2m1 codes, two to a byte (the even element in the low
+ * half), with a power of two as scale for every 32 elements along K (the byte s + 127 for 2^s; 255 is NaN):
+ *   y[p, n] = sum_b 2^(xs[p, b] + ws[e, n, b]) * sum_{k in block b} x[p, k] * w[e, n, k]
+ * on the 4-bit tensor cores, which apply the scales themselves; sums are fp32. Rows, offs, workspace and
+ * errors as ft_moe_group_gemm. Scale bytes of four neighbouring blocks (128 elements) form a word, the
+ * first block's byte lowest; bytes of blocks beyond K are 0.
+ *   x        device codes, rows ld_x bytes apart (a multiple of 16), 16-byte aligned
+ *   x_scale  device words [ceil(K / 128)][ld_xs], one per row, ld_xs >= P and a multiple of 4, 16-byte aligned
+ *   w        device codes [E, N, K / 2], contiguous, 16-byte aligned
+ *   w_scale  device words [E, ceil(N / 128), ceil(K / 128), 128], 16-byte aligned: a tile of 128 rows and
+ *            128 elements has row n's word at 4 * (n % 32) + n % 128 / 32. (Words of rows beyond N may be any.)
+ *   y        device bf16 or fp32 rows, ld_y >= N apart, 16-byte aligned
+ * K is a multiple of 32; N is any size. */
+ft_status ft_moe_group_gemm_mxfp4(const void *x, int64_t ld_x, const void *x_scale, int64_t ld_xs, const void *w,
+                                  const void *w_scale, const int32_t *offs, int32_t E, int32_t P, int32_t N, int32_t K, void *y,
+                                  int64_t ld_y, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* MXFP4 codes and scales of activation rows, as ft_moe_group_gemm_mxfp4 reads x: per 32 values of a row the
+ * scale is the smallest power of two 2^s (s >= -127) with amax <= 6 * 2^s, 6 being the largest e2m1 value, and
+ * code = e2m1(v * 2^-s), to nearest with ties to even: exact scaling, nothing saturates. A block that holds an
+ * infinity or a NaN gets the scale NaN.
+ *   src     device bf16 or fp32 rows, ld_src elements apart, 16-byte aligned rows
+ *   codes   device u8 rows, ld_codes bytes apart (a multiple of 16), 16-byte aligned (out)
+ *   scales  device words [ceil(K / 128)][ld_scales], ld_scales >= rows (out)
+ * K is a multiple of 32. rows = 0 is a no-op. The _weights form quantizes matrices [E, N, K] (contiguous) into
+ * codes [E, N, K / 2] and the tiles that the product reads as w_scale; ft_moe_pack_mxfp4_scales makes
+ * those tiles of a checkpoint's scale bytes [E, N, K / 32]. Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED,
+ * FT_ERR_CUDA. */
+ft_status ft_moe_quantize_mxfp4(const void *src, int32_t src_dtype, int64_t ld_src, int32_t rows, int32_t K, uint8_t *codes,
+                                int64_t ld_codes, void *scales, int64_t ld_scales, void *stream);
+ft_status ft_moe_quantize_mxfp4_weights(const void *src, int32_t src_dtype, int32_t E, int32_t N, int32_t K, uint8_t *codes,
+                                        void *tiles, void *stream);
+ft_status ft_moe_pack_mxfp4_scales(const uint8_t *src, int32_t E, int32_t N, int32_t K, void *tiles, void *stream);
+
+/* ft_moe_swiglu whose fp32 result is stored in MXFP4 with ft_moe_quantize_mxfp4's rule (I a multiple of 32,
+ * 16-byte aligned rows). */
+ft_status ft_moe_swiglu_quantize_mxfp4(const void *gu, int64_t ld_gu, const float *w, int32_t rows, int32_t I, uint8_t *codes,
+                                       int64_t ld_codes, void *scales, int64_t ld_scales, void *stream);
+
+/* ---- tokens sorted by expert, and back ------------------------------------------ */
+
+/* Slot s = t * k + j is token t's j-th expert. slot[p] is the slot that the sorted row p holds (ft_moe_align's
+ * sorted_slot; with block = 1 row p belongs to expert e for offs[e] <= p < offs[e + 1]), and pos[s] the row
+ * that holds slot s.
+ *   dispatch           out[p] = x[slot[p] / k], and the rows' block scales and weights along with them:
+ *                      out_scale[b, p] = x_scale[b, slot[p] / k],  row_w[p] = w[slot[p]],  pos[slot[p]] = p
+ *   dispatch_backward  dx[t] = sum_j dout[pos[t, j]],  dw[t, j] = drow_w[pos[t, j]]
+ *   combine            out[t] = sum_j w[t, j] * y[pos[t, j]] + add[t]
+ *   combine_backward   dy[pos[t, j]] = w[t, j] * dout[t],  dw[t, j] = sum_h dout[t, h] * y[pos[t, j], h]
+ * Sums run over j in order, in fp32, rounded once when stored; results do not change from run to run.
+ *   x, out     dispatch: device rows of any type, row_bytes each (even), ld_x and ld_out bytes apart, 2-byte aligned
+ *   slot       device i32 [P]; a value outside [0, T * k) (ft_moe_align's padding) makes a row of zeros with
+ *              zero scales and weight
+ *   count      device i32 [1] or NULL: rows from it on are left as they were (ft_moe_align's n_padded, which is
+ *              below P where ids were invalid)
+ *   x_scale, out_scale  device words [scale_blocks][ld], one 4-byte scale (or four 1-byte ones) per 128 columns
+ *              and row, as the quantizers write them; scale_blocks = 0: none
+ *   w          device f32 [T, k]; combine and its backward: NULL means 1
+ *   row_w      device f32 [P] (out) or NULL
+ *   pos        device i32 [T, k]; dispatch writes it (out, or NULL): -1 where no row holds the slot, the last
+ *              row where several do. The others read it: a value outside [0, P) counts as no row (nothing added,
+ *              dw 0), two slots with the same row are undefined for combine_backward's dy
+ *   y, dout, add, dx  device bf16 or fp32 rows (add: of out's type, may be out itself); dy bf16; any H, aligned to
+ *              an element (16-byte aligned rows with H a multiple of 8 are faster). combine_backward leaves
+ *              rows of dy that no slot has as they were
+ *   dw         device f32 [T, k] (out) or NULL (combine_backward: y is then not read)
+ * k <= 32, T <= 2^20, P <= 2^25. T = 0 or P = 0 is allowed. Outputs may not overlap inputs otherwise. Errors:
+ * FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED, FT_ERR_CUDA. */
+ft_status ft_moe_dispatch(const void *x, int64_t ld_x, int32_t row_bytes, int32_t T, int32_t k, const int32_t *slot, int32_t P,
+                          const int32_t *count, void *out, int64_t ld_out, const void *x_scale, int64_t ld_xs,
+                          int32_t scale_blocks, void *out_scale, int64_t ld_os, const float *w, float *row_w, int32_t *pos,
+                          void *stream);
+ft_status ft_moe_dispatch_backward(const void *dout, int64_t ld_dout, int32_t dout_dtype, const int32_t *pos, int32_t T,
+                                   int32_t k, int32_t P, int32_t H, const float *drow_w, void *dx, int64_t ld_dx,
+                                   int32_t dx_dtype, float *dw, void *stream);
+ft_status ft_moe_combine(const void *y, int64_t ld_y, int32_t y_dtype, const int32_t *pos, const float *w, int32_t T, int32_t k,
+                         int32_t P, int32_t H, const void *add, int64_t ld_add, void *out, int64_t ld_out, int32_t out_dtype,
+                         void *stream);
+ft_status ft_moe_combine_backward(const void *dout, int64_t ld_dout, int32_t dout_dtype, const void *y, int64_t ld_y,
+                                  int32_t y_dtype, const int32_t *pos, const float *w, int32_t T, int32_t k, int32_t P,
+                                  int32_t H, void *dy, int64_t ld_dy, float *dw, void *stream);
+
+/* ---- residual norm ---------------------------------------------------------------- */
+
+/* Root-mean-square norm of rows with the residual's addition, in front of an expert layer:
+ *   total = x + residual        stored in the residual's type (total = x, not stored, without a residual)
+ *   rstd  = 1 / sqrt(mean_h total^2 + eps)
+ *   y     = total * rstd * (w_offset + w)
+ * of the total as it is stored; fp32 inside. y goes into bf16 (y), into e4m3 codes with block scales by
+ * ft_moe_quantize_fp8's rule from the fp32 y (codes, scales; H a multiple of 16), or both.
+ *   x         device bf16 rows
+ *   residual, total  device rows of total_dtype (bf16 or fp32), both or neither; total may be residual itself
+ *   w         device [H], bf16 or fp32 (w_dtype)
+ *   y         device bf16 rows or NULL;  codes, scales as in ft_moe_quantize_fp8, or NULL
+ *   rstd      device f32 [rows] (out) or NULL: the backward pass wants it
+ * Rows are ld_* elements apart, aligned to an element (16-byte aligned ones with H a multiple of 8 are faster). The
+ * backward form gives, from dy and the gradient dtotal that reaches total past the norm (or NULL), with
+ * n = total * rstd and g = dy * (w_offset + w):
+ *   dx = dtotal + rstd * (g - n * mean_h(g * n))       (of total's type: the gradient of x and of the residual)
+ *   dw = sum over the rows of dy * n                   (f32 [H], or NULL; accumulate = 1 adds to it)
+ * dx may be dtotal itself. workspace (for dw): >= ft_moe_rmsnorm_workspace_size bytes, 256-byte aligned, one call
+ * at a time. Results do not change from run to run. H <= 16384, rows <= 2^25. rows = 0 computes nothing (backward then
+ * clears dw, or leaves it when accumulating). Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED, FT_ERR_WORKSPACE,
+ * FT_ERR_CUDA. */
+ft_status ft_moe_rmsnorm(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, void *total,
+                         int64_t ld_total, int32_t total_dtype, const void *w, int32_t w_dtype, float w_offset, float eps,
+                         int32_t rows, int32_t H, void *y, int64_t ld_y, uint8_t *codes, int64_t ld_codes, float *scales,
+                         int64_t ld_scales, float *rstd, void *stream);
+ft_status ft_moe_rmsnorm_workspace_size(int32_t rows, int32_t H, size_t *bytes);
+ft_status ft_moe_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *total, int64_t ld_total, int32_t total_dtype,
+                                  const void *w, int32_t w_dtype, float w_offset, const float *rstd, const void *dtotal,
+                                  int64_t ld_dtotal, int32_t rows, int32_t H, void *dx, int64_t ld_dx, float *dw,
+                                  int32_t accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- test and debug exports ------------------------------------------------ */
 
 /* Expert-sorted, tile-padded slot order (the moe_align step named in "feat(qwen3_5_moe):
@@ -459,7 +575,7 @@ ft_status ft_moe_debug_inject_stall(uint64_t wait_limit_ns, int32_t skip_produce
  * along the rows (wgrad: along N), CTAs that share a tile's contraction, and whether tiles are handed out
  * by a counter (1) or in turn (0). P >= 1; out_dtype and accumulate as in the calls (accumulate: wgrad
  * into fp32 only). Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED, FT_ERR_CUDA. */
-enum { FT_GROUP_FORWARD = 0, FT_GROUP_DGRAD, FT_GROUP_WGRAD, FT_GROUP_FP8 };
+enum { FT_GROUP_FORWARD = 0, FT_GROUP_DGRAD, FT_GROUP_WGRAD, FT_GROUP_FP8, FT_GROUP_MXFP4 };
 ft_status ft_moe_debug_group_plan(int32_t product, int32_t E, int32_t P, int32_t N, int32_t K, int32_t out_dtype,
                                   int32_t accumulate, int32_t plan[4]);
 

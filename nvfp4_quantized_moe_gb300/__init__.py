@@ -23,7 +23,11 @@ __all__ = [
     "ft_moe_quantize_nvfp4", "ft_moe_group_workspace_size", "ft_moe_group_gemm", "ft_moe_group_gemm_dgrad",
     "ft_moe_group_gemm_wgrad", "ft_moe_group_gemm_fp8", "ft_moe_quantize_fp8", "ft_moe_swiglu",
     "ft_moe_swiglu_quantize_fp8", "ft_moe_swiglu_backward", "ft_moe_debug_group_plan", "FT_GROUP_FORWARD",
-    "FT_GROUP_DGRAD", "FT_GROUP_WGRAD", "FT_GROUP_FP8",
+    "FT_GROUP_DGRAD", "FT_GROUP_WGRAD", "FT_GROUP_FP8", "FT_GROUP_MXFP4", "ft_moe_group_gemm_mxfp4",
+    "ft_moe_quantize_mxfp4", "ft_moe_quantize_mxfp4_weights", "ft_moe_pack_mxfp4_scales",
+    "ft_moe_swiglu_quantize_mxfp4", "alloc_mxfp4_scales", "ft_moe_dispatch", "ft_moe_dispatch_backward",
+    "ft_moe_combine", "ft_moe_combine_backward", "ft_moe_rmsnorm", "ft_moe_rmsnorm_workspace_size",
+    "ft_moe_rmsnorm_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libftmoe.so")
@@ -43,8 +47,11 @@ EXPORTS = ("ft_moe_layout", "ft_moe_pack", "ft_moe_route", "ft_moe_route_gemm", 
            "ft_moe_debug_inject_stall", "ft_moe_workspace_size_w4a4", "ft_moe_forward_w4a4", "ft_moe_quantize_nvfp4",
            "ft_moe_group_workspace_size", "ft_moe_group_gemm", "ft_moe_group_gemm_dgrad", "ft_moe_group_gemm_wgrad",
            "ft_moe_group_gemm_fp8", "ft_moe_quantize_fp8", "ft_moe_swiglu", "ft_moe_swiglu_quantize_fp8",
-           "ft_moe_swiglu_backward", "ft_moe_debug_group_plan")
-FT_GROUP_FORWARD, FT_GROUP_DGRAD, FT_GROUP_WGRAD, FT_GROUP_FP8 = range(4)
+           "ft_moe_swiglu_backward", "ft_moe_debug_group_plan", "ft_moe_group_gemm_mxfp4", "ft_moe_quantize_mxfp4",
+           "ft_moe_quantize_mxfp4_weights", "ft_moe_pack_mxfp4_scales", "ft_moe_swiglu_quantize_mxfp4",
+           "ft_moe_dispatch", "ft_moe_dispatch_backward", "ft_moe_combine", "ft_moe_combine_backward",
+           "ft_moe_rmsnorm", "ft_moe_rmsnorm_workspace_size", "ft_moe_rmsnorm_backward")
+FT_GROUP_FORWARD, FT_GROUP_DGRAD, FT_GROUP_WGRAD, FT_GROUP_FP8, FT_GROUP_MXFP4 = range(5)
 FT_NSTAGES = 6
 STAGES = ("align", "gate_up", "shared_gate_up", "down", "shared_down", "combine")
 
@@ -97,6 +104,7 @@ def load():
             raise ImportError(f"libftmoe.so not built at {LIB_PATH}: run nvfp4_quantized_moe_gb300/build.py")
         L = ctypes.CDLL(LIB_PATH)
         P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        F32 = ctypes.c_float
         sigs = {
             "ft_moe_layout": [P, I32, P],
             "ft_moe_pack": [P, I32, P, P, P],
@@ -123,6 +131,18 @@ def load():
             "ft_moe_swiglu_quantize_fp8": [P, I64, P, I32, I32, P, I64, P, I64, P],
             "ft_moe_debug_group_plan": [I32, I32, I32, I32, I32, I32, I32, P],
             "ft_moe_swiglu_backward": [P, I64, P, P, I64, I32, I32, P, I64, P, P],
+            "ft_moe_group_gemm_mxfp4": [P, I64, P, I64, P, P, P, I32, I32, I32, I32, P, I64, I32, P, SZ, P],
+            "ft_moe_quantize_mxfp4": [P, I32, I64, I32, I32, P, I64, P, I64, P],
+            "ft_moe_quantize_mxfp4_weights": [P, I32, I32, I32, I32, P, P, P],
+            "ft_moe_pack_mxfp4_scales": [P, I32, I32, I32, P, P],
+            "ft_moe_swiglu_quantize_mxfp4": [P, I64, P, I32, I32, P, I64, P, I64, P],
+            "ft_moe_dispatch": [P, I64, I32, I32, I32, P, I32, P, P, I64, P, I64, I32, P, I64, P, P, P, P],
+            "ft_moe_dispatch_backward": [P, I64, I32, P, I32, I32, I32, I32, P, P, I64, I32, P, P],
+            "ft_moe_combine": [P, I64, I32, P, P, I32, I32, I32, I32, P, I64, P, I64, I32, P],
+            "ft_moe_combine_backward": [P, I64, I32, P, I64, I32, P, P, I32, I32, I32, I32, P, I64, P, P],
+            "ft_moe_rmsnorm": [P, I64, P, I64, P, I64, I32, P, I32, F32, F32, I32, I32, P, I64, P, I64, P, I64, P, P],
+            "ft_moe_rmsnorm_workspace_size": [I32, I32, P],
+            "ft_moe_rmsnorm_backward": [P, I64, P, I64, I32, P, I32, F32, P, P, I64, I32, I32, P, I64, P, I32, P, SZ, P],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -267,6 +287,7 @@ def ft_moe_quantize_nvfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.
 # integers.
 _BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 _OUT, _E4M3 = (torch.bfloat16, torch.float32), (torch.uint8, torch.float8_e4m3fn)
+_U8, _E8M0 = (torch.uint8,), (torch.uint8, torch.float8_e8m0fnu)
 _OUT_CODE = {torch.bfloat16: FT_DTYPE_BF16, torch.float32: FT_DTYPE_F32}
 
 
@@ -314,6 +335,9 @@ def _stream_of(stream, dev):
         raise ValueError("expected tensors on the GPU")
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if dev != torch._C._cuda_getDevice():  # (a device's default stream is 0 on every device)
+        raise ValueError(f"the tensors lie on cuda:{dev}, which is not the current device: make it current, or pass a "
+                         "stream of it")
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -432,6 +456,196 @@ def ft_moe_swiglu_backward(gu: torch.Tensor, w, dh: torch.Tensor, dgu: torch.Ten
         gu.data_ptr(), _rows("gu", gu, dev, _BF16, rows, 2 * I), _whole("w", w, dev, _F32, (rows,)), dh.data_ptr(),
         _rows("dh", dh, dev, _BF16, rows, I), rows, I, dgu.data_ptr(), _rows("dgu", dgu, dev, _BF16, rows, 2 * I),
         _whole("dw", dw, dev, _F32, (rows,)), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def _opt_rows(name, t, dev, dtypes, rows, cols):
+    """Address and row stride of a tensor that may be left out."""
+    if t is None:
+        return None, 0
+    return t.data_ptr(), _rows(name, t, dev, dtypes, rows, cols)
+
+
+def alloc_mxfp4_scales(rows: int, K: int, device="cuda") -> torch.Tensor:
+    """Scales uint8 [ceil(K/128), rows, 4] of MXFP4 rows, with the row stride that ft_moe_group_gemm_mxfp4 needs."""
+    return torch.empty(((K + 127) // 128, (rows + 3) // 4 * 4, 4), dtype=torch.uint8, device=device)[:, :rows]
+
+
+def _words(name, t, dev, rows, K):
+    """Address and row stride (in words) of MXFP4 scales [ceil(K/128), rows, 4]."""
+    nb = (K + 127) // 128
+    if t.dtype not in _E8M0 or t.shape != (nb, rows, 4) or t.get_device() != dev:
+        _refuse(name, t, _E8M0, (nb, rows, 4))
+    ld, word, byte = t.stride()
+    if byte != 1 or (word != 4 and rows > 1) or (ld % 4 and nb > 1):
+        raise ValueError(f"{name}: expected words of four bytes, 4 bytes apart in rows a multiple of 4 apart, got strides "
+                         f"{t.stride()}")
+    return t.data_ptr(), ld // 4 if nb > 1 else (rows + 3) // 4 * 4
+
+
+def ft_moe_group_gemm_mxfp4(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, offs,
+                            y: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """ft_moe_group_gemm on MXFP4 operands: codes uint8 x [P, K/2] and w [E, N, K/2]; x_scale uint8
+    [ceil(K/128), P, 4] (see alloc_mxfp4_scales), w_scale uint8 [E, ceil(N/128), ceil(K/128), 512]."""
+    E, N, half = _dims("w", w, 3)
+    P, dev, K = _dims("x", x, 2)[0], x.get_device(), 2 * half
+    status = (_lib or load()).ft_moe_group_gemm_mxfp4(
+        x.data_ptr(), _rows("x", x, dev, _U8, P, half), *_words("x_scale", x_scale, dev, P, K),
+        _whole("w", w, dev, _U8, (E, N, half)),
+        _whole("w_scale", w_scale, dev, _U8, (E, (N + 127) // 128, (K + 127) // 128, 512)), _offsets(offs, dev, E), E, P, N, K,
+        y.data_ptr(), _rows("y", y, dev, _OUT, P, N), _OUT_CODE[y.dtype], *_scratch(workspace, dev), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_quantize_mxfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """MXFP4 codes uint8 [rows, K/2] and scales uint8 [ceil(K/128), rows, 4] of bf16 or fp32 rows."""
+    (rows, K), dev = _dims("src", src, 2), src.get_device()
+    status = (_lib or load()).ft_moe_quantize_mxfp4(
+        src.data_ptr(), _OUT_CODE.get(src.dtype, 0), _rows("src", src, dev, _OUT, rows, K), rows, K, codes.data_ptr(),
+        _rows("codes", codes, dev, _U8, rows, K // 2), *_words("scales", scales, dev, rows, K), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_quantize_mxfp4_weights(src: torch.Tensor, codes: torch.Tensor, tiles: torch.Tensor, stream=None):
+    """MXFP4 codes uint8 [E, N, K/2] and scale tiles uint8 [E, ceil(N/128), ceil(K/128), 512] of bf16 or fp32
+    weights [E, N, K]."""
+    (E, N, K), dev = _dims("src", src, 3), src.get_device()
+    status = (_lib or load()).ft_moe_quantize_mxfp4_weights(
+        _whole("src", src, dev, _OUT, (E, N, K)), _OUT_CODE.get(src.dtype, 0), E, N, K,
+        _whole("codes", codes, dev, _U8, (E, N, K // 2)),
+        _whole("tiles", tiles, dev, _U8, (E, (N + 127) // 128, (K + 127) // 128, 512)), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_pack_mxfp4_scales(src: torch.Tensor, tiles: torch.Tensor, stream=None):
+    """Scale tiles uint8 [E, ceil(N/128), ceil(K/128), 512] of a checkpoint's scale bytes [E, N, K/32]."""
+    (E, N, blocks), dev = _dims("src", src, 3), src.get_device()
+    status = (_lib or load()).ft_moe_pack_mxfp4_scales(
+        _whole("src", src, dev, _E8M0, (E, N, blocks)), E, N, 32 * blocks,
+        _whole("tiles", tiles, dev, _U8, (E, (N + 127) // 128, (blocks + 3) // 4, 512)), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_swiglu_quantize_mxfp4(gu: torch.Tensor, w, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """ft_moe_swiglu stored as MXFP4 codes uint8 [rows, I/2] and scales uint8 [ceil(I/128), rows, 4]."""
+    (rows, half), dev = _dims("codes", codes, 2), gu.get_device()
+    I = 2 * half
+    status = (_lib or load()).ft_moe_swiglu_quantize_mxfp4(
+        gu.data_ptr(), _rows("gu", gu, dev, _BF16, rows, 2 * I), _whole("w", w, dev, _F32, (rows,)), rows, I,
+        codes.data_ptr(), _rows("codes", codes, dev, _U8, rows, half), *_words("scales", scales, dev, rows, I),
+        _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_dispatch(x: torch.Tensor, slot: torch.Tensor, k: int, out: torch.Tensor, x_scale=None, out_scale=None, w=None,
+                    row_w=None, pos=None, count=None, stream=None):
+    """out[p] = x[slot[p] // k] (rows of any type), with block scales ([blocks, T] to [blocks, P], fp32, or
+    [blocks, T, 4] to [blocks, P, 4], uint8), row weights (w fp32 [T, k] to row_w [P]) and pos int32 [T, k], the rows of
+    the slots. count int32 [1]: rows in use."""
+    (T, cols), dev, size = _dims("x", x, 2), x.get_device(), x.element_size()
+    P = _dims("slot", slot, 1)[0]
+    blocks, xs, os_ = 0, (None, 0), (None, 0)
+    if (x_scale is None) != (out_scale is None) or (w is None) != (row_w is None):
+        raise ValueError("x_scale and out_scale, and w and row_w, are given together")
+    if x_scale is not None:
+        blocks = x_scale.shape[0]
+        if x_scale.dim() == 3:
+            xs, os_ = _words("x_scale", x_scale, dev, T, 128 * blocks), _words("out_scale", out_scale, dev, P, 128 * blocks)
+        else:
+            xs = x_scale.data_ptr(), _rows("x_scale", x_scale, dev, _F32, blocks, T)
+            os_ = out_scale.data_ptr(), _rows("out_scale", out_scale, dev, _F32, blocks, P)
+    status = (_lib or load()).ft_moe_dispatch(
+        x.data_ptr(), _rows("x", x, dev, (x.dtype,), T, cols) * size, cols * size, T, k,
+        _whole("slot", slot, dev, _I32, (P,)), P, _whole("count", count, dev, _I32, (1,)), out.data_ptr(),
+        _rows("out", out, dev, (x.dtype,), P, cols) * size, *xs, blocks, *os_, _whole("w", w, dev, _F32, (T, k)),
+        _whole("row_w", row_w, dev, _F32, (P,)), _whole("pos", pos, dev, _I32, (T, k)), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_dispatch_backward(dout: torch.Tensor, pos: torch.Tensor, dx: torch.Tensor, drow_w=None, dw=None, stream=None):
+    """dx[t] = sum of dout[pos[t, j]] over j (bf16 or fp32 each); dw[t, j] = drow_w[pos[t, j]] where given."""
+    (P, H), dev, (T, k) = _dims("dout", dout, 2), dout.get_device(), _dims("pos", pos, 2)
+    if (drow_w is None) != (dw is None):
+        raise ValueError("drow_w and dw are given together")
+    status = (_lib or load()).ft_moe_dispatch_backward(
+        dout.data_ptr(), _rows("dout", dout, dev, _OUT, P, H), _OUT_CODE[dout.dtype], _whole("pos", pos, dev, _I32, (T, k)), T, k,
+        P, H, _whole("drow_w", drow_w, dev, _F32, (P,)), dx.data_ptr(), _rows("dx", dx, dev, _OUT, T, H), _OUT_CODE[dx.dtype],
+        _whole("dw", dw, dev, _F32, (T, k)), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_combine(y: torch.Tensor, pos: torch.Tensor, w, out: torch.Tensor, add=None, stream=None):
+    """out[t] = sum of w[t, j] * y[pos[t, j]] over j, plus add[t] (of out's type, or None); w fp32 [T, k], None for 1."""
+    (P, H), dev, (T, k) = _dims("y", y, 2), y.get_device(), _dims("pos", pos, 2)
+    status = (_lib or load()).ft_moe_combine(
+        y.data_ptr(), _rows("y", y, dev, _OUT, P, H), _OUT_CODE[y.dtype], _whole("pos", pos, dev, _I32, (T, k)),
+        _whole("w", w, dev, _F32, (T, k)), T, k, P, H, *_opt_rows("add", add, dev, (out.dtype,), T, H), out.data_ptr(),
+        _rows("out", out, dev, _OUT, T, H), _OUT_CODE[out.dtype], _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_combine_backward(dout: torch.Tensor, y, pos: torch.Tensor, w, dy: torch.Tensor, dw=None, stream=None):
+    """dy[pos[t, j]] = w[t, j] * dout[t] (bf16) and, where dw is given, dw[t, j] = <dout[t], y[pos[t, j]]>."""
+    (P, H), dev, (T, k) = _dims("dy", dy, 2), dout.get_device(), _dims("pos", pos, 2)
+    if y is None and dw is not None:
+        raise ValueError("dw needs y")
+    status = (_lib or load()).ft_moe_combine_backward(
+        dout.data_ptr(), _rows("dout", dout, dev, _OUT, T, H), _OUT_CODE[dout.dtype], *_opt_rows("y", y, dev, _OUT, P, H),
+        FT_DTYPE_BF16 if y is None else _OUT_CODE[y.dtype], _whole("pos", pos, dev, _I32, (T, k)),
+        _whole("w", w, dev, _F32, (T, k)), T, k, P, H, dy.data_ptr(), _rows("dy", dy, dev, _BF16, P, H),
+        _whole("dw", dw, dev, _F32, (T, k)), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y=None, residual=None, total=None, codes=None,
+                   scales=None, rstd=None, weight_offset: float = 0.0, stream=None):
+    """total = x + residual, y = total / rms(total) * (weight_offset + weight), into y (bf16), into e4m3 codes [rows, H] and
+    scales [ceil(H/128), rows], or both; rstd fp32 [rows] for the backward pass."""
+    (rows, H), dev = _dims("x", x, 2), x.get_device()
+    if (residual is None) != (total is None) or (codes is None) != (scales is None):
+        raise ValueError("residual and total, and codes and scales, are given together")
+    kind = _BF16 if residual is None else (residual.dtype,)
+    status = (_lib or load()).ft_moe_rmsnorm(
+        x.data_ptr(), _rows("x", x, dev, _BF16, rows, H), *_opt_rows("residual", residual, dev, _OUT, rows, H),
+        *_opt_rows("total", total, dev, kind, rows, H), _OUT_CODE[kind[0]], _whole("weight", weight, dev, _OUT, (H,)),
+        _OUT_CODE[weight.dtype], weight_offset, eps, rows, H, *_opt_rows("y", y, dev, _BF16, rows, H),
+        *_opt_rows("codes", codes, dev, _E4M3, rows, H), *_opt_rows("scales", scales, dev, _F32, (H + 127) // 128, rows),
+        _whole("rstd", rstd, dev, _F32, (rows,)), _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
+def ft_moe_rmsnorm_workspace_size(rows: int, H: int) -> int:
+    n = ctypes.c_size_t()
+    status = (_lib or load()).ft_moe_rmsnorm_workspace_size(rows, H, ctypes.byref(n))
+    if status:
+        _check(status)
+    return n.value
+
+
+def ft_moe_rmsnorm_backward(dy: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                            workspace=None, dw=None, dtotal=None, weight_offset: float = 0.0, accumulate: bool = False,
+                            stream=None):
+    """Gradients of ft_moe_rmsnorm: dx (of total's type, for x and the residual; dtotal reaches total past the norm) and,
+    where given, dw fp32 [H] (which needs the workspace; accumulate adds to it)."""
+    (rows, H), dev = _dims("dy", dy, 2), dy.get_device()
+    kind = (total.dtype,)
+    status = (_lib or load()).ft_moe_rmsnorm_backward(
+        dy.data_ptr(), _rows("dy", dy, dev, _BF16, rows, H), total.data_ptr(), _rows("total", total, dev, _OUT, rows, H),
+        _OUT_CODE[total.dtype], _whole("weight", weight, dev, _OUT, (H,)), _OUT_CODE[weight.dtype], weight_offset,
+        _whole("rstd", rstd, dev, _F32, (rows,)), *_opt_rows("dtotal", dtotal, dev, kind, rows, H), rows, H, dx.data_ptr(),
+        _rows("dx", dx, dev, kind, rows, H), _whole("dw", dw, dev, _F32, (H,)), 1 if accumulate else 0,
+        *((None, 0) if workspace is None else _scratch(workspace, dev)), _stream_of(stream, dev))
     if status:
         _check(status)
 

@@ -203,6 +203,35 @@ struct GroupGemm8 {
     int32_t *plan;               // as in GroupGemm
 };
 cudaError_t launch_group_gemm_fp8(const GroupGemm8 &g, cudaStream_t s);
+// A grouped MXFP4 product (group_gemm_mxfp4.cu).
+struct GroupGemm4 {
+    const int *offs;
+    int E, P, N, K;
+    const void *x, *w;           // packed e2m1 codes; ld_x in bytes
+    const uint32_t *xs;          // [ceil(K / 128)][ld_xs] words of four scale bytes
+    const uint8_t *ws;           // [E][ceil(N / 128)][ceil(K / 128)][512]
+    int64_t ld_x, ld_xs, ld_out;
+    void *out;
+    int out_f32;
+    int *status;
+    int32_t *plan;               // as in GroupGemm
+};
+cudaError_t launch_group_gemm_mxfp4(const GroupGemm4 &g, cudaStream_t s);
+// mxfp4_quant.cu. src: rows of K values (SwiGLU: of 2 K), strides in elements; codes: ld_codes in bytes.
+struct Quant4Params {
+    const void *src;
+    int64_t ld_src;
+    const float *w;              // SwiGLU: the rows' weights, or null
+    int rows, K;
+    uint8_t *codes;
+    int64_t ld_codes;
+    uint32_t *scales;            // words [ceil(K / 128)][ld_scales], or tiles
+    int64_t ld_scales;
+    int tile_rows;               // 0, or the rows of each weight matrix, whose scales go in tiles
+};
+cudaError_t launch_quantize_mxfp4(const Quant4Params &p, bool f32, cudaStream_t s);
+cudaError_t launch_swiglu_quantize_mxfp4(const Quant4Params &p, cudaStream_t s);
+cudaError_t launch_pack_mxfp4_scales(const uint8_t *src, int E, int N, int K, uint32_t *tiles, cudaStream_t s);
 // expert_act.cu. Strides in elements; scales are [ceil(columns / 128)][ld_scales].
 cudaError_t launch_quantize_fp8(const void *src, bool f32, int64_t ld, int rows, int K, uint8_t *codes, int64_t ld_codes,
                                 float *scales, int64_t ld_scales, cudaStream_t s);
@@ -212,6 +241,76 @@ cudaError_t launch_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const floa
                                        int64_t ld_codes, float *scales, int64_t ld_scales, cudaStream_t s);
 cudaError_t launch_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, const void *dh, int64_t ld_dh, int rows,
                                    int I, void *dgu, int64_t ld_dgu, float *dw, cudaStream_t s);
+
+// norm.cu. Strides in elements; scales are [ceil(H / 128)][ld_scales].
+struct NormParams {
+    const void *x, *residual, *w;  // residual may be null
+    void *total, *y;               // total: with a residual only; y may be null
+    int64_t ld_x, ld_residual, ld_total, ld_y;
+    uint8_t *codes;                // may be null
+    int64_t ld_codes;
+    float *scales;
+    int64_t ld_scales;
+    float *rstd;                   // may be null
+    float offset, eps;
+    int rows, H;
+    int total_f32, w_f32;
+};
+cudaError_t launch_rmsnorm(const NormParams &p, cudaStream_t s);
+struct NormBackParams {
+    const void *dy, *total, *w, *dtotal;  // dtotal may be null
+    void *dx;
+    int64_t ld_dy, ld_total, ld_dtotal, ld_dx;
+    const float *rstd;
+    float offset;
+    int rows, H;
+    int total_f32, w_f32;
+    float *part;                          // [norm_parts][H], or null
+};
+constexpr int kMaxNormWidth = 16384;
+// Rows of partial sums of the weight's gradient: a function of the sizes alone.
+int norm_parts(int rows, int H);
+cudaError_t launch_rmsnorm_backward(NormBackParams p, float *dw, int accumulate, void *workspace, cudaStream_t s);
+
+// order.cu. Strides of x and out in bytes (dispatch), else in elements.
+struct DispatchParams {
+    const char *x;
+    char *out;
+    int64_t ld_x, ld_out;
+    int row_bytes;
+    int T, k, P;
+    const int *slot, *count;                // count may be null
+    const uint32_t *x_scale;                // [blocks][ld_xs]
+    uint32_t *out_scale;
+    int64_t ld_xs, ld_os;
+    int blocks;                             // 0: no scales
+    const float *w;
+    float *row_w;                           // may be null
+    int *pos;                               // may be null
+    int small, clear;                       // set by the launch
+};
+cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s);
+struct CombineParams {
+    const void *y, *add;                    // add may be null; of out's type
+    void *out;
+    int64_t ld_y, ld_add, ld_out;
+    const int *pos;
+    const float *w;                         // may be null: weights of 1
+    const float *drow_w;
+    float *dw;                              // may be null
+    int T, k, P, H;
+};
+cudaError_t launch_combine_rows(const CombineParams &p, bool y_f32, bool out_f32, cudaStream_t s);
+struct CombineBackParams {
+    const void *dout, *y;
+    void *dy;
+    int64_t ld_dout, ld_y, ld_dy;
+    const int *pos;
+    const float *w;                         // may be null
+    float *dw;                              // may be null
+    int T, k, P, H;
+};
+cudaError_t launch_combine_backward(const CombineBackParams &p, bool dout_f32, bool y_f32, cudaStream_t s);
 
 // While one exists, the fault injection armed on this thread applies to the launches made; its
 // end disarms it. (A call makes one when its arguments are checked: a refused call launches

@@ -1,34 +1,13 @@
 // extern "C" entry points of the grouped expert products and the row kernels around them:
 // argument validation and launches. See include/ft_moe.h for the contract of every call.
 #include <cuda_runtime.h>
-#include <stdarg.h>
-#include <stdio.h>
 
+#include "api_check.h"
 #include "ft_moe.h"
 #include "ftmoe_internal.h"
 
 namespace ftmoe {
 
-static ft_status reject(ft_status code, const char *fmt, ...)
-{
-    char text[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(text, sizeof(text), fmt, ap);
-    va_end(ap);
-    return report_error(code, text);
-}
-
-static ft_status finish(cudaError_t e, const char *what)
-{
-    if (e == cudaSuccess) return report_error(FT_OK, "");
-    return reject(FT_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-static bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-constexpr int kMaxRows = 1 << 25;   // T <= 2^20 tokens of up to 32 slots
-constexpr int kMaxWidth = 1 << 16;
 constexpr size_t kGroupWorkspace = 256;  // the status word
 
 static ft_status check_sizes(int E, int P, int N, int K, int unit_n, int unit_k)
@@ -52,29 +31,6 @@ static ft_status check_group(const int32_t *offs, int E, const void *workspace, 
     if (bytes < kGroupWorkspace) return reject(FT_ERR_WORKSPACE, "workspace needs %zu bytes", kGroupWorkspace);
     return FT_OK;
 }
-
-// A matrix operand: rows `ld` elements apart, 16-byte aligned rows.
-static ft_status check_matrix(const char *name, const void *p, int64_t ld, int cols, int unit)
-{
-    if (!p || !aligned(p, 16)) return reject(FT_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", name);
-    if (ld < cols || ld % unit || ld > (int64_t)1 << 32)
-        return reject(FT_ERR_INVALID_ARG, "the row stride of %s must be a multiple of %d elements, at least %d (got %lld)", name,
-                      unit, cols, (long long)ld);
-    return FT_OK;
-}
-
-static ft_status check_out_dtype(int32_t dtype)
-{
-    if (dtype != FT_DTYPE_BF16 && dtype != FT_DTYPE_F32)
-        return reject(FT_ERR_INVALID_ARG, "the output's dtype must be FT_DTYPE_BF16 or FT_DTYPE_F32");
-    return FT_OK;
-}
-
-#define FT_TRY(...)                       \
-    do {                                  \
-        const ft_status st_ = __VA_ARGS__; \
-        if (st_ != FT_OK) return st_;     \
-    } while (0)
 
 // No rows: nothing to compute, the status word is cleared.
 static ft_status no_rows(void *workspace, cudaStream_t s)
@@ -198,15 +154,47 @@ ft_status ft_moe_group_gemm_fp8(const void *x, int64_t ld_x, const float *x_scal
     return finish(launch_group_gemm_fp8(g, static_cast<cudaStream_t>(stream)), "grouped 8-bit product launch");
 }
 
+ft_status ft_moe_group_gemm_mxfp4(const void *x, int64_t ld_x, const void *x_scale, int64_t ld_xs, const void *w,
+                                  const void *w_scale, const int32_t *offs, int32_t E, int32_t P, int32_t N, int32_t K, void *y,
+                                  int64_t ld_y, int32_t y_dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    FT_NVTX_RANGE("ft_moe_group_gemm_mxfp4");
+    FT_TRY(check_sizes(E, P, N, K, 1, 32));
+    FT_TRY(check_out_dtype(y_dtype));
+    FT_TRY(check_group(offs, E, workspace, workspace_bytes));
+    if (P == 0) return no_rows(workspace, static_cast<cudaStream_t>(stream));
+    FT_TRY(check_matrix("x", x, ld_x, K / 2, 16));
+    FT_TRY(check_matrix("w", w, K / 2, K / 2, 16));
+    FT_TRY(check_matrix("y", y, ld_y, N, 1));
+    FT_TRY(check_matrix("x_scale", x_scale, ld_xs, P, 4));
+    if (!w_scale || !aligned(w_scale, 16))
+        return reject(FT_ERR_INVALID_ARG, "w_scale must be non-NULL and 16-byte aligned");
+    GroupGemm4 g = {};
+    g.offs = offs; g.E = E; g.P = P; g.N = N; g.K = K;
+    g.x = x; g.ld_x = ld_x; g.xs = static_cast<const uint32_t *>(x_scale); g.ld_xs = ld_xs;
+    g.w = w; g.ws = static_cast<const uint8_t *>(w_scale);
+    g.out = y; g.ld_out = ld_y; g.out_f32 = y_dtype == FT_DTYPE_F32;
+    g.status = static_cast<int *>(workspace);
+    const StallScope stall;
+    return finish(launch_group_gemm_mxfp4(g, static_cast<cudaStream_t>(stream)), "grouped 4-bit product launch");
+}
+
 ft_status ft_moe_debug_group_plan(int32_t product, int32_t E, int32_t P, int32_t N, int32_t K, int32_t out_dtype,
                                   int32_t accumulate, int32_t *plan)
 {
-    if (product < FT_GROUP_FORWARD || product > FT_GROUP_FP8 || P < 1 || !plan || accumulate < 0 ||
+    if (product < FT_GROUP_FORWARD || product > FT_GROUP_MXFP4 || P < 1 || !plan || accumulate < 0 ||
         accumulate > (product == FT_GROUP_WGRAD && out_dtype == FT_DTYPE_F32))
         return reject(FT_ERR_INVALID_ARG, "need a product, P >= 1, accumulate for a wgrad into fp32 only, and room for the plan");
-    const bool fp8 = product == FT_GROUP_FP8;
-    FT_TRY(check_sizes(E, P, N, K, fp8 ? 1 : 8, fp8 ? 16 : 8));
+    const bool fp8 = product == FT_GROUP_FP8, mxfp4 = product == FT_GROUP_MXFP4;
+    FT_TRY(check_sizes(E, P, N, K, fp8 || mxfp4 ? 1 : 8, mxfp4 ? 32 : fp8 ? 16 : 8));
     FT_TRY(check_out_dtype(out_dtype));
+    if (mxfp4) {
+        GroupGemm4 g = {};
+        g.E = E; g.P = P; g.N = N; g.K = K;
+        g.out_f32 = out_dtype == FT_DTYPE_F32;
+        g.plan = plan;
+        return finish(launch_group_gemm_mxfp4(g, nullptr), "plan of a grouped 4-bit product");
+    }
     if (fp8) {
         GroupGemm8 g = {};
         g.E = E; g.P = P; g.N = N; g.K = K;
@@ -220,31 +208,6 @@ ft_status ft_moe_debug_group_plan(int32_t product, int32_t E, int32_t P, int32_t
     g.out_f32 = out_dtype == FT_DTYPE_F32; g.accumulate = accumulate;
     g.plan = plan;
     return finish(launch_group_gemm(g, nullptr), "plan of a grouped product");
-}
-
-// Rows and columns of the row kernels.
-static ft_status check_rows(int rows, int cols, int unit)
-{
-    if (rows < 0 || cols <= 0) return reject(FT_ERR_INVALID_ARG, "need rows >= 0 and columns > 0");
-    if (rows > kMaxRows || cols > kMaxWidth || cols % unit)
-        return reject(FT_ERR_UNSUPPORTED, "need rows <= 2^25 and columns <= 65536, a multiple of %d (got %d x %d)", unit, rows,
-                      cols);
-    return FT_OK;
-}
-
-// An operand of the SwiGLU kernels that take any alignment.
-static ft_status check_values(const char *name, const void *p, int64_t ld, int cols)
-{
-    if (!p || !aligned(p, 2) || ld < cols)
-        return reject(FT_ERR_INVALID_ARG, "%s must be non-NULL, 2-byte aligned, with rows of at least %d elements", name, cols);
-    return FT_OK;
-}
-
-static ft_status check_scales(const float *scales, int64_t ld, int rows)
-{
-    if (!scales || !aligned(scales, 4) || ld < rows)
-        return reject(FT_ERR_INVALID_ARG, "scales must be non-NULL, 4-byte aligned, with rows of at least %d elements", rows);
-    return FT_OK;
 }
 
 ft_status ft_moe_quantize_fp8(const void *src, int32_t src_dtype, int64_t ld_src, int32_t rows, int32_t K, uint8_t *codes,
@@ -288,6 +251,66 @@ ft_status ft_moe_swiglu_quantize_fp8(const void *gu, int64_t ld_gu, const float 
     return finish(launch_swiglu_quantize_fp8(gu, ld_gu, w, rows, I, codes, ld_codes, scales, ld_scales,
                                              static_cast<cudaStream_t>(stream)),
                   "8-bit SwiGLU launch");
+}
+
+ft_status ft_moe_quantize_mxfp4(const void *src, int32_t src_dtype, int64_t ld_src, int32_t rows, int32_t K, uint8_t *codes,
+                                int64_t ld_codes, void *scales, int64_t ld_scales, void *stream)
+{
+    FT_NVTX_RANGE("ft_moe_quantize_mxfp4");
+    if (src_dtype != FT_DTYPE_BF16 && src_dtype != FT_DTYPE_F32)
+        return reject(FT_ERR_INVALID_ARG, "src_dtype must be FT_DTYPE_BF16 or FT_DTYPE_F32");
+    FT_TRY(check_rows(rows, K, 32));
+    if (rows == 0) return report_error(FT_OK, "");
+    FT_TRY(check_matrix("src", src, ld_src, K, src_dtype == FT_DTYPE_F32 ? 4 : 8));
+    FT_TRY(check_matrix("codes", codes, ld_codes, K / 2, 16));
+    FT_TRY(check_scales(static_cast<float *>(scales), ld_scales, rows));
+    Quant4Params p = {};
+    p.src = src; p.ld_src = ld_src; p.rows = rows; p.K = K;
+    p.codes = codes; p.ld_codes = ld_codes; p.scales = static_cast<uint32_t *>(scales); p.ld_scales = ld_scales;
+    return finish(launch_quantize_mxfp4(p, src_dtype == FT_DTYPE_F32, static_cast<cudaStream_t>(stream)), "4-bit quantizer launch");
+}
+
+ft_status ft_moe_quantize_mxfp4_weights(const void *src, int32_t src_dtype, int32_t E, int32_t N, int32_t K, uint8_t *codes,
+                                        void *tiles, void *stream)
+{
+    FT_NVTX_RANGE("ft_moe_quantize_mxfp4_weights");
+    if (src_dtype != FT_DTYPE_BF16 && src_dtype != FT_DTYPE_F32)
+        return reject(FT_ERR_INVALID_ARG, "src_dtype must be FT_DTYPE_BF16 or FT_DTYPE_F32");
+    FT_TRY(check_sizes(E, 0, N, K, 1, 32));
+    FT_TRY(check_matrix("src", src, K, K, src_dtype == FT_DTYPE_F32 ? 4 : 8));
+    FT_TRY(check_matrix("codes", codes, K / 2, K / 2, 16));
+    if (!tiles || !aligned(tiles, 16)) return reject(FT_ERR_INVALID_ARG, "tiles must be non-NULL and 16-byte aligned");
+    Quant4Params p = {};
+    p.src = src; p.ld_src = K; p.rows = E * N; p.K = K;
+    p.codes = codes; p.ld_codes = K / 2; p.scales = static_cast<uint32_t *>(tiles); p.tile_rows = N;
+    return finish(launch_quantize_mxfp4(p, src_dtype == FT_DTYPE_F32, static_cast<cudaStream_t>(stream)),
+                  "4-bit weight quantizer launch");
+}
+
+ft_status ft_moe_pack_mxfp4_scales(const uint8_t *src, int32_t E, int32_t N, int32_t K, void *tiles, void *stream)
+{
+    FT_NVTX_RANGE("ft_moe_pack_mxfp4_scales");
+    FT_TRY(check_sizes(E, 0, N, K, 1, 32));
+    if (!src) return reject(FT_ERR_INVALID_ARG, "src is NULL");
+    if (!tiles || !aligned(tiles, 16)) return reject(FT_ERR_INVALID_ARG, "tiles must be non-NULL and 16-byte aligned");
+    return finish(launch_pack_mxfp4_scales(src, E, N, K, static_cast<uint32_t *>(tiles), static_cast<cudaStream_t>(stream)),
+                  "4-bit scale packing launch");
+}
+
+ft_status ft_moe_swiglu_quantize_mxfp4(const void *gu, int64_t ld_gu, const float *w, int32_t rows, int32_t I, uint8_t *codes,
+                                       int64_t ld_codes, void *scales, int64_t ld_scales, void *stream)
+{
+    FT_NVTX_RANGE("ft_moe_swiglu_quantize_mxfp4");
+    FT_TRY(check_rows(rows, I, 32));
+    if (rows == 0) return report_error(FT_OK, "");
+    FT_TRY(check_matrix("gu", gu, ld_gu, 2 * I, 8));
+    FT_TRY(check_matrix("codes", codes, ld_codes, I / 2, 16));
+    FT_TRY(check_scales(static_cast<float *>(scales), ld_scales, rows));
+    if (!aligned(w, 4)) return reject(FT_ERR_INVALID_ARG, "w must be 4-byte aligned");
+    Quant4Params p = {};
+    p.src = gu; p.ld_src = ld_gu; p.w = w; p.rows = rows; p.K = I;
+    p.codes = codes; p.ld_codes = ld_codes; p.scales = static_cast<uint32_t *>(scales); p.ld_scales = ld_scales;
+    return finish(launch_swiglu_quantize_mxfp4(p, static_cast<cudaStream_t>(stream)), "4-bit SwiGLU launch");
 }
 
 ft_status ft_moe_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, const void *dh, int64_t ld_dh, int32_t rows,

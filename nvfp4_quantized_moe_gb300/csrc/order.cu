@@ -1,0 +1,284 @@
+// Tokens sorted by expert and back. Slot s = t k + j is token t's j-th expert; slot[p] is the slot of the sorted row p
+// (ft_moe_align with block = 1) and pos[s] the row of slot s, its inverse:
+//
+//   dispatch            out[p] = x[slot[p] / k], block scales and row weights along, pos
+//   dispatch backward   dx[t] = sum_j dout[pos[t k + j]],   dw[s] = drow_w[pos[s]]
+//   combine             out[t] = add[t] + sum_j w[s] y[pos[s]]
+//   combine backward    dy[pos[s]] = w[s] dout[t],   dw[s] = <dout[t], y[pos[s]]>
+//
+// Bound by memory: k rows are read for one that is written, or the other way round, each once; what repeats (a
+// token's row on its way to k experts) repeats in L2. Sums run over j in order, in fp32, and every output element is
+// written by one thread, so that results do not change from run to run. A row number out of range (a slot that no
+// row holds, a padding row) is skipped or read as zero: no value of slot or pos makes a kernel leave its arrays.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ftmoe_device.cuh"
+#include "ftmoe_internal.h"
+#include "row_ops.cuh"
+
+namespace ftmoe {
+
+using namespace rows;
+
+namespace {
+
+constexpr int kOrderThreads = 256;
+// Up to this many slots one CTA clears and fills pos by itself; above, a memset goes before the launch.
+constexpr int kPosByOneCta = 4096;
+
+__device__ __forceinline__ int rows_of(const DispatchParams &p)
+{
+    return p.count ? min(max(__ldg(p.count), 0), p.P) : p.P;
+}
+
+}  // namespace
+
+// The first `small` CTAs carry what is small (positions, row weights, block scales), the others the rows: a warp
+// takes 32 x kUnits pieces of T (16 bytes, or 2 where rows are not made of 16-byte pieces) of one row at a time.
+template <typename T, int kUnits>
+__global__ void __launch_bounds__(kOrderThreads) dispatch_kernel(const __grid_constant__ DispatchParams p)
+{
+    pdl_enter();
+    const int n = rows_of(p), slots = p.T * p.k;
+    if ((int)blockIdx.x < p.small) {
+        const int threads = p.small * kOrderThreads, me = blockIdx.x * kOrderThreads + threadIdx.x;
+        if (p.pos && p.clear) {  // (one CTA's work: nobody else touches pos)
+            if (blockIdx.x == 0) {
+                for (int i = threadIdx.x; i < slots; i += kOrderThreads) p.pos[i] = -1;
+                __syncthreads();
+                for (int r = threadIdx.x; r < n; r += kOrderThreads) {
+                    const int s = __ldg(p.slot + r);
+                    if (s >= 0 && s < slots) atomicMax(p.pos + s, r);
+                }
+            }
+        } else if (p.pos) {
+            for (int r = me; r < n; r += threads) {
+                const int s = __ldg(p.slot + r);
+                if (s >= 0 && s < slots) atomicMax(p.pos + s, r);
+            }
+        }
+        if (p.row_w)
+            for (int r = me; r < n; r += threads) {
+                const int s = __ldg(p.slot + r);
+                p.row_w[r] = s >= 0 && s < slots ? __ldg(p.w + s) : 0.f;
+            }
+        for (int b = 0; b < p.blocks; ++b)
+            for (int r = me; r < n; r += threads) {
+                const int s = __ldg(p.slot + r);
+                p.out_scale[b * p.ld_os + r] = s >= 0 && s < slots ? __ldg(p.x_scale + b * p.ld_xs + s / p.k) : 0u;
+            }
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int pieces = p.row_bytes / (int)sizeof(T), chunks = (pieces + 32 * kUnits - 1) / (32 * kUnits);
+    const int64_t units = (int64_t)n * chunks;
+    const int64_t step = (int64_t)(gridDim.x - p.small) * (kOrderThreads / 32);
+    for (int64_t u = (int64_t)(blockIdx.x - p.small) * (kOrderThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
+        const int r = (int)(u / chunks), c0 = (int)(u - (int64_t)r * chunks) * 32 * kUnits + lane;
+        const int s = __ldg(p.slot + r);
+        const bool in = s >= 0 && s < slots;
+        const T *from = reinterpret_cast<const T *>(p.x + (in ? s / p.k : 0) * p.ld_x);
+        T *to = reinterpret_cast<T *>(p.out + r * p.ld_out);
+        T v[kUnits];
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            v[i] = T{};
+            if (in && c0 + 32 * i < pieces) v[i] = __ldg(from + c0 + 32 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+            if (c0 + 32 * i < pieces) to[c0 + 32 * i] = v[i];
+    }
+}
+
+// Combine, and the backward of dispatch (no weights): one token per CTA and step, 8 columns per thread (or one
+// where rows are not made of 16-byte pieces), the loads of up to 8 rows in flight together.
+template <bool YF32, bool OF32, bool VEC>
+__global__ void __launch_bounds__(kOrderThreads) combine_rows_kernel(const __grid_constant__ CombineParams p)
+{
+    constexpr int W = VEC ? 8 : 1;
+    pdl_enter();
+    const int64_t t = blockIdx.x;
+    const int *pos = p.pos + t * p.k;
+    const float *w = p.w ? p.w + t * p.k : nullptr;
+    if (p.dw && blockIdx.y == 0 && (int)threadIdx.x < p.k) {
+        const int r = __ldg(pos + threadIdx.x);
+        p.dw[t * p.k + threadIdx.x] = r >= 0 && r < p.P ? __ldg(p.drow_w + r) : 0.f;
+    }
+    const int c = W * (blockIdx.y * kOrderThreads + threadIdx.x);
+    if (c >= p.H) return;
+    float acc[W] = {};
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        float v[8][W], f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f[j] = 0.f;
+            if (j0 + j < p.k) {
+                const int r = __ldg(pos + j0 + j);
+                if (r >= 0 && r < p.P) {
+                    f[j] = w ? __ldg(w + j0 + j) : 1.f;
+                    const char *row = static_cast<const char *>(p.y) + r * p.ld_y * (YF32 ? 4 : 2);
+                    if constexpr (VEC) load8<YF32>(row, c, v[j]);
+                    else v[j][0] = YF32 ? __ldg(reinterpret_cast<const float *>(row) + c)
+                                        : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + c) << 16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) v[j][i] = 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[j][i] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] = fmaf(f[j], v[j][i], acc[i]);
+    }
+    const int size = OF32 ? 4 : 2;
+    char *out = static_cast<char *>(p.out) + t * p.ld_out * size;
+    if (p.add) {
+        const char *add = static_cast<const char *>(p.add) + t * p.ld_add * size;
+        float a[W];
+        if constexpr (VEC) load8<OF32>(add, c, a);
+        else a[0] = OF32 ? __ldg(reinterpret_cast<const float *>(add) + c)
+                         : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(add) + c) << 16);
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] += a[i];
+    }
+    if constexpr (VEC) {
+        if constexpr (OF32) {
+            float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + c);
+            o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + c) = pack8(acc);
+        }
+    } else if constexpr (OF32) {
+        reinterpret_cast<float *>(out)[c] = acc[0];
+    } else {
+        reinterpret_cast<uint16_t *>(out)[c] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
+    }
+}
+
+// One warp per slot (neighbouring warps share a token, whose row then comes from L1).
+template <bool DF32, bool YF32, bool VEC>
+__global__ void __launch_bounds__(kOrderThreads) combine_backward_kernel(const __grid_constant__ CombineBackParams p)
+{
+    constexpr int W = VEC ? 8 : 1, U = VEC ? 4 : 8;
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const int64_t slots = (int64_t)p.T * p.k, step = (int64_t)gridDim.x * (kOrderThreads / 32);
+    for (int64_t s = (int64_t)blockIdx.x * (kOrderThreads / 32) + (threadIdx.x >> 5); s < slots; s += step) {
+        const int r = __ldg(p.pos + s);
+        const bool in = r >= 0 && r < p.P;
+        if (!in) {
+            if (p.dw && lane == 0) p.dw[s] = 0.f;
+            continue;
+        }
+        const float f = p.w ? __ldg(p.w + s) : 1.f;
+        const char *d = static_cast<const char *>(p.dout) + s / p.k * p.ld_dout * (DF32 ? 4 : 2);
+        const char *y = static_cast<const char *>(p.y) + r * p.ld_y * (YF32 ? 4 : 2);
+        uint16_t *o = static_cast<uint16_t *>(p.dy) + r * p.ld_dy;
+        float sum = 0.f;
+        for (int c0 = W * lane; c0 < p.H; c0 += 32 * W * U) {
+            float a[U][W], b[U][W];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int c = c0 + 32 * W * i;
+#pragma unroll
+                for (int j = 0; j < W; ++j) a[i][j] = b[i][j] = 0.f;
+                if (c < p.H) {
+                    if constexpr (VEC) {
+                        load8<DF32>(d, c, a[i]);
+                        if (p.dw) load8<YF32>(y, c, b[i]);
+                    } else {
+                        a[i][0] = DF32 ? __ldg(reinterpret_cast<const float *>(d) + c)
+                                       : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(d) + c) << 16);
+                        if (p.dw)
+                            b[i][0] = YF32 ? __ldg(reinterpret_cast<const float *>(y) + c)
+                                           : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(y) + c) << 16);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int c = c0 + 32 * W * i;
+                if (c >= p.H) continue;
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    sum = fmaf(a[i][j], b[i][j], sum);
+                    a[i][j] *= f;
+                }
+                if constexpr (VEC) *reinterpret_cast<uint4 *>(o + c) = pack8(a[i]);
+                else o[c] = __bfloat16_as_ushort(__float2bfloat16_rn(a[i][0]));
+            }
+        }
+        if (p.dw) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+            if (lane == 0) p.dw[s] = sum;
+        }
+    }
+}
+
+namespace {
+
+bool vec16(const void *p, int64_t row_bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0; }
+
+}  // namespace
+
+cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s)
+{
+    const int slots = p.T * p.k;
+    p.clear = slots <= kPosByOneCta && p.P <= kPosByOneCta;
+    if (p.pos && !p.clear) {
+        const cudaError_t e = cudaMemsetAsync(p.pos, 0xFF, sizeof(int) * (size_t)slots, s);
+        if (e != cudaSuccess) return e;
+    }
+    const int per = kOrderThreads / 32;
+    const bool vec = vec16(p.x, p.ld_x) && vec16(p.out, p.ld_out) && p.row_bytes % 16 == 0;
+    const int piece = vec ? 16 : 2, unit = vec ? 4 : 8;
+    const int chunks = (p.row_bytes / piece + 32 * unit - 1) / (32 * unit);
+    const int64_t want = ((int64_t)p.P * chunks + per - 1) / per, most = (int64_t)sm_count() * 32;
+    p.small = 0;
+    if (p.pos || p.row_w || p.blocks) p.small = p.P <= kPosByOneCta ? 1 + p.P / 1024 : p.P / 1024 < sm_count() ? p.P / 1024 : sm_count();
+    const unsigned grid = (unsigned)(want < most ? want : most) + p.small;
+    if (vec) FT_LAUNCH(dispatch_kernel<uint4, 4>, dim3(grid), dim3(kOrderThreads), 0, s, p);
+    else FT_LAUNCH(dispatch_kernel<uint16_t, 8>, dim3(grid), dim3(kOrderThreads), 0, s, p);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_rows(const CombineParams &p, bool y_f32, bool out_f32, cudaStream_t s)
+{
+    const int ys = y_f32 ? 4 : 2, os = out_f32 ? 4 : 2;
+    const bool vec = p.H % 8 == 0 && vec16(p.y, p.ld_y * ys) && vec16(p.out, p.ld_out * os) && vec16(p.add, p.ld_add * os);
+    const int cols = kOrderThreads * (vec ? 8 : 1);
+    const dim3 grid(p.T, (p.H + cols - 1) / cols);
+    auto kern = y_f32 ? (out_f32 ? (vec ? combine_rows_kernel<true, true, true> : combine_rows_kernel<true, true, false>)
+                                 : (vec ? combine_rows_kernel<true, false, true> : combine_rows_kernel<true, false, false>))
+                      : (out_f32 ? (vec ? combine_rows_kernel<false, true, true> : combine_rows_kernel<false, true, false>)
+                                 : (vec ? combine_rows_kernel<false, false, true> : combine_rows_kernel<false, false, false>));
+    FT_LAUNCH(kern, grid, dim3(kOrderThreads), 0, s, p);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine_backward(const CombineBackParams &p, bool dout_f32, bool y_f32, cudaStream_t s)
+{
+    const int ds = dout_f32 ? 4 : 2, ys = y_f32 ? 4 : 2;
+    const bool vec = p.H % 8 == 0 && vec16(p.dout, p.ld_dout * ds) && vec16(p.dy, p.ld_dy * 2) &&
+                     (!p.dw || vec16(p.y, p.ld_y * ys));
+    const int64_t want = ((int64_t)p.T * p.k + kOrderThreads / 32 - 1) / (kOrderThreads / 32), most = (int64_t)sm_count() * 32;
+    auto kern = dout_f32 ? (y_f32 ? (vec ? combine_backward_kernel<true, true, true> : combine_backward_kernel<true, true, false>)
+                                  : (vec ? combine_backward_kernel<true, false, true> : combine_backward_kernel<true, false, false>))
+                         : (y_f32 ? (vec ? combine_backward_kernel<false, true, true> : combine_backward_kernel<false, true, false>)
+                                  : (vec ? combine_backward_kernel<false, false, true> : combine_backward_kernel<false, false, false>));
+    FT_LAUNCH(kern, dim3((unsigned)(want < most ? want : most)), dim3(kOrderThreads), 0, s, p);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace ftmoe
