@@ -154,9 +154,11 @@ cudaError_t launch_quant_nvfp4(const void *src, bool f32_src, int K, const int *
                                uint8_t *scales, float *glob, cudaStream_t s, int *status);
 
 // 2D tiled tensor map (rows of `row_bytes` bytes, `inner` elements used per row) through
-// the driver's cuTensorMapEncodeTiled; false when the driver refuses the shape.
+// the driver's cuTensorMapEncodeTiled; false when the driver refuses the shape. A box takes box_rows rows, row_step
+// apart (at most 8, with box_rows * row_step <= 256).
 bool make_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
-                        uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz);
+                        uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz,
+                        uint32_t row_step = 1);
 
 // The same for a stack of `mats` matrices mat_bytes apart (boxes lie inside one matrix; what a box
 // reaches beyond its matrix reads as zero). Lines come into L2 in pairs: a 128-byte wide box walks

@@ -308,7 +308,9 @@ struct Tile {
 
 // Offsets of the experts (clamped into [0, P], never decreasing inside an expert) and the
 // running count of their tiles, in shared memory: [E + 1] ints each. Run by all threads.
-// Returns whether the offsets were valid. `sh_flag` is one int of shared memory.
+// Returns whether the offsets were valid. `sh_flag` is one int of shared memory. ALIGN: tiles begin at multiples of it
+// (find_aligned_tile).
+template <int ALIGN = 1>
 __device__ __forceinline__ bool build_table(const int *offs, int E, int P, int BN, int *sh_offs, int *sh_tiles, int *sh_flag)
 {
     if (threadIdx.x == 0) *sh_flag = 0;
@@ -325,7 +327,9 @@ __device__ __forceinline__ bool build_table(const int *offs, int E, int P, int B
         int base = 0;
         for (int i0 = 0; i0 < E; i0 += 32) {
             const int i = i0 + threadIdx.x;
-            int t = i < E ? (max(sh_offs[i + 1] - sh_offs[i], 0) + BN - 1) / BN : 0;
+            int t = 0;
+            if (i < E && sh_offs[i + 1] > sh_offs[i])
+                t = (sh_offs[i + 1] - (ALIGN > 1 ? sh_offs[i] / ALIGN * ALIGN : sh_offs[i]) + BN - 1) / BN;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
@@ -354,6 +358,29 @@ __device__ __forceinline__ Tile find_tile(int t, int E, int BN, int gran, const 
     r.e = lo;
     r.row0 = sh_offs[lo] + j * len;
     r.rows = max(min(len, n - j * len), 0);
+    return r;
+}
+
+// The same where the first tile of an expert begins at the multiple of ALIGN at or before its first row and the
+// others BN rows apart: row0 may lie before the expert's rows [first, first + n), which `lo` and `hi` give relative to it.
+struct AlignedTile {
+    int e, row0, lo, hi;
+};
+
+template <int ALIGN>
+__device__ __forceinline__ AlignedTile find_aligned_tile(int t, int E, int BN, const int *sh_offs, const int *sh_tiles)
+{
+    int lo = 0, hi = E;  // sh_tiles[lo] <= t < sh_tiles[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh_tiles[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    AlignedTile r;
+    r.e = lo;
+    r.row0 = sh_offs[lo] / ALIGN * ALIGN + (t - sh_tiles[lo]) * BN;
+    r.lo = max(sh_offs[lo] - r.row0, 0);
+    r.hi = min(sh_offs[lo + 1] - r.row0, BN);
     return r;
 }
 

@@ -12,6 +12,8 @@
 // order with the MMAs that follow it.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "group_gemm.cuh"
 
 namespace ftmoe {
@@ -50,6 +52,7 @@ struct Group4Params {
     int64_t ld;
     int split;            // CTAs (one cluster) that share a unit's contraction
     int pairs;            // bf16 out: N even and rows 4-byte aligned
+    int vec;              // N and the rows of out are multiples of 16 bytes
     int *status;
     uint64_t wait_ns;
     int skip_producer;
@@ -376,6 +379,291 @@ __global__ void __launch_bounds__(kThreads4, 1)
     if (warp == 1) tmem_dealloc<1>(tmem, T::tmem);
 }
 
+// ---------------------------------------------------------------- many rows per expert
+//
+// The rows along the M axis (thread = lane = row) and the weight rows along N, by pairs of CTAs: 256 rows x 192
+// columns, each CTA its own 128 rows and half of the shared weight tile (both CTAs' scales of the weights are whole).
+// Everything comes by TMA, the scales too, so that no warp stands between memory and the tensor cores. For that
+// the rows' scale words must lie in shared memory in tensor memory's order as they come: lane r of 32 takes four
+// neighbouring words, of rows 4 r .. 4 r + 3, for the MMA's rows r, 32 + r, 64 + r and 96 + r. So row 4 r + j of the tile is
+// the MMA's row 32 j + r: the codes are fetched in four boxes of every fourth row (the tensor map's row step), and a
+// tile begins at a multiple of four rows, at most three before its expert's first one (neither those nor the rows behind
+// the expert's last are stored). Tensor memory holds two accumulators of 192 columns and two stages' scales; 256
+// columns would fill it with the accumulators alone.
+
+namespace {
+
+struct RingP {
+    static constexpr int BN = 192, half = BN / 2;
+    static constexpr int b_bytes = half * kChunkBytes;
+    static constexpr int a_sf = 2 * kTileBytes, b_sf = 4 * kTileBytes;  // [steps of 128], [tile][steps of 128]
+    static constexpr int stage = kABytes + b_bytes + a_sf + b_sf;
+    static constexpr int stages = 6;
+    static constexpr int groups = BN / 64;           // epilogue: four warps for each 64 columns
+    static constexpr int warps = 4 * groups;
+    static constexpr int threads = 128 + 32 * warps;
+    static constexpr int out = warps * 16 * 128;     // 16 rows x 128 bytes per warp, on their way out
+    static constexpr int sf_col = 2 * BN, sf_cols = 24;
+    static_assert(stage % 1024 == 0 && sf_col + 2 * sf_cols <= 512, "layout");
+};
+
+}  // namespace
+
+template <bool F32>
+__global__ void __launch_bounds__(RingP::threads, 1)
+    group_gemm_mxfp4_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                                 const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs,
+                                 const __grid_constant__ Group4Params p)
+{
+    using T = RingP;
+    constexpr int S = T::stages, BN = T::BN;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char *sh_out = smem + S * T::stage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sh_out + T::out);
+    uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
+    int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 2 * T::warps);  // the epilogue warps of both CTAs
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tc::prefetch_map(&map_w);
+        tc::prefetch_map(&map_x);
+        tc::prefetch_map(&map_ws);
+        tc::prefetch_map(&map_xs);
+    }
+    if (warp == 1) tmem_alloc<2>(tmem_slot, 512);
+    pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
+    const bool valid = build_table<4>(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles, sh_flag);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
+    tc::fence_before_sync();
+    cluster_sync();
+    tc::fence_after_sync();
+    const uint32_t tmem = uniform(*tmem_slot);
+
+    const int n_tiles = (p.N + BN - 1) / BN;
+    const int units = uniform(sh_tiles[p.E]) * n_tiles;
+    const int nb = (p.K + kStep4 - 1) / kStep4, kt = (p.K + 127) / 128, nt128 = (p.N + 127) / 128;
+    const int u0 = blockIdx.x / 2, du = gridDim.x / 2;
+    struct UnitP {
+        int e, row0, lo, hi;  // rows [row0 + lo, row0 + hi) are the expert's
+        int n0, half;         // first weight row, and how many of them each CTA loads for the MMA (in steps of 16)
+    };
+    auto unit_of = [&](int u) {
+        const int t = u / n_tiles;
+        const AlignedTile x = find_aligned_tile<4>(t, p.E, 2 * kTileM, sh_offs, sh_tiles);
+        UnitP r;
+        r.e = uniform(x.e);
+        r.row0 = uniform(x.row0);
+        r.lo = uniform(x.lo);
+        r.hi = uniform(x.hi);
+        r.n0 = uniform((u - t * n_tiles) * BN);
+        r.half = uniform((min(p.N - r.n0, BN) + 31) / 32 * 16);
+        return r;
+    };
+    bool dead = false;
+
+    if (warp < 4) {
+        if (warp == 0 && !p.skip_producer) {
+            // -------------------------------------------------------- producer
+            const bool one = elect_one();
+            int s = 0, it = 0;
+            uint32_t ph = 1;
+            for (int u = u0; u < units && !dead; u += du) {
+                const UnitP x = unit_of(u);
+                const bool rows[2] = {x.hi > 0, x.hi > kTileM};         // whether a CTA has rows
+                const int t0 = x.n0 / 128, tiles = min(nt128 - t0, 2);  // tiles of the weights' scales
+                const uint32_t each = T::b_bytes + tiles * 2 * kTileBytes;
+                const uint32_t bytes = 2 * each + ((int)rows[0] + (int)rows[1]) * (kABytes + T::a_sf);
+                const int64_t ws_row = ((int64_t)x.e * nt128 + t0) * kt;
+                for (int b = 0; b < nb; ++b, ++it) {
+                    if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
+                    unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes, *sf = sb + T::b_bytes;
+                    const uint32_t bar = map_rank(full + s, 0);
+                    if (one) {
+                        if (leader) mbar_arrive_expect_tx(full + s, bytes);
+                        load_3d<2>(sb, &map_w, b * kChunkBytes, x.n0 + (int)rank * x.half, x.e, bar);
+                        for (int i = 0; i < tiles; ++i)
+                            load_2d<2>(sf + T::a_sf + i * 2 * kTileBytes, &map_ws, 0, (int)(ws_row + i * kt) + 2 * b, bar);
+                        if (rows[rank]) {
+                            const int row = x.row0 + (int)rank * kTileM;
+                            for (int j = 0; j < 4; ++j) load_2d<2>(sa + j * 32 * kChunkBytes, &map_x, b * kChunkBytes, row + j, bar);
+                            load_2d<2>(sf, &map_xs, row, 2 * b, bar);
+                        }
+                    }
+                    __syncwarp();
+                    if (++s == S) { s = 0; ph ^= 1; }
+                }
+            }
+            // The last stages' MMAs also arrive in the other CTA: neither leaves before all have.
+            for (int i = 0; i < S && !dead; ++i) {
+                if (!warp_wait(empty + s, ph, abort_flag, wl)) dead = true;
+                if (++s == S) { s = 0; ph ^= 1; }
+            }
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+            if (dead && leader)  // every issued copy lands before the exit
+                for (int i = 0; i < S && i < it; ++i) {
+                    const int last = it - 1 - i;
+                    mbar_wait_timed(full + last % S, (last / S) & 1, nullptr, wl);
+                }
+        } else if (warp == 1 && leader) {
+            // -------------------------------------------------------- MMA issuer
+            const bool one = elect_one();
+            int s = 0, ac = 0, it = 0;
+            uint32_t ph = 0;
+            for (int u = u0; u < units && !dead; u += du) {
+                const UnitP x = unit_of(u);
+                const uint32_t idesc[2] = {idesc_mxf4(2 * kTileM, 2 * x.half, 0), idesc_mxf4(2 * kTileM, 2 * x.half, 1)};
+                const bool two = nt128 - x.n0 / 128 > 1;
+                const uint32_t col0 = x.n0 % 128 / 32;  // of the unit's first weight row in its tile's scales
+                for (int b = 0; b < nb; ++b, ++it) {
+                    const int in_part = F32 ? b % kPart4 : b;
+                    const bool first = in_part == 0, last = b + 1 == nb || (F32 && in_part == kPart4 - 1);
+                    if ((first && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) ||
+                        !warp_wait(full + s, ph, abort_flag, wl)) {
+                        dead = true;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t sa = smem_u32(smem + s * T::stage);
+                    const uint64_t ad = tc::sw128_desc(sa), bd = tc::sw128_desc(sa + kABytes);
+                    const uint64_t xs = scale_desc(sa + kABytes + T::b_bytes), ws = xs + T::a_sf / 16;
+                    const uint32_t d = tmem + (uint32_t)(ac & 1) * BN, sf = tmem + T::sf_col + (it & 1) * T::sf_cols;
+                    const int steps = min((p.K - b * kStep4 + 63) / 64, 4);  // instructions that have something to multiply
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (2 * k < steps) {  // columns: four of the rows' scales, eight of the weights'
+                                copy_scales<2>(sf + 12 * k, xs + k * (kTileBytes / 16));
+                                copy_scales<2>(sf + 12 * k + 4, ws + k * (kTileBytes / 16));
+                                if (two) copy_scales<2>(sf + 12 * k + 8, ws + (2 + k) * (kTileBytes / 16));
+                            }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < steps)
+                                mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + 4 + col0,
+                                            !first || j != 0);
+                        commit<2>(empty + s);
+                        if (last) commit<2>(acc_full + (ac & 1));
+                    }
+                    __syncwarp();
+                    if (last) ++ac;
+                    if (++s == S) { s = 0; ph ^= 1; }
+                }
+            }
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        // the warp takes 64 columns of the rows 4 l + q (lane l of its quarter q)
+        const int q = warp & 3, g = (warp - 4) >> 2;
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + 64 * g;
+        const uint32_t empty_bar = map_rank(acc_empty, 0);
+        unsigned char *tile = sh_out + (warp - 4) * 16 * 128;
+        const int parts = F32 ? (nb + kPart4 - 1) / kPart4 : 1;
+        int ac = 0;
+        for (int u = u0; u < units && !dead; u += du) {
+            const UnitP x = unit_of(u);
+            float sum[64];
+            for (int t = 0; t < parts; ++t, ++ac) {
+                if (!warp_wait(acc_full + (ac & 1), (ac >> 1) & 1, abort_flag, wl)) { dead = true; break; }
+                tc::fence_after_sync();
+                const uint32_t addr = lane_addr + (uint32_t)(ac & 1) * BN;
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t v[32];
+                    tc::ld32(addr + c, v);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[c + i] = F32 && t ? sum[c + i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive_cluster_relaxed(empty_bar + 8 * (ac & 1));
+            }
+            if (dead) break;
+            // 128 bytes of each row at a time through shared memory (16-byte pieces swizzled by the row, free of bank
+            // conflicts), so that a store instruction writes whole lines of four rows; rows that are not made of
+            // 16-byte pieces leave a row at a time, an element a lane
+            constexpr int per = F32 ? 32 : 64;
+            const int n0 = x.n0 + 64 * g, mine = min(max(p.N - n0, 0), 64);
+            const int first = (int)rank * kTileM + q;  // of the warp's rows, four apart
+            const int64_t at = (int64_t)x.row0 * p.ld + n0;
+            const int l8 = lane & 7, r4 = lane >> 3;
+#pragma unroll
+            for (int c = 0; c < 64; c += per) {
+                if (c >= mine) break;
+                uint4 o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (F32) {
+                        const float *f = sum + c + 4 * i;
+                        o[i] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+                    } else {
+                        const float *f = sum + 8 * i;
+                        o[i] = make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+                    }
+                }
+                const int col = c + l8 * (per / 8);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+                    __syncwarp();
+                    if (lane >> 4 == h) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(tile + (lane & 15) * 128 + ((i ^ l8) << 4)) = o[i];
+                    }
+                    __syncwarp();
+                    if (p.vec) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 4 * i + r4, row = first + 4 * (16 * h + r);
+                            const uint4 w = *reinterpret_cast<const uint4 *>(tile + r * 128 + ((l8 ^ (r & 7)) << 4));
+                            if (row >= x.lo && row < x.hi && col < mine)
+                                *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + (at + row * p.ld + col) * (F32 ? 4 : 2)) = w;
+                        }
+                    } else {
+                        using O = std::conditional_t<F32, uint32_t, uint16_t>;
+                        constexpr int each = 16 / (int)sizeof(O);
+#pragma unroll 4
+                        for (int r = 0; r < 16; ++r) {
+                            const int row = first + 4 * (16 * h + r);
+#pragma unroll
+                            for (int i = lane; i < per; i += 32)
+                                if (row >= x.lo && row < x.hi && c + i < mine)
+                                    static_cast<O *>(p.out)[at + row * p.ld + c + i] =
+                                        reinterpret_cast<const O *>(tile + r * 128 + (((i / each) ^ (r & 7)) << 4))[i % each];
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+    }
+
+    // wind down; a cluster leaves together
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tc::fence_after_sync();
+    if (warp == 1) tmem_dealloc<2>(tmem, 512);
+}
+
 namespace {
 
 template <int BN, bool F32>
@@ -409,6 +697,28 @@ cudaError_t launch4(const CUtensorMap &w, const CUtensorMap &x, Group4Params &p,
     return cudaGetLastError();
 }
 
+template <bool F32>
+cudaError_t launch_wide4(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &ws, const CUtensorMap &xs,
+                         const Group4Params &p, cudaStream_t s)
+{
+    using T = RingP;
+    auto kern = group_gemm_mxfp4_wide_kernel<F32>;
+    constexpr size_t fixed = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 4) + 16;
+    constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
+    static_assert(most <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e != cudaSuccess) return e;
+    const int64_t units = (int64_t)((p.N + T::BN - 1) / T::BN) * (p.P / (2 * kTileM) + 2 * (p.E < p.P ? p.E : p.P));  // at most
+    static ClusterLimit clusters;
+    int64_t grid = clusters.get(kern, 2, T::threads, most);
+    if (units < grid) grid = units;
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), fixed + table_bytes(p.E), 2, s, w, x, ws,
+                                          xs, p);
+    if (le != cudaSuccess) return le;
+    count_launches(1);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_group_gemm_mxfp4(const GroupGemm4 &g, cudaStream_t s)
@@ -425,20 +735,35 @@ cudaError_t launch_group_gemm_mxfp4(const GroupGemm4 &g, cudaStream_t s)
     p.out = g.out;
     p.ld = g.ld_out;
     p.pairs = g.N % 2 == 0 && g.ld_out % 2 == 0;
+    p.vec = g.N % (g.out_f32 ? 4 : 8) == 0 && g.ld_out % (g.out_f32 ? 4 : 8) == 0;
     p.status = g.status;
     injected_stall(&p.wait_ns, &p.skip_producer);
     const int64_t per = g.P / (g.E < g.P ? g.E : g.P);
-    const int bn = per <= 24 ? 32 : 128;
-    CUtensorMap w, x;
-    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const uint64_t bytes = g.K / 2;
+    const int64_t pairs = (int64_t)(g.N + RingP::BN - 1) / RingP::BN * (g.P / 256 + (g.E < g.P ? g.E : g.P));
+    const int bn = per <= 24 ? 32 : per < 128 || g.N <= kTileM || 4 * pairs < sm_count() ? 128 : 256;
+    if (g.plan && bn == 256) {
+        write_plan(g.plan, 2, bn, 1, false);
+        return cudaSuccess;
+    }
+    CUtensorMap w, x, ws, xs;
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
+    const uint64_t bytes = g.K / 2, kt = (g.K + 127) / 128, nt = (g.N + 127) / 128;
+    bool ok = true;
     if (g.plan) {  // nothing to read
-    } else if (!make_tensor_map_3d(&w, u8, g.w, bytes, g.N, g.E, bytes, bytes * g.N, kChunkBytes, kTileM, CU_TENSOR_MAP_SWIZZLE_128B) ||
-               !make_tensor_map_2d(&x, u8, g.x, bytes, g.P, g.ld_x, kChunkBytes, bn == 32 ? Ring4<32>::box_rows : Ring4<128>::box_rows,
-                                   CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
+    } else if (bn == 256) {
+        ok = make_tensor_map_3d(&w, u8, g.w, bytes, g.N, g.E, bytes, bytes * g.N, kChunkBytes, RingP::half, sw) &&
+             make_tensor_map_2d(&x, u8, g.x, bytes, g.P, g.ld_x, kChunkBytes, 32, sw, 4) &&
+             make_tensor_map_2d(&ws, u32, g.ws, 128, g.E * nt * kt, kTileBytes, 128, 2, none) &&
+             make_tensor_map_2d(&xs, u32, g.xs, g.P, kt, 4 * g.ld_xs, 128, 2, none);
+    } else {
+        ok = make_tensor_map_3d(&w, u8, g.w, bytes, g.N, g.E, bytes, bytes * g.N, kChunkBytes, kTileM, sw) &&
+             make_tensor_map_2d(&x, u8, g.x, bytes, g.P, g.ld_x, kChunkBytes, bn == 32 ? Ring4<32>::box_rows : Ring4<128>::box_rows, sw);
+    }
+    if (!ok) return cudaErrorInvalidValue;
     if (bn == 32) return g.out_f32 ? launch4<32, true>(w, x, p, g.plan, s) : launch4<32, false>(w, x, p, g.plan, s);
-    return g.out_f32 ? launch4<128, true>(w, x, p, g.plan, s) : launch4<128, false>(w, x, p, g.plan, s);
+    if (bn == 128) return g.out_f32 ? launch4<128, true>(w, x, p, g.plan, s) : launch4<128, false>(w, x, p, g.plan, s);
+    return g.out_f32 ? launch_wide4<true>(w, x, ws, xs, p, s) : launch_wide4<false>(w, x, ws, xs, p, s);
 }
 
 }  // namespace ftmoe

@@ -23,7 +23,7 @@ using namespace rows;
 namespace {
 
 // Sum over the TPR threads of a row, the same in all of them and from run to run. `red` holds one float per warp
-// of the CTA; rows of one warp need none.
+// of the CTA; rows of one warp need none. (Sums in turn take two `red` by turns: then one barrier each is enough.)
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *red)
 {
@@ -31,7 +31,6 @@ __device__ __forceinline__ float row_sum(float v, float *red)
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     if constexpr (TPR > 32) {
         constexpr int kWarps = TPR / 32;
-        __syncthreads();  // (the sum before has been read)
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
         const int first = threadIdx.x / TPR * kWarps;
@@ -162,62 +161,118 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_kernel(const __grid_
     }
 }
 
+// 8 values as they lie in memory.
+template <bool F32>
+struct Raw8 {
+    uint4 q[F32 ? 2 : 1];
+};
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void fetch8(const void *row, int c, int H, Raw8<F32> &r)
+{
+    if constexpr (VEC) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + c * (F32 ? 4 : 2));
+        r.q[0] = ldg_nc_v4(p);
+        if constexpr (F32) r.q[1] = ldg_nc_v4(p + 1);
+    } else {
+        float v[8];
+        get8<F32, false>(row, c, H, v);
+        if constexpr (F32) {
+            r.q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            r.q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+        } else {
+            r.q[0] = pack8(v);  // (exact: the values are bf16)
+        }
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void open8(const Raw8<F32> &r, float (&v)[8])
+{
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(r.q[i].x);
+            v[4 * i + 1] = __uint_as_float(r.q[i].y);
+            v[4 * i + 2] = __uint_as_float(r.q[i].z);
+            v[4 * i + 3] = __uint_as_float(r.q[i].w);
+        }
+    } else {
+        unpack8(r.q[0], v);
+    }
+}
+
 // Gradient. A CTA takes every gridDim-th group of rows, and its threads always the same columns, so that the
 // weight's gradient adds up in registers; the CTAs' sums go to the workspace [gridDim][H] and
-// norm_weight_kernel adds them in order.
+// norm_weight_kernel adds them in order. The next rows' loads are in flight while these are worked on.
 template <int TPR, int NV, bool F32, bool VEC>
 __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_backward_kernel(const __grid_constant__ NormBackParams p)
 {
     constexpr int kRows = cta_threads(TPR) / TPR;
     extern __shared__ float sh_sum[];  // [kRows - 1][H] where several rows share a CTA
-    __shared__ float red[32];
+    __shared__ float red[2][32];
     pdl_enter();
     const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
     const int H = p.H;
     float acc[NV][8] = {};
-    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < p.rows; row0 += (int64_t)gridDim.x * kRows) {
-        const int64_t row = row0 + team;
-        const bool live = row < p.rows;
+    Raw8<F32> total[NV] = {}, past[NV] = {};
+    Raw8<false> dy[NV] = {};
+    float rstd = 0.f;
+    auto fetch = [&](int64_t row) {
+        if (row >= p.rows) return;
         const char *sr = static_cast<const char *>(p.total) + row * p.ld_total * (F32 ? 4 : 2);
         const char *pr = static_cast<const char *>(p.dtotal) + row * p.ld_dtotal * (F32 ? 4 : 2);
-        char *out = static_cast<char *>(p.dx) + row * p.ld_dx * (F32 ? 4 : 2);
         const uint16_t *dr = static_cast<const uint16_t *>(p.dy) + row * p.ld_dy;
-        const float rstd = live ? __ldg(p.rstd + row) : 0.f;
-        float n[NV][8], g[NV][8], past[NV][8];
+        rstd = __ldg(p.rstd + row);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = 8 * (t + i * TPR);
+            if (c < H) {
+                fetch8<F32, VEC>(sr, c, H, total[i]);
+                fetch8<false, VEC>(dr, c, H, dy[i]);
+                if (p.dtotal) fetch8<F32, VEC>(pr, c, H, past[i]);
+            }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    fetch((int64_t)blockIdx.x * kRows + team);
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < p.rows; row0 += step, turn ^= 1) {
+        const int64_t row = row0 + team;
+        const bool live = row < p.rows;
+        char *out = static_cast<char *>(p.dx) + row * p.ld_dx * (F32 ? 4 : 2);
+        float n[NV][8], g[NV][8];
+        Raw8<F32> ds[NV];
+        const float r = rstd;
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = 8 * (t + i * TPR);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) n[i][j] = g[i][j] = past[i][j] = 0.f;
-            if (live && c < H) {
-                get8<F32, VEC>(sr, c, H, n[i]);
-                get8<false, VEC>(dr, c, H, g[i]);
-                if (p.dtotal) get8<F32, VEC>(pr, c, H, past[i]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (t + i * TPR);
+            open8(total[i], n[i]);
+            open8(dy[i], g[i]);
+            ds[i] = past[i];
             if (live && c < H) {
                 float w[8];
                 gain8<VEC>(p.w, p.w_f32, p.offset, c, H, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    n[i][j] *= rstd;
+                    n[i][j] *= r;
                     acc[i][j] = fmaf(g[i][j], n[i][j], acc[i][j]);
                     g[i][j] *= w[j];
                     dot = fmaf(g[i][j], n[i][j], dot);
                 }
             }
         }
-        const float mean = __fdiv_rn(row_sum<TPR>(dot, red), (float)H);
+        fetch(row + step);
+        const float mean = __fdiv_rn(row_sum<TPR>(dot, red[turn]), (float)H);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = 8 * (t + i * TPR);
             if (live && c < H) {
+                float d[8];
+                open8(ds[i], d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) n[i][j] = fmaf(rstd, fmaf(-n[i][j], mean, g[i][j]), past[i][j]);
+                for (int j = 0; j < 8; ++j) n[i][j] = fmaf(r, fmaf(-n[i][j], mean, g[i][j]), d[j]);
                 put8<F32, VEC>(out, c, H, n[i]);
             }
         }

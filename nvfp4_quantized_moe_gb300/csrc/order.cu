@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kOrderThreads = 256;
 // Up to this many slots one CTA clears and fills pos by itself; above, a memset goes before the launch.
-constexpr int kPosByOneCta = 4096;
+constexpr int kPosByOneCta = 2048;
 
 __device__ __forceinline__ int rows_of(const DispatchParams &p)
 {
@@ -42,32 +42,27 @@ __global__ void __launch_bounds__(kOrderThreads) dispatch_kernel(const __grid_co
     pdl_enter();
     const int n = rows_of(p), slots = p.T * p.k;
     if ((int)blockIdx.x < p.small) {
-        const int threads = p.small * kOrderThreads, me = blockIdx.x * kOrderThreads + threadIdx.x;
-        if (p.pos && p.clear) {  // (one CTA's work: nobody else touches pos)
-            if (blockIdx.x == 0) {
-                for (int i = threadIdx.x; i < slots; i += kOrderThreads) p.pos[i] = -1;
-                __syncthreads();
-                for (int r = threadIdx.x; r < n; r += kOrderThreads) {
-                    const int s = __ldg(p.slot + r);
-                    if (s >= 0 && s < slots) atomicMax(p.pos + s, r);
-                }
-            }
-        } else if (p.pos) {
-            for (int r = me; r < n; r += threads) {
-                const int s = __ldg(p.slot + r);
-                if (s >= 0 && s < slots) atomicMax(p.pos + s, r);
-            }
+        // positions: cleared and filled by the first CTA alone, or, cleared before the launch, by all
+        const int me = blockIdx.x * kOrderThreads + threadIdx.x, threads = p.small * kOrderThreads;
+        if (p.pos && p.clear && blockIdx.x == 0) {
+            for (int i = threadIdx.x; i < slots; i += kOrderThreads) p.pos[i] = -1;
+            __syncthreads();
         }
-        if (p.row_w)
-            for (int r = me; r < n; r += threads) {
+        const bool alone = p.clear;
+        if ((p.pos || p.row_w) && (!alone || blockIdx.x == 0))
+            for (int r = alone ? threadIdx.x : me; r < n; r += alone ? kOrderThreads : threads) {
                 const int s = __ldg(p.slot + r);
-                p.row_w[r] = s >= 0 && s < slots ? __ldg(p.w + s) : 0.f;
+                const bool in = s >= 0 && s < slots;
+                if (p.pos && in) atomicMax(p.pos + s, r);
+                if (p.row_w) p.row_w[r] = in ? __ldg(p.w + s) : 0.f;
             }
-        for (int b = 0; b < p.blocks; ++b)
-            for (int r = me; r < n; r += threads) {
-                const int s = __ldg(p.slot + r);
-                p.out_scale[b * p.ld_os + r] = s >= 0 && s < slots ? __ldg(p.x_scale + b * p.ld_xs + s / p.k) : 0u;
-            }
+        // block scales: a thread per scale, those of a block of columns side by side
+        for (int64_t i = me; i < (int64_t)p.blocks * p.P; i += threads) {
+            const int b = (int)(i / p.P), r = (int)(i - (int64_t)b * p.P);
+            if (r >= n) continue;
+            const int s = __ldg(p.slot + r);
+            p.out_scale[b * p.ld_os + r] = s >= 0 && s < slots ? __ldg(p.x_scale + b * p.ld_xs + s / p.k) : 0u;
+        }
         return;
     }
     const int lane = threadIdx.x & 31;
@@ -162,6 +157,40 @@ __global__ void __launch_bounds__(kOrderThreads) combine_rows_kernel(const __gri
     }
 }
 
+// 8 values of a row (or one) as they lie in memory.
+template <bool F32, bool VEC>
+struct Raw {
+    uint4 q[F32 && VEC ? 2 : 1];
+    __device__ __forceinline__ void load(const char *row, int c)
+    {
+        if constexpr (VEC) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(row + c * (F32 ? 4 : 2));
+            q[0] = __ldg(p);
+            if constexpr (F32) q[1] = __ldg(p + 1);
+        } else if constexpr (F32) {
+            q[0].x = __ldg(reinterpret_cast<const uint32_t *>(row) + c);
+        } else {
+            q[0].x = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + c) << 16;
+        }
+    }
+    __device__ __forceinline__ void open(float (&v)[VEC ? 8 : 1]) const
+    {
+        if constexpr (!VEC) {
+            v[0] = __uint_as_float(q[0].x);
+        } else if constexpr (F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(q[i].x);
+                v[4 * i + 1] = __uint_as_float(q[i].y);
+                v[4 * i + 2] = __uint_as_float(q[i].z);
+                v[4 * i + 3] = __uint_as_float(q[i].w);
+            }
+        } else {
+            unpack8(q[0], v);
+        }
+    }
+};
+
 // One warp per slot (neighbouring warps share a token, whose row then comes from L1).
 template <bool DF32, bool YF32, bool VEC>
 __global__ void __launch_bounds__(kOrderThreads) combine_backward_kernel(const __grid_constant__ CombineBackParams p)
@@ -183,36 +212,33 @@ __global__ void __launch_bounds__(kOrderThreads) combine_backward_kernel(const _
         uint16_t *o = static_cast<uint16_t *>(p.dy) + r * p.ld_dy;
         float sum = 0.f;
         for (int c0 = W * lane; c0 < p.H; c0 += 32 * W * U) {
-            float a[U][W], b[U][W];
+            Raw<DF32, VEC> a[U];
+            Raw<YF32, VEC> b[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int c = c0 + 32 * W * i;
+                if (c < p.H && p.dw) b[i].load(y, c);
+            }
 #pragma unroll
-                for (int j = 0; j < W; ++j) a[i][j] = b[i][j] = 0.f;
-                if (c < p.H) {
-                    if constexpr (VEC) {
-                        load8<DF32>(d, c, a[i]);
-                        if (p.dw) load8<YF32>(y, c, b[i]);
-                    } else {
-                        a[i][0] = DF32 ? __ldg(reinterpret_cast<const float *>(d) + c)
-                                       : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(d) + c) << 16);
-                        if (p.dw)
-                            b[i][0] = YF32 ? __ldg(reinterpret_cast<const float *>(y) + c)
-                                           : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(y) + c) << 16);
-                    }
-                }
+            for (int i = 0; i < U; ++i) {
+                const int c = c0 + 32 * W * i;
+                if (c < p.H) a[i].load(d, c);
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int c = c0 + 32 * W * i;
                 if (c >= p.H) continue;
+                float u[W], v[W];
+                a[i].open(u);
+                if (p.dw) {
+                    b[i].open(v);
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    sum = fmaf(a[i][j], b[i][j], sum);
-                    a[i][j] *= f;
+                    for (int j = 0; j < W; ++j) sum = fmaf(u[j], v[j], sum);
                 }
-                if constexpr (VEC) *reinterpret_cast<uint4 *>(o + c) = pack8(a[i]);
-                else o[c] = __bfloat16_as_ushort(__float2bfloat16_rn(a[i][0]));
+#pragma unroll
+                for (int j = 0; j < W; ++j) u[j] *= f;
+                if constexpr (VEC) *reinterpret_cast<uint4 *>(o + c) = pack8(u);
+                else o[c] = __bfloat16_as_ushort(__float2bfloat16_rn(u[0]));
             }
         }
         if (p.dw) {
@@ -242,8 +268,10 @@ cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s)
     const int piece = vec ? 16 : 2, unit = vec ? 4 : 8;
     const int chunks = (p.row_bytes / piece + 32 * unit - 1) / (32 * unit);
     const int64_t want = ((int64_t)p.P * chunks + per - 1) / per, most = (int64_t)sm_count() * 32;
+    // CTAs for what is small: a thread per scale or slot, up to one CTA per SM
+    const int64_t items = (int64_t)p.P * (p.blocks > 0 ? p.blocks : 1), each = (items + kOrderThreads - 1) / kOrderThreads;
     p.small = 0;
-    if (p.pos || p.row_w || p.blocks) p.small = p.P <= kPosByOneCta ? 1 + p.P / 1024 : p.P / 1024 < sm_count() ? p.P / 1024 : sm_count();
+    if (p.pos || p.row_w || p.blocks) p.small = p.clear && !p.blocks ? 1 : (int)(each < sm_count() ? each : sm_count());
     const unsigned grid = (unsigned)(want < most ? want : most) + p.small;
     if (vec) FT_LAUNCH(dispatch_kernel<uint4, 4>, dim3(grid), dim3(kOrderThreads), 0, s, p);
     else FT_LAUNCH(dispatch_kernel<uint16_t, 8>, dim3(grid), dim3(kOrderThreads), 0, s, p);

@@ -647,11 +647,12 @@ static EncodeTiledFn encode_fn()
 // wants one: such a thread gets its device's context here. (Calls that launch another kernel first
 // never meet this; a call that begins with its tensor maps would fail in every new thread.)
 static bool encode(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const cuuint64_t *dims,
-                   const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swz, CUtensorMapL2promotion l2)
+                   const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swz, CUtensorMapL2promotion l2,
+                   uint32_t row_step = 1)
 {
     const EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[3] = {1, row_step, 1};
     auto once = [&]() {
         return fn(map, dt, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swz, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -662,12 +663,12 @@ static bool encode(CUtensorMap *map, CUtensorMapDataType dt, int rank, const voi
 }
 
 bool make_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
-                        uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz)
+                        uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz, uint32_t row_step)
 {
     const cuuint64_t dims[2] = {inner, rows};
     const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {box_inner, box_rows};
-    return encode(map, dt, 2, base, dims, strides, box, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    const cuuint32_t box[2] = {box_inner, box_rows * row_step};
+    return encode(map, dt, 2, base, dims, strides, box, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, row_step);
 }
 
 bool make_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,

@@ -51,7 +51,6 @@ def test_quantizer_is_bit_exact(ft, P, K, pad, dtype):
         x[0, :15] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, -0.25, -0.75, -1.25, -1.75, -2.5, -3.5, -5.0])
         x[0, 15:32] = 0
     codes = torch.full((P, K // 2 + 16), 0xAA, dtype=U8, device="cuda")
-    scales = torch.full(((K + 127) // 128, P + 3, 4), 0xBB, dtype=U8, device="cuda")
     scales = torch.full(((K + 127) // 128, (P + 7) // 4 * 4, 4), 0xBB, dtype=U8, device="cuda")
     ft.ft_moe_quantize_mxfp4(x[:, :K], codes[:, :K // 2], scales[:, :P])
     ref_c, ref_s = rule(x[:, :K].float())
@@ -164,6 +163,9 @@ GROUPS = [
     ([1], 128, 32), ([1], 128, 256), ([3], 130, 96), ([1], 2048, 2048), ([8], 1024, 4096), ([31, 0, 2], 200, 544),
     ([0, 5, 0, 1, 17, 0], 257, 320), ([16, 24, 33], 640, 512), ([100, 0, 3, 250], 384, 672), ([129], 96, 1024),
     ([300], 256, 2048), ([1, 700, 64], 1000, 288), ([513, 511], 512, 512), ([2000, 100], 776, 256), ([1] * 40, 256, 544),
+    # by pairs of CTAs: first rows at every remainder of four, tiles that end one before, at and behind their last row
+    ([301, 0, 258, 3, 1023, 130], 1000, 544), ([255, 257, 256, 1, 511], 1213, 96), ([700, 640], 3000, 2112), ([5000], 520, 288),
+    ([129] * 20, 264, 320), ([253, 254, 255, 256, 257, 258, 259], 1984, 128), ([9000, 1], 192, 64),
 ]
 
 
