@@ -160,13 +160,13 @@ bool make_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *ba
                         uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz,
                         uint32_t row_step = 1);
 
-// The same for a stack of `mats` matrices mat_bytes apart (boxes lie inside one matrix; what a box
+// The same for a stack of `mats` matrices mat_bytes apart (a box takes box_mats of them; what it
 // reaches beyond its matrix reads as zero). Lines come into L2 in pairs: a 128-byte wide box walks
 // along the rows, and its next step reads the other half (64 decode rows over 256 experts: 152 us
 // with single lines, 144 with pairs).
 bool make_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t mats, uint64_t row_bytes, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_rows,
-                        CUtensorMapSwizzle swz);
+                        CUtensorMapSwizzle swz, uint32_t box_mats = 1);
 
 // A grouped bf16 product (group_gemm.cu). Forward uses x and w, dgrad dy and w, wgrad dy and x;
 // `out` is y, dx or dw. Pointers, strides and sizes are the entry points', already checked.

@@ -22,7 +22,7 @@ namespace {
 
 using namespace grp;
 
-constexpr int kThreads4 = 384;   // warps: 0 TMA, 1 MMA, 2-3 scales of x, 4..11 epilogue
+constexpr int kThreads4 = 416;   // warps: 0 TMA, 1 MMA, 2-3 scales of x, 4..11 epilogue, 12 units
 constexpr int kStep4 = 256;      // contraction steps per stage
 constexpr int kTileBytes = 512;  // scale words of 128 rows x 128 steps
 // fp32 outputs: sums in parts of this many stages (32 instructions), added in registers, since the tensor cores
@@ -108,8 +108,72 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, int pair)
            ((uint32_t)(2 * pair) << 4) | ((uint32_t)(2 * pair) << 29);
 }
 
+// Where a unit's tile lies: found by one warp of the CTA ahead of the others, which take it from a ring in shared memory.
+// (Finding it, a binary search over the experts and a division, takes a warp 800 cycles with one expert and up to 2000
+// with 256: done by the issuing warps themselves, the tensor cores stood still that long between two units.)
 struct Unit4 {
-    int e, m0, row0, rows, cols;  // cols: rows in whole MMA columns
+    int e;           // expert, or -1 after the last unit
+    int row0;        // first row of the tile
+    int lo, hi;      // wide tiles: rows [row0 + lo, row0 + hi) are the expert's; else lo = 0 and hi of them are
+    int n0;          // first weight row
+    int cols;        // columns of an MMA: rows (wide tiles: weight rows) in whole MMA columns
+    int pad[2];
+};
+static_assert(sizeof(Unit4) == 32, "two 16-byte stores");
+
+constexpr int kUnitSlots = 4;
+
+struct UnitRing {
+    Unit4 *slot;
+    uint64_t *full, *empty;
+    volatile int *abort_flag;
+    uint64_t wl;
+    int turn = 0;
+
+    __device__ __forceinline__ UnitRing(void *smem, uint64_t *bars, volatile int *flag, uint64_t limit)
+        : slot(static_cast<Unit4 *>(smem)), full(bars), empty(bars + kUnitSlots), abort_flag(flag), wl(limit) {}
+
+    // By one thread: `readers` warps take every unit.
+    __device__ __forceinline__ void init(int readers)
+    {
+        for (int i = 0; i < kUnitSlots; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, readers);
+        }
+    }
+
+    // The finding warp; false: given up.
+    __device__ __forceinline__ bool put(const Unit4 &x)
+    {
+        const int i = turn % kUnitSlots;
+        if (!warp_wait(empty + i, ((turn / kUnitSlots) & 1) ^ 1, abort_flag, wl)) return false;
+        if ((threadIdx.x & 31) == 0) {
+            int4 *to = reinterpret_cast<int4 *>(slot + i);
+            to[0] = make_int4(x.e, x.row0, x.lo, x.hi);
+            to[1] = make_int4(x.n0, x.cols, 0, 0);
+            mbar_arrive(full + i);
+        }
+        __syncwarp();
+        ++turn;
+        return true;
+    }
+
+    // The others: the next unit, the same in all lanes. `dead` is set where the wait gave up.
+    __device__ __forceinline__ bool get(Unit4 &x, bool &dead)
+    {
+        const int i = turn % kUnitSlots;
+        if (!warp_wait(full + i, (turn / kUnitSlots) & 1, abort_flag, wl)) {
+            dead = true;
+            return false;
+        }
+        const int4 *from = reinterpret_cast<const int4 *>(slot + i);
+        const int4 a = from[0], b = from[1];
+        x.e = uniform(a.x); x.row0 = uniform(a.y); x.lo = uniform(a.z); x.hi = uniform(a.w);
+        x.n0 = uniform(b.x); x.cols = uniform(b.y);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(empty + i);  // (after the shuffles: every lane has read)
+        ++turn;
+        return x.e >= 0;
+    }
 };
 
 }  // namespace
@@ -127,12 +191,15 @@ __global__ void __launch_bounds__(kThreads4, 1)
     unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S * T::stage);
     uint64_t *empty = full + S, *sc_full = empty + S, *acc_full = sc_full + S, *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *unit_bars = acc_empty + 2;
+    Unit4 *sh_unit = reinterpret_cast<Unit4 *>(unit_bars + 2 * kUnitSlots);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + kUnitSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
+    UnitRing ring(sh_unit, unit_bars, abort_flag, wl);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(full + i, 1);
@@ -143,6 +210,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
             mbar_init(acc_full + i, 1);
             mbar_init(acc_empty + i, 8);  // every epilogue warp
         }
+        ring.init(12);  // all warps but the one that finds the units
         *abort_flag = 0;
         fence_mbar_init();
         tc::prefetch_map(&map_w);
@@ -168,15 +236,12 @@ __global__ void __launch_bounds__(kThreads4, 1)
         const Tile x = find_tile(t, p.E, BN, 16, sh_offs, sh_tiles);
         Unit4 r;
         r.e = x.e;
-        r.m0 = (u - t * m_tiles) * kTileM;
+        r.n0 = (u - t * m_tiles) * kTileM;
         r.row0 = x.row0;
-        r.rows = x.rows;
+        r.lo = 0;
+        r.hi = x.rows;
         r.cols = (x.rows + 15) / 16 * 16;
         return r;
-    };
-    auto uniform_unit = [](Unit4 x) {
-        x.e = uniform(x.e); x.m0 = uniform(x.m0); x.row0 = uniform(x.row0); x.rows = uniform(x.rows); x.cols = uniform(x.cols);
-        return x;
     };
     bool dead = false;
 
@@ -186,10 +251,9 @@ __global__ void __launch_bounds__(kThreads4, 1)
             const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
-            for (int u = u0; u < units && !dead; u += du) {
-                const Unit4 x = uniform_unit(unit_of(u));
+            for (Unit4 x; !dead && ring.get(x, dead);) {
                 const int boxes = (x.cols + T::box_rows - 1) / T::box_rows;
-                const uint8_t *ws = p.ws + ((int64_t)x.e * m_tiles + x.m0 / kTileM) * kt * kTileBytes;
+                const uint8_t *ws = p.ws + ((int64_t)x.e * m_tiles + x.n0 / kTileM) * kt * kTileBytes;
                 for (int b = b0; b < nb; ++b, ++it) {
                     if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
@@ -197,7 +261,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
                     const uint32_t sf = min(kt - 2 * b, 2) * kTileBytes;  // (the last stage may have one word a row)
                     if (one) {
                         mbar_arrive_expect_tx(full + s, kABytes + boxes * T::box_rows * kChunkBytes + sf);
-                        load_3d<1>(sa, &map_w, b * kChunkBytes, x.m0, x.e, bar);
+                        load_3d<1>(sa, &map_w, b * kChunkBytes, x.n0, x.e, bar);
                         bulk_g2s(sb + T::b_bytes, ws + 2 * b * kTileBytes, sf, full + s);
                         for (int i = 0; i < boxes; ++i)
                             load_2d<1>(sb + i * T::box_rows * kChunkBytes, &map_x, b * kChunkBytes, x.row0 + i * T::box_rows, bar);
@@ -218,8 +282,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
         const bool one = elect_one();
         int s = 0, ac = 0, it = 0;
         uint32_t ph = 0;
-        for (int u = u0; u < units && !dead; u += du) {
-            const Unit4 x = uniform_unit(unit_of(u));
+        for (Unit4 x; !dead && ring.get(x, dead);) {
             const uint32_t idesc[2] = {idesc_mxf4(kTileM, x.cols, 0), idesc_mxf4(kTileM, x.cols, 1)};
             for (int b = b0; b < nb; ++b, ++it) {
                 const int in_part = F32 ? (b - b0) % kPart4 : b - b0;
@@ -261,8 +324,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
         // word c / 32 of lane c % 32; columns beyond the tile's rows get zeros (their sums are not stored).
         constexpr int G = T::group, C = BN / 32;
         int g = 0, it = 0;  // groups and stages so far, over all units
-        for (int u = u0; u < units && !dead; u += du) {
-            const Unit4 x = unit_of(u);
+        for (Unit4 x; !dead && ring.get(x, dead);) {
             const uint32_t *xr = p.xs + x.row0;
             for (int b = b0; b < nb; b += G, ++g) {
                 const int len = min(G, nb - b);
@@ -275,7 +337,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
 #pragma unroll
                             for (int c = 0; c < C; ++c) {
                                 const int at = 2 * (b + i) + k;
-                                v[i][k][c] = at < kt && 32 * c + lane < x.rows ? __ldg(xr + at * p.ld_xs + 32 * c + lane) : 0u;
+                                v[i][k][c] = at < kt && 32 * c + lane < x.hi ? __ldg(xr + at * p.ld_xs + 32 * c + lane) : 0u;
                             }
 #pragma unroll
                     for (int i = 0; i < G; ++i) {
@@ -300,17 +362,16 @@ __global__ void __launch_bounds__(kThreads4, 1)
             }
         }
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
-    } else {
+    } else if (warp < 12) {
         // ------------------------------------------------------------ epilogue
         // thread = TMEM lane = weight row; columns [h * HC, h * HC + HC) of the tile
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16) + h * HC;
         int ac = 0;
         const int parts = F32 ? (nb - b0 + kPart4 - 1) / kPart4 : 1;
-        for (int u = u0; u < units && !dead; u += du) {
-            const Unit4 x = unit_of(u);
-            const int mine = min(max(x.rows - h * HC, 0), HC);  // columns of this half in use
-            const int m = x.m0 + 32 * q + lane;
+        for (Unit4 x; !dead && ring.get(x, dead);) {
+            const int mine = min(max(x.hi - h * HC, 0), HC);  // columns of this half in use
+            const int m = x.n0 + 32 * q + lane;
             const int64_t row0 = x.row0 + h * HC;
             auto emit = [&](int c, const float (&v)[W]) {
                 if (split > 1) {
@@ -362,6 +423,16 @@ __global__ void __launch_bounds__(kThreads4, 1)
             }
         }
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+    } else {
+        // ------------------------------------------------------------ units
+        Unit4 x;
+        for (int u = u0; u < units && !dead; u += du) {
+            x = unit_of(u);
+            dead = !ring.put(x);
+        }
+        x.e = -1;
+        if (!dead) dead = !ring.put(x);
+        if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     }
 
     // wind down; a cluster leaves together
@@ -371,7 +442,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
         cluster_sync();
         if (u0 < units) {
             const Unit4 x = unit_of(u0);
-            add_parts<F32>(reinterpret_cast<const float *>(smem), x.rows, x.m0, p.N, x.row0, p.out, p.ld, split, part);
+            add_parts<F32>(reinterpret_cast<const float *>(smem), x.hi, x.n0, p.N, x.row0, p.out, p.ld, split, part);
         }
         cluster_sync();
     }
@@ -386,9 +457,9 @@ __global__ void __launch_bounds__(kThreads4, 1)
 // Everything comes by TMA, the scales too, so that no warp stands between memory and the tensor cores. For that
 // the rows' scale words must lie in shared memory in tensor memory's order as they come: lane r of 32 takes four
 // neighbouring words, of rows 4 r .. 4 r + 3, for the MMA's rows r, 32 + r, 64 + r and 96 + r. So row 4 r + j of the tile is
-// the MMA's row 32 j + r: the codes are fetched in four boxes of every fourth row (the tensor map's row step), and a
-// tile begins at a multiple of four rows, at most three before its expert's first one (neither those nor the rows behind
-// the expert's last are stored). Tensor memory holds two accumulators of 192 columns and two stages' scales; 256
+// the MMA's row 32 j + r: one box fetches the codes in that order from x seen as [4][P / 4] rows (the tile that holds
+// the last P % 4 rows takes four boxes of every fourth row instead), and a tile begins at a multiple of four rows, at
+// most three before its expert's first one (neither those nor the rows behind the expert's last are stored). Tensor memory holds two accumulators of 192 columns and two stages' scales; 256
 // columns would fill it with the accumulators alone.
 
 namespace {
@@ -412,8 +483,8 @@ struct RingP {
 template <bool F32>
 __global__ void __launch_bounds__(RingP::threads, 1)
     group_gemm_mxfp4_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                                 const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs,
-                                 const __grid_constant__ Group4Params p)
+                                 const __grid_constant__ CUtensorMap map_x_end, const __grid_constant__ CUtensorMap map_ws,
+                                 const __grid_constant__ CUtensorMap map_xs, const __grid_constant__ Group4Params p)
 {
     using T = RingP;
     constexpr int S = T::stages, BN = T::BN;
@@ -422,7 +493,9 @@ __global__ void __launch_bounds__(RingP::threads, 1)
     unsigned char *sh_out = smem + S * T::stage;
     uint64_t *full = reinterpret_cast<uint64_t *>(sh_out + T::out);
     uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint64_t *unit_bars = acc_empty + 2;
+    Unit4 *sh_unit = reinterpret_cast<Unit4 *>(unit_bars + 2 * kUnitSlots);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + kUnitSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
@@ -430,6 +503,7 @@ __global__ void __launch_bounds__(RingP::threads, 1)
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
+    UnitRing ring(sh_unit, unit_bars, abort_flag, wl);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(full + i, 1);
@@ -439,10 +513,12 @@ __global__ void __launch_bounds__(RingP::threads, 1)
             mbar_init(acc_full + i, 1);
             mbar_init(acc_empty + i, 2 * T::warps);  // the epilogue warps of both CTAs
         }
+        ring.init(T::warps + 1 + (int)leader);  // the producer and the epilogue, in the leader the MMA issuer
         *abort_flag = 0;
         fence_mbar_init();
         tc::prefetch_map(&map_w);
         tc::prefetch_map(&map_x);
+        tc::prefetch_map(&map_x_end);
         tc::prefetch_map(&map_ws);
         tc::prefetch_map(&map_xs);
     }
@@ -457,22 +533,18 @@ __global__ void __launch_bounds__(RingP::threads, 1)
 
     const int n_tiles = (p.N + BN - 1) / BN;
     const int units = uniform(sh_tiles[p.E]) * n_tiles;
-    const int nb = (p.K + kStep4 - 1) / kStep4, kt = (p.K + 127) / 128, nt128 = (p.N + 127) / 128;
+    const int nb = (p.K + kStep4 - 1) / kStep4, nt128 = (p.N + 127) / 128;
     const int u0 = blockIdx.x / 2, du = gridDim.x / 2;
-    struct UnitP {
-        int e, row0, lo, hi;  // rows [row0 + lo, row0 + hi) are the expert's
-        int n0, half;         // first weight row, and how many of them each CTA loads for the MMA (in steps of 16)
-    };
     auto unit_of = [&](int u) {
         const int t = u / n_tiles;
         const AlignedTile x = find_aligned_tile<4>(t, p.E, 2 * kTileM, sh_offs, sh_tiles);
-        UnitP r;
-        r.e = uniform(x.e);
-        r.row0 = uniform(x.row0);
-        r.lo = uniform(x.lo);
-        r.hi = uniform(x.hi);
-        r.n0 = uniform((u - t * n_tiles) * BN);
-        r.half = uniform((min(p.N - r.n0, BN) + 31) / 32 * 16);
+        Unit4 r;
+        r.e = x.e;
+        r.row0 = x.row0;
+        r.lo = x.lo;
+        r.hi = x.hi;
+        r.n0 = (u - t * n_tiles) * BN;
+        r.cols = (min(p.N - r.n0, BN) + 31) / 32 * 32;
         return r;
     };
     bool dead = false;
@@ -483,26 +555,24 @@ __global__ void __launch_bounds__(RingP::threads, 1)
             const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
-            for (int u = u0; u < units && !dead; u += du) {
-                const UnitP x = unit_of(u);
+            for (Unit4 x; !dead && ring.get(x, dead);) {
                 const bool rows[2] = {x.hi > 0, x.hi > kTileM};         // whether a CTA has rows
-                const int t0 = x.n0 / 128, tiles = min(nt128 - t0, 2);  // tiles of the weights' scales
-                const uint32_t each = T::b_bytes + tiles * 2 * kTileBytes;
-                const uint32_t bytes = 2 * each + ((int)rows[0] + (int)rows[1]) * (kABytes + T::a_sf);
-                const int64_t ws_row = ((int64_t)x.e * nt128 + t0) * kt;
+                const uint32_t bytes = 2 * (T::b_bytes + T::b_sf) + ((int)rows[0] + (int)rows[1]) * (kABytes + T::a_sf);
+                const int ws_tile = x.e * nt128 + x.n0 / 128, row = x.row0 + (int)rank * kTileM;
+                const bool whole = row + kTileM <= p.P / 4 * 4 || p.P % 4 == 0;
                 for (int b = 0; b < nb; ++b, ++it) {
                     if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes, *sf = sb + T::b_bytes;
                     const uint32_t bar = map_rank(full + s, 0);
                     if (one) {
                         if (leader) mbar_arrive_expect_tx(full + s, bytes);
-                        load_3d<2>(sb, &map_w, b * kChunkBytes, x.n0 + (int)rank * x.half, x.e, bar);
-                        for (int i = 0; i < tiles; ++i)
-                            load_2d<2>(sf + T::a_sf + i * 2 * kTileBytes, &map_ws, 0, (int)(ws_row + i * kt) + 2 * b, bar);
+                        load_3d<2>(sb, &map_w, b * kChunkBytes, x.n0 + (int)rank * (x.cols / 2), x.e, bar);
+                        load_3d<2>(sf + T::a_sf, &map_ws, 0, 2 * b, ws_tile, bar);
                         if (rows[rank]) {
-                            const int row = x.row0 + (int)rank * kTileM;
-                            for (int j = 0; j < 4; ++j) load_2d<2>(sa + j * 32 * kChunkBytes, &map_x, b * kChunkBytes, row + j, bar);
                             load_2d<2>(sf, &map_xs, row, 2 * b, bar);
+                            if (whole) load_3d<2>(sa, &map_x, b * kChunkBytes, row / 4, 0, bar);
+                            else
+                                for (int j = 0; j < 4; ++j) load_2d<2>(sa + j * 32 * kChunkBytes, &map_x_end, b * kChunkBytes, row + j, bar);
                         }
                     }
                     __syncwarp();
@@ -525,9 +595,8 @@ __global__ void __launch_bounds__(RingP::threads, 1)
             const bool one = elect_one();
             int s = 0, ac = 0, it = 0;
             uint32_t ph = 0;
-            for (int u = u0; u < units && !dead; u += du) {
-                const UnitP x = unit_of(u);
-                const uint32_t idesc[2] = {idesc_mxf4(2 * kTileM, 2 * x.half, 0), idesc_mxf4(2 * kTileM, 2 * x.half, 1)};
+            for (Unit4 x; !dead && ring.get(x, dead);) {
+                const uint32_t idesc[2] = {idesc_mxf4(2 * kTileM, x.cols, 0), idesc_mxf4(2 * kTileM, x.cols, 1)};
                 const bool two = nt128 - x.n0 / 128 > 1;
                 const uint32_t col0 = x.n0 % 128 / 32;  // of the unit's first weight row in its tile's scales
                 for (int b = 0; b < nb; ++b, ++it) {
@@ -566,6 +635,16 @@ __global__ void __launch_bounds__(RingP::threads, 1)
                 }
             }
             if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
+        } else if (warp == 2) {
+            // -------------------------------------------------------- units
+            Unit4 x;
+            for (int u = u0; u < units && !dead; u += du) {
+                x = unit_of(u);
+                dead = !ring.put(x);
+            }
+            x.e = -1;
+            if (!dead) dead = !ring.put(x);
+            if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -576,8 +655,7 @@ __global__ void __launch_bounds__(RingP::threads, 1)
         unsigned char *tile = sh_out + (warp - 4) * 16 * 128;
         const int parts = F32 ? (nb + kPart4 - 1) / kPart4 : 1;
         int ac = 0;
-        for (int u = u0; u < units && !dead; u += du) {
-            const UnitP x = unit_of(u);
+        for (Unit4 x; !dead && ring.get(x, dead);) {
             float sum[64];
             for (int t = 0; t < parts; ++t, ++ac) {
                 if (!warp_wait(acc_full + (ac & 1), (ac >> 1) & 1, abort_flag, wl)) { dead = true; break; }
@@ -671,7 +749,7 @@ cudaError_t launch4(const CUtensorMap &w, const CUtensorMap &x, Group4Params &p,
 {
     using T = Ring4<BN>;
     auto kern = group_gemm_mxfp4_kernel<BN, F32>;
-    constexpr size_t fixed = 1024 + T::stages * T::stage + 8 * (3 * T::stages + 4) + 16;
+    constexpr size_t fixed = 1024 + T::stages * T::stage + 8 * (3 * T::stages + 4 + 2 * kUnitSlots) + kUnitSlots * sizeof(Unit4) + 16;
     constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
     static_assert(most <= 227 * 1024, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
@@ -698,12 +776,12 @@ cudaError_t launch4(const CUtensorMap &w, const CUtensorMap &x, Group4Params &p,
 }
 
 template <bool F32>
-cudaError_t launch_wide4(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &ws, const CUtensorMap &xs,
-                         const Group4Params &p, cudaStream_t s)
+cudaError_t launch_wide4(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &x_end, const CUtensorMap &ws,
+                         const CUtensorMap &xs, const Group4Params &p, cudaStream_t s)
 {
     using T = RingP;
     auto kern = group_gemm_mxfp4_wide_kernel<F32>;
-    constexpr size_t fixed = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 4) + 16;
+    constexpr size_t fixed = 1024 + T::stages * T::stage + T::out + 8 * (2 * T::stages + 4 + 2 * kUnitSlots) + kUnitSlots * sizeof(Unit4) + 16;
     constexpr size_t most = fixed + table_bytes(kGroupMaxExperts);
     static_assert(most <= 227 * 1024, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
@@ -712,8 +790,8 @@ cudaError_t launch_wide4(const CUtensorMap &w, const CUtensorMap &x, const CUten
     static ClusterLimit clusters;
     int64_t grid = clusters.get(kern, 2, T::threads, most);
     if (units < grid) grid = units;
-    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), fixed + table_bytes(p.E), 2, s, w, x, ws,
-                                          xs, p);
+    const cudaError_t le = launch_cluster(kern, dim3((unsigned)grid * 2), dim3(T::threads), fixed + table_bytes(p.E), 2, s, w, x,
+                                          x_end, ws, xs, p);
     if (le != cudaSuccess) return le;
     count_launches(1);
     return cudaGetLastError();
@@ -745,7 +823,7 @@ cudaError_t launch_group_gemm_mxfp4(const GroupGemm4 &g, cudaStream_t s)
         write_plan(g.plan, 2, bn, 1, false);
         return cudaSuccess;
     }
-    CUtensorMap w, x, ws, xs;
+    CUtensorMap w, x, x_end, ws, xs;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
     const uint64_t bytes = g.K / 2, kt = (g.K + 127) / 128, nt = (g.N + 127) / 128;
@@ -753,8 +831,9 @@ cudaError_t launch_group_gemm_mxfp4(const GroupGemm4 &g, cudaStream_t s)
     if (g.plan) {  // nothing to read
     } else if (bn == 256) {
         ok = make_tensor_map_3d(&w, u8, g.w, bytes, g.N, g.E, bytes, bytes * g.N, kChunkBytes, RingP::half, sw) &&
-             make_tensor_map_2d(&x, u8, g.x, bytes, g.P, g.ld_x, kChunkBytes, 32, sw, 4) &&
-             make_tensor_map_2d(&ws, u32, g.ws, 128, g.E * nt * kt, kTileBytes, 128, 2, none) &&
+             make_tensor_map_3d(&x, u8, g.x, bytes, g.P / 4, 4, 4 * g.ld_x, g.ld_x, kChunkBytes, 32, sw, 4) &&
+             make_tensor_map_2d(&x_end, u8, g.x, bytes, g.P, g.ld_x, kChunkBytes, 32, sw, 4) &&
+             make_tensor_map_3d(&ws, u32, g.ws, 128, kt, g.E * nt, kTileBytes, kTileBytes * kt, 128, 2, none, 2) &&
              make_tensor_map_2d(&xs, u32, g.xs, g.P, kt, 4 * g.ld_xs, 128, 2, none);
     } else {
         ok = make_tensor_map_3d(&w, u8, g.w, bytes, g.N, g.E, bytes, bytes * g.N, kChunkBytes, kTileM, sw) &&
@@ -763,7 +842,7 @@ cudaError_t launch_group_gemm_mxfp4(const GroupGemm4 &g, cudaStream_t s)
     if (!ok) return cudaErrorInvalidValue;
     if (bn == 32) return g.out_f32 ? launch4<32, true>(w, x, p, g.plan, s) : launch4<32, false>(w, x, p, g.plan, s);
     if (bn == 128) return g.out_f32 ? launch4<128, true>(w, x, p, g.plan, s) : launch4<128, false>(w, x, p, g.plan, s);
-    return g.out_f32 ? launch_wide4<true>(w, x, ws, xs, p, s) : launch_wide4<false>(w, x, ws, xs, p, s);
+    return g.out_f32 ? launch_wide4<true>(w, x, x_end, ws, xs, p, s) : launch_wide4<false>(w, x, x_end, ws, xs, p, s);
 }
 
 }  // namespace ftmoe

@@ -673,11 +673,11 @@ bool make_tensor_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *ba
 
 bool make_tensor_map_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows,
                         uint64_t mats, uint64_t row_bytes, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_rows,
-                        CUtensorMapSwizzle swz)
+                        CUtensorMapSwizzle swz, uint32_t box_mats)
 {
     const cuuint64_t dims[3] = {inner, rows, mats};
     const cuuint64_t strides[2] = {row_bytes, mat_bytes};
-    const cuuint32_t box[3] = {box_inner, box_rows, 1};
+    const cuuint32_t box[3] = {box_inner, box_rows, box_mats};
     return encode(map, dt, 3, base, dims, strides, box, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
