@@ -308,40 +308,50 @@ struct Tile {
 
 // Offsets of the experts (clamped into [0, P], never decreasing inside an expert) and the
 // running count of their tiles, in shared memory: [E + 1] ints each. Run by all threads.
-// Returns whether the offsets were valid. `sh_flag` is one int of shared memory. ALIGN: tiles begin at multiples of it
-// (find_aligned_tile).
+// Returns whether the offsets were valid. ALIGN: tiles begin at multiples of it (find_aligned_tile).
+// Every warp finds what lies before its own experts by itself, so that one barrier is all it takes (the callers
+// synchronise before the table is used).
 template <int ALIGN = 1>
-__device__ __forceinline__ bool build_table(const int *offs, int E, int P, int BN, int *sh_offs, int *sh_tiles, int *sh_flag)
+__device__ __forceinline__ bool build_table(const int *offs, int E, int P, int BN, int *sh_offs, int *sh_tiles)
 {
-    if (threadIdx.x == 0) *sh_flag = 0;
-    __syncthreads();
+    bool bad = false;
     for (int i = threadIdx.x; i <= E; i += blockDim.x) {
-        const int v = offs ? __ldg(offs + i) : (i ? P : 0);
+        const int v = offs ? __ldg(offs + i) : (i ? P : 0), next = offs && i < E ? __ldg(offs + i + 1) : v;
         sh_offs[i] = min(max(v, 0), P);
-        bool bad = v < 0 || v > P;
-        if (i < E && offs) bad |= __ldg(offs + i + 1) < v;
-        if (bad) *sh_flag = 1;
+        bad |= v < 0 || v > P || (offs && next < v);
     }
-    __syncthreads();
-    if (threadIdx.x < 32) {
+    const bool valid = !__syncthreads_or(bad);
+    auto tiles = [&](int i) {
+        const int first = sh_offs[i], last = sh_offs[i + 1];
+        return last > first ? (last - (ALIGN > 1 ? first / ALIGN * ALIGN : first) + BN - 1) / BN : 0;
+    };
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    for (int i0 = 32 * (threadIdx.x >> 5); i0 < E; i0 += 32 * warps) {
         int base = 0;
-        for (int i0 = 0; i0 < E; i0 += 32) {
-            const int i = i0 + threadIdx.x;
-            int t = 0;
-            if (i < E && sh_offs[i + 1] > sh_offs[i])
-                t = (sh_offs[i + 1] - (ALIGN > 1 ? sh_offs[i] / ALIGN * ALIGN : sh_offs[i]) + BN - 1) / BN;
+        for (int i = lane; i < i0; i += 32) base += tiles(i);
+        base = __reduce_add_sync(0xFFFFFFFFu, base);
+        const int i = i0 + lane;
+        int t = i < E ? tiles(i) : 0;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
-                if ((int)threadIdx.x >= d) t += o;
-            }
-            if (i < E) sh_tiles[i + 1] = base + t;
-            base += __shfl_sync(0xFFFFFFFFu, t, 31);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
+            if (lane >= d) t += o;
         }
-        if (threadIdx.x == 0) sh_tiles[0] = 0;
+        if (i < E) sh_tiles[i + 1] = base + t;
     }
-    __syncthreads();
-    return *sh_flag == 0;
+    if (threadIdx.x == 0) sh_tiles[0] = 0;
+    return valid;
+}
+
+__device__ __forceinline__ Tile tile_of(int t, int e, int BN, int gran, const int *sh_offs, const int *sh_tiles)
+{
+    const int n = sh_offs[e + 1] - sh_offs[e], nt = (n + BN - 1) / BN, j = t - sh_tiles[e];
+    const int len = ((n + nt - 1) / nt + gran - 1) / gran * gran;
+    Tile r;
+    r.e = e;
+    r.row0 = sh_offs[e] + j * len;
+    r.rows = max(min(len, n - j * len), 0);
+    return r;
 }
 
 __device__ __forceinline__ Tile find_tile(int t, int E, int BN, int gran, const int *sh_offs, const int *sh_tiles)
@@ -352,13 +362,16 @@ __device__ __forceinline__ Tile find_tile(int t, int E, int BN, int gran, const 
         if (sh_tiles[mid] <= t) lo = mid;
         else hi = mid;
     }
-    const int n = sh_offs[lo + 1] - sh_offs[lo], nt = (n + BN - 1) / BN, j = t - sh_tiles[lo];
-    const int len = ((n + nt - 1) / nt + gran - 1) / gran * gran;
-    Tile r;
-    r.e = lo;
-    r.row0 = sh_offs[lo] + j * len;
-    r.rows = max(min(len, n - j * len), 0);
-    return r;
+    return tile_of(t, lo, BN, gran, sh_offs, sh_tiles);
+}
+
+// The expert of tile t, by a whole warp: the last one whose running count is t or less.
+__device__ __forceinline__ int expert_of(int t, int E, const int *sh_tiles)
+{
+    const int lane = threadIdx.x & 31;
+    const int c = __popc(__ballot_sync(0xFFFFFFFFu, 32 * lane < E && sh_tiles[32 * lane] <= t)) - 1;  // its group of 32
+    const int i = 32 * c + lane;
+    return 32 * c + __popc(__ballot_sync(0xFFFFFFFFu, i < E && sh_tiles[i] <= t)) - 1;
 }
 
 // The same where the first tile of an expert begins at the multiple of ALIGN at or before its first row and the
@@ -370,12 +383,7 @@ struct AlignedTile {
 template <int ALIGN>
 __device__ __forceinline__ AlignedTile find_aligned_tile(int t, int E, int BN, const int *sh_offs, const int *sh_tiles)
 {
-    int lo = 0, hi = E;  // sh_tiles[lo] <= t < sh_tiles[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh_tiles[mid] <= t) lo = mid;
-        else hi = mid;
-    }
+    const int lo = expert_of(t, E, sh_tiles);
     AlignedTile r;
     r.e = lo;
     r.row0 = sh_offs[lo] / ALIGN * ALIGN + (t - sh_tiles[lo]) * BN;

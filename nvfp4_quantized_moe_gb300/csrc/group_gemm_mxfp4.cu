@@ -117,7 +117,8 @@ struct Unit4 {
     int lo, hi;      // wide tiles: rows [row0 + lo, row0 + hi) are the expert's; else lo = 0 and hi of them are
     int n0;          // first weight row
     int cols;        // columns of an MMA: rows (wide tiles: weight rows) in whole MMA columns
-    int pad[2];
+    int width;       // wide tiles: weight rows
+    int unused;
 };
 static_assert(sizeof(Unit4) == 32, "two 16-byte stores");
 
@@ -150,7 +151,7 @@ struct UnitRing {
         if ((threadIdx.x & 31) == 0) {
             int4 *to = reinterpret_cast<int4 *>(slot + i);
             to[0] = make_int4(x.e, x.row0, x.lo, x.hi);
-            to[1] = make_int4(x.n0, x.cols, 0, 0);
+            to[1] = make_int4(x.n0, x.cols, x.width, 0);
             mbar_arrive(full + i);
         }
         __syncwarp();
@@ -169,7 +170,7 @@ struct UnitRing {
         const int4 *from = reinterpret_cast<const int4 *>(slot + i);
         const int4 a = from[0], b = from[1];
         x.e = uniform(a.x); x.row0 = uniform(a.y); x.lo = uniform(a.z); x.hi = uniform(a.w);
-        x.n0 = uniform(b.x); x.cols = uniform(b.y);
+        x.n0 = uniform(b.x); x.cols = uniform(b.y); x.width = uniform(b.z);
         if ((threadIdx.x & 31) == 0) mbar_arrive(empty + i);  // (after the shuffles: every lane has read)
         ++turn;
         return x.e >= 0;
@@ -195,7 +196,6 @@ __global__ void __launch_bounds__(kThreads4, 1)
     Unit4 *sh_unit = reinterpret_cast<Unit4 *>(unit_bars + 2 * kUnitSlots);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + kUnitSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
@@ -217,8 +217,11 @@ __global__ void __launch_bounds__(kThreads4, 1)
         tc::prefetch_map(&map_x);
     }
     if (warp == 1) tmem_alloc<1>(tmem_slot, T::tmem);
-    pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
-    const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles, sh_flag);
+    // (only now: the set-up above overlaps the end of the kernel before. The kernel behind this one is not let in early:
+    // its CTAs would come to SMs whose L1 is almost all shared memory here, and keep them so. A quantizer of 16384 x
+    // 2048 values behind this kernel took 24 us instead of 15.)
+    pdl_wait();
+    const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
     __syncthreads();
@@ -233,8 +236,8 @@ __global__ void __launch_bounds__(kThreads4, 1)
     const int u0 = blockIdx.x / split, du = gridDim.x / split;
     auto unit_of = [&](int u) {
         const int t = u / m_tiles;
-        const Tile x = find_tile(t, p.E, BN, 16, sh_offs, sh_tiles);
-        Unit4 r;
+        const Tile x = tile_of(t, expert_of(t, p.E, sh_tiles), BN, 16, sh_offs, sh_tiles);
+        Unit4 r = {};
         r.e = x.e;
         r.n0 = (u - t * m_tiles) * kTileM;
         r.row0 = x.row0;
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     } else {
         // ------------------------------------------------------------ units
-        Unit4 x;
+        Unit4 x = {};
         for (int u = u0; u < units && !dead; u += du) {
             x = unit_of(u);
             dead = !ring.put(x);
@@ -497,7 +500,6 @@ __global__ void __launch_bounds__(RingP::threads, 1)
     Unit4 *sh_unit = reinterpret_cast<Unit4 *>(unit_bars + 2 * kUnitSlots);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + kUnitSlots);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -523,28 +525,33 @@ __global__ void __launch_bounds__(RingP::threads, 1)
         tc::prefetch_map(&map_xs);
     }
     if (warp == 1) tmem_alloc<2>(tmem_slot, 512);
-    pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
-    const bool valid = build_table<4>(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles, sh_flag);
+    // (only now: the set-up above overlaps the end of the kernel before. The kernel behind this one is not let in early:
+    // its CTAs would come to SMs whose L1 is almost all shared memory here, and keep them so. A quantizer of 65536 x
+    // 2048 values behind this kernel took 85 us instead of 57.)
+    pdl_wait();
+    const bool valid = build_table<4>(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
     cluster_sync();
     tc::fence_after_sync();
     const uint32_t tmem = uniform(*tmem_slot);
 
-    const int n_tiles = (p.N + BN - 1) / BN;
+    // columns are dealt out in 64s: as many to every tile, or one more
+    const int n_tiles = (p.N + BN - 1) / BN, n64 = (p.N + 63) / 64;
     const int units = uniform(sh_tiles[p.E]) * n_tiles;
     const int nb = (p.K + kStep4 - 1) / kStep4, nt128 = (p.N + 127) / 128;
     const int u0 = blockIdx.x / 2, du = gridDim.x / 2;
     auto unit_of = [&](int u) {
-        const int t = u / n_tiles;
+        const int t = u / n_tiles, j = u - t * n_tiles;
         const AlignedTile x = find_aligned_tile<4>(t, p.E, 2 * kTileM, sh_offs, sh_tiles);
-        Unit4 r;
+        Unit4 r = {};
         r.e = x.e;
         r.row0 = x.row0;
         r.lo = x.lo;
         r.hi = x.hi;
-        r.n0 = (u - t * n_tiles) * BN;
-        r.cols = (min(p.N - r.n0, BN) + 31) / 32 * 32;
+        r.n0 = n64 * j / n_tiles * 64;
+        r.width = min(n64 * (j + 1) / n_tiles * 64, p.N) - r.n0;
+        r.cols = (r.width + 31) / 32 * 32;
         return r;
     };
     bool dead = false;
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(RingP::threads, 1)
             uint32_t ph = 0;
             for (Unit4 x; !dead && ring.get(x, dead);) {
                 const uint32_t idesc[2] = {idesc_mxf4(2 * kTileM, x.cols, 0), idesc_mxf4(2 * kTileM, x.cols, 1)};
-                const bool two = nt128 - x.n0 / 128 > 1;
+                const bool two = x.n0 % 128 + x.cols > 128;
                 const uint32_t col0 = x.n0 % 128 / 32;  // of the unit's first weight row in its tile's scales
                 for (int b = 0; b < nb; ++b, ++it) {
                     const int in_part = F32 ? b % kPart4 : b;
@@ -637,7 +644,7 @@ __global__ void __launch_bounds__(RingP::threads, 1)
             if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
         } else if (warp == 2) {
             // -------------------------------------------------------- units
-            Unit4 x;
+            Unit4 x = {};
             for (int u = u0; u < units && !dead; u += du) {
                 x = unit_of(u);
                 dead = !ring.put(x);
@@ -678,7 +685,7 @@ __global__ void __launch_bounds__(RingP::threads, 1)
             // conflicts), so that a store instruction writes whole lines of four rows; rows that are not made of
             // 16-byte pieces leave a row at a time, an element a lane
             constexpr int per = F32 ? 32 : 64;
-            const int n0 = x.n0 + 64 * g, mine = min(max(p.N - n0, 0), 64);
+            const int n0 = x.n0 + 64 * g, mine = min(max(x.width - 64 * g, 0), 64);
             const int first = (int)rank * kTileM + q;  // of the warp's rows, four apart
             const int64_t at = (int64_t)x.row0 * p.ld + n0;
             const int l8 = lane & 7, r4 = lane >> 3;
