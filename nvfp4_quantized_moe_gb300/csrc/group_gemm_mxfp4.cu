@@ -89,6 +89,20 @@ __device__ __forceinline__ void copy_scales(uint32_t to, uint64_t from)
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(from) : "memory");
 }
 
+// Whether phase `parity` of `bar` is complete, without waiting; if so, what other CTAs of the cluster released is seen.
+__device__ __forceinline__ bool test_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Shared-memory descriptor of such 512 bytes: no swizzle, groups of eight 16-byte rows 128 bytes apart.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t smem_addr)
 {
@@ -599,31 +613,56 @@ __global__ void __launch_bounds__(RingP::threads, 1)
                 }
         } else if (warp == 1 && leader) {
             // -------------------------------------------------------- MMA issuer
+            // A stage takes the tensor cores 500 cycles, and this loop must not take longer: the next stage's barrier is
+            // looked at before this stage's instructions are issued, and a whole stage's have no conditions.
             const bool one = elect_one();
-            int s = 0, ac = 0, it = 0;
-            uint32_t ph = 0;
+            const uint32_t base = smem_u32(smem);
+            const uint64_t a0 = tc::sw128_desc(base), b0 = tc::sw128_desc(base + kABytes);
+            const uint64_t f0 = scale_desc(base + kABytes + T::b_bytes);  // the rows' scales, then the weights'
+            const int whole = p.K / kStep4;                               // stages with four instructions
+            int s = 0, ac = 0;
+            uint32_t ph = 0, sf = tmem + T::sf_col;
+            bool ready = false;
             for (Unit4 x; !dead && ring.get(x, dead);) {
                 const uint32_t idesc[2] = {idesc_mxf4(2 * kTileM, x.cols, 0), idesc_mxf4(2 * kTileM, x.cols, 1)};
                 const bool two = x.n0 % 128 + x.cols > 128;
-                const uint32_t col0 = x.n0 % 128 / 32;  // of the unit's first weight row in its tile's scales
-                for (int b = 0; b < nb; ++b, ++it) {
+                const uint32_t col0 = 4 + x.n0 % 128 / 32;  // of the unit's first weight row in its tile's scales
+                for (int b = 0; b < nb; ++b) {
                     const int in_part = F32 ? b % kPart4 : b;
                     const bool first = in_part == 0, last = b + 1 == nb || (F32 && in_part == kPart4 - 1);
                     if ((first && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) ||
-                        !warp_wait(full + s, ph, abort_flag, wl)) {
+                        (!ready && !warp_wait(full + s, ph, abort_flag, wl))) {
                         dead = true;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint32_t sa = smem_u32(smem + s * T::stage);
-                    const uint64_t ad = tc::sw128_desc(sa), bd = tc::sw128_desc(sa + kABytes);
-                    const uint64_t xs = scale_desc(sa + kABytes + T::b_bytes), ws = xs + T::a_sf / 16;
-                    const uint32_t d = tmem + (uint32_t)(ac & 1) * BN, sf = tmem + T::sf_col + (it & 1) * T::sf_cols;
-                    const int steps = min((p.K - b * kStep4 + 63) / 64, 4);  // instructions that have something to multiply
-                    if (one) {
+                    const uint32_t at = (uint32_t)s * (T::stage / 16);
+                    const uint64_t ad = a0 + at, bd = b0 + at, xs = f0 + at, ws = xs + T::a_sf / 16;
+                    const uint32_t d = tmem + (uint32_t)(ac & 1) * BN;
+                    uint64_t *done = empty + s;
+                    if (++s == S) { s = 0; ph ^= 1; }
+                    const bool seen = test_cluster(full + s, ph);
+                    // columns: four of the rows' scales, eight of the weights', for each 128 steps
+                    if (b < whole) {
+                        if (one) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                copy_scales<2>(sf + 12 * k, xs + k * (kTileBytes / 16));
+                                copy_scales<2>(sf + 12 * k + 4, ws + k * (kTileBytes / 16));
+                                if (two) copy_scales<2>(sf + 12 * k + 8, ws + (2 + k) * (kTileBytes / 16));
+                            }
+                            mma_mxf4<2>(d, ad, bd, idesc[0], sf, sf + col0, !first);
+#pragma unroll
+                            for (int j = 1; j < 4; ++j)
+                                mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + col0, 1);
+                            commit<2>(done);
+                            if (last) commit<2>(acc_full + (ac & 1));
+                        }
+                    } else if (one) {
+                        const int steps = (p.K - b * kStep4 + 63) / 64;  // instructions that have something to multiply
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            if (2 * k < steps) {  // columns: four of the rows' scales, eight of the weights'
+                            if (2 * k < steps) {
                                 copy_scales<2>(sf + 12 * k, xs + k * (kTileBytes / 16));
                                 copy_scales<2>(sf + 12 * k + 4, ws + k * (kTileBytes / 16));
                                 if (two) copy_scales<2>(sf + 12 * k + 8, ws + (2 + k) * (kTileBytes / 16));
@@ -631,14 +670,15 @@ __global__ void __launch_bounds__(RingP::threads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (j < steps)
-                                mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + 4 + col0,
+                                mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + col0,
                                             !first || j != 0);
-                        commit<2>(empty + s);
+                        commit<2>(done);
                         if (last) commit<2>(acc_full + (ac & 1));
                     }
                     __syncwarp();
+                    ready = __all_sync(0xFFFFFFFFu, seen);
+                    sf ^= (tmem + T::sf_col) ^ (tmem + T::sf_col + T::sf_cols);
                     if (last) ++ac;
-                    if (++s == S) { s = 0; ph ^= 1; }
                 }
             }
             if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }

@@ -307,27 +307,34 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_backward_kernel(cons
         }
 }
 
-// dw[c] = (dw[c] +) the sum of part[i][c] over i: 32 columns per CTA, its warps a share of the parts each, joined in order.
-__global__ void __launch_bounds__(256)
+// dw[c] = (dw[c] +) the sum of part[i][c] over i: 32 columns per CTA, each of its 32 warps a share of the parts (all
+// loads in flight), the shares joined in order. Bound by the latency of two rounds of loads: 608 parts of 2048 columns
+// take 3 us; with eight warps a CTA they took 9.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps)
     norm_weight_kernel(const float *__restrict__ part, int parts, int H, float *__restrict__ dw, int accumulate)
 {
-    __shared__ float sum[8][32];
+    __shared__ float sum[kJoinWarps][32];
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    float a[4] = {};
-    if (c < H) {
-        int i = warp;
-        for (; i + 24 < parts; i += 32)
+    float s = 0.f;
+    if (c < H)
+        for (int i0 = warp; i0 < parts; i0 += 16 * kJoinWarps) {
+            float v[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] += part[(int64_t)(i + 8 * k) * H + c];
-        for (; i < parts; i += 8) a[0] += part[(int64_t)i * H + c];
-    }
-    sum[warp][lane] = (a[0] + a[1]) + (a[2] + a[3]);
+            for (int k = 0; k < 16; ++k) {
+                const int i = i0 + k * kJoinWarps;
+                v[k] = i < parts ? part[(int64_t)i * H + c] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) s += v[k];
+        }
+    sum[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < H) {
-        float s = 0.f;
+        s = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += sum[k][lane];
+        for (int k = 0; k < kJoinWarps; ++k) s += sum[k][lane];
         dw[c] = accumulate ? dw[c] + s : s;
     }
 }
@@ -410,7 +417,7 @@ cudaError_t launch_rmsnorm_backward(NormBackParams p, float *dw, int accumulate,
     p.part = dw ? static_cast<float *>(workspace) : nullptr;
     const cudaError_t e = p.total_f32 ? launch_back_sized<true>(p, vec, grid, s) : launch_back_sized<false>(p, vec, grid, s);
     if (e != cudaSuccess || !dw) return e;
-    FT_LAUNCH(norm_weight_kernel, dim3((p.H + 31) / 32), dim3(256), 0, s, (const float *)p.part, grid, p.H, dw, accumulate);
+    FT_LAUNCH(norm_weight_kernel, dim3((p.H + 31) / 32), dim3(32 * kJoinWarps), 0, s, (const float *)p.part, grid, p.H, dw, accumulate);
     count_launches(1);
     return cudaGetLastError();
 }
