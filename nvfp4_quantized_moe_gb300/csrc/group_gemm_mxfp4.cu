@@ -574,30 +574,32 @@ __global__ void __launch_bounds__(RingP::threads, 1)
         if (warp == 0 && !p.skip_producer) {
             // -------------------------------------------------------- producer
             const bool one = elect_one();
+            const uint32_t full0 = map_rank(full, 0);
             int s = 0, it = 0;
             uint32_t ph = 1;
+            bool ready = false;
             for (Unit4 x; !dead && ring.get(x, dead);) {
-                const bool rows[2] = {x.hi > 0, x.hi > kTileM};         // whether a CTA has rows
-                const uint32_t bytes = 2 * (T::b_bytes + T::b_sf) + ((int)rows[0] + (int)rows[1]) * (kABytes + T::a_sf);
-                const int ws_tile = x.e * nt128 + x.n0 / 128, row = x.row0 + (int)rank * kTileM;
+                const int mine = x.hi - (int)rank * kTileM;  // rows of this CTA, if positive
+                const uint32_t bytes = 2 * (T::b_bytes + T::b_sf) + (x.hi > kTileM ? 2 : 1) * (kABytes + T::a_sf);
+                const int ws_tile = x.e * nt128 + x.n0 / 128, row = x.row0 + (int)rank * kTileM, n0 = x.n0 + (int)rank * (x.cols / 2);
                 const bool whole = row + kTileM <= p.P / 4 * 4 || p.P % 4 == 0;
                 for (int b = 0; b < nb; ++b, ++it) {
-                    if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
+                    if (!ready && !warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes, *sf = sb + T::b_bytes;
-                    const uint32_t bar = map_rank(full + s, 0);
+                    const uint32_t bar = full0 + 8 * s;
                     if (one) {
                         if (leader) mbar_arrive_expect_tx(full + s, bytes);
-                        load_3d<2>(sb, &map_w, b * kChunkBytes, x.n0 + (int)rank * (x.cols / 2), x.e, bar);
-                        load_3d<2>(sf + T::a_sf, &map_ws, 0, 2 * b, ws_tile, bar);
-                        if (rows[rank]) {
-                            load_2d<2>(sf, &map_xs, row, 2 * b, bar);
+                        load_3d<2>(sb, &map_w, b * kChunkBytes, n0, x.e, bar);
+                        if (mine > 0) {
                             if (whole) load_3d<2>(sa, &map_x, b * kChunkBytes, row / 4, 0, bar);
                             else
                                 for (int j = 0; j < 4; ++j) load_2d<2>(sa + j * 32 * kChunkBytes, &map_x_end, b * kChunkBytes, row + j, bar);
+                            load_2d<2>(sf, &map_xs, row, 2 * b, bar);
                         }
+                        load_3d<2>(sf + T::a_sf, &map_ws, 0, 2 * b, ws_tile, bar);
                     }
-                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
+                    ready = __all_sync(0xFFFFFFFFu, test_cluster(empty + s, ph));
                 }
             }
             // The last stages' MMAs also arrive in the other CTA: neither leaves before all have.
@@ -623,63 +625,75 @@ __global__ void __launch_bounds__(RingP::threads, 1)
             int s = 0, ac = 0;
             uint32_t ph = 0, sf = tmem + T::sf_col;
             bool ready = false;
-            for (Unit4 x; !dead && ring.get(x, dead);) {
-                const uint32_t idesc[2] = {idesc_mxf4(2 * kTileM, x.cols, 0), idesc_mxf4(2 * kTileM, x.cols, 1)};
-                const bool two = x.n0 % 128 + x.cols > 128;
-                const uint32_t col0 = 4 + x.n0 % 128 / 32;  // of the unit's first weight row in its tile's scales
-                for (int b = 0; b < nb; ++b) {
-                    const int in_part = F32 ? b % kPart4 : b;
-                    const bool first = in_part == 0, last = b + 1 == nb || (F32 && in_part == kPart4 - 1);
-                    if ((first && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) ||
-                        (!ready && !warp_wait(full + s, ph, abort_flag, wl))) {
-                        dead = true;
-                        break;
-                    }
-                    tc::fence_after_sync();
-                    const uint32_t at = (uint32_t)s * (T::stage / 16);
-                    const uint64_t ad = a0 + at, bd = b0 + at, xs = f0 + at, ws = xs + T::a_sf / 16;
-                    const uint32_t d = tmem + (uint32_t)(ac & 1) * BN;
-                    uint64_t *done = empty + s;
-                    if (++s == S) { s = 0; ph ^= 1; }
-                    const bool seen = test_cluster(full + s, ph);
-                    // columns: four of the rows' scales, eight of the weights', for each 128 steps
-                    if (b < whole) {
-                        if (one) {
+            Unit4 x = {};
+            uint32_t idesc[2] = {}, col0 = 0;
+            bool two = false;
+            auto enter = [&]() {
+                idesc[0] = idesc_mxf4(2 * kTileM, x.cols, 0);
+                idesc[1] = idesc_mxf4(2 * kTileM, x.cols, 1);
+                two = x.n0 % 128 + x.cols > 128;
+                col0 = 4 + x.n0 % 128 / 32;  // of the unit's first weight row in its tile's scales
+            };
+            auto stage = [&](int b, bool end) {
+                const int in_part = F32 ? b % kPart4 : b;
+                const bool first = in_part == 0, last = end || (F32 && in_part == kPart4 - 1);
+                if ((first && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) ||
+                    (!ready && !warp_wait(full + s, ph, abort_flag, wl))) {
+                    dead = true;
+                    return;
+                }
+                tc::fence_after_sync();
+                const uint32_t at = (uint32_t)s * (T::stage / 16);
+                const uint64_t ad = a0 + at, bd = b0 + at, xs = f0 + at, ws = xs + T::a_sf / 16;
+                const uint32_t d = tmem + (uint32_t)(ac & 1) * BN;
+                uint64_t *done = empty + s;
+                if (++s == S) { s = 0; ph ^= 1; }
+                const bool seen = test_cluster(full + s, ph);
+                // columns: four of the rows' scales, eight of the weights', for each 128 steps
+                if (b < whole) {
+                    if (one) {
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                copy_scales<2>(sf + 12 * k, xs + k * (kTileBytes / 16));
-                                copy_scales<2>(sf + 12 * k + 4, ws + k * (kTileBytes / 16));
-                                if (two) copy_scales<2>(sf + 12 * k + 8, ws + (2 + k) * (kTileBytes / 16));
-                            }
-                            mma_mxf4<2>(d, ad, bd, idesc[0], sf, sf + col0, !first);
-#pragma unroll
-                            for (int j = 1; j < 4; ++j)
-                                mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + col0, 1);
-                            commit<2>(done);
-                            if (last) commit<2>(acc_full + (ac & 1));
+                        for (int k = 0; k < 2; ++k) {
+                            copy_scales<2>(sf + 12 * k, xs + k * (kTileBytes / 16));
+                            copy_scales<2>(sf + 12 * k + 4, ws + k * (kTileBytes / 16));
+                            if (two) copy_scales<2>(sf + 12 * k + 8, ws + (2 + k) * (kTileBytes / 16));
                         }
-                    } else if (one) {
-                        const int steps = (p.K - b * kStep4 + 63) / 64;  // instructions that have something to multiply
+                        mma_mxf4<2>(d, ad, bd, idesc[0], sf, sf + col0, !first);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (2 * k < steps) {
-                                copy_scales<2>(sf + 12 * k, xs + k * (kTileBytes / 16));
-                                copy_scales<2>(sf + 12 * k + 4, ws + k * (kTileBytes / 16));
-                                if (two) copy_scales<2>(sf + 12 * k + 8, ws + (2 + k) * (kTileBytes / 16));
-                            }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (j < steps)
-                                mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + col0,
-                                            !first || j != 0);
+                        for (int j = 1; j < 4; ++j)
+                            mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + col0, 1);
                         commit<2>(done);
                         if (last) commit<2>(acc_full + (ac & 1));
                     }
-                    __syncwarp();
-                    ready = __all_sync(0xFFFFFFFFu, seen);
-                    sf ^= (tmem + T::sf_col) ^ (tmem + T::sf_col + T::sf_cols);
-                    if (last) ++ac;
+                } else if (one) {
+                    const int steps = (p.K - b * kStep4 + 63) / 64;  // instructions that have something to multiply
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (2 * k < steps) {
+                            copy_scales<2>(sf + 12 * k, xs + k * (kTileBytes / 16));
+                            copy_scales<2>(sf + 12 * k + 4, ws + k * (kTileBytes / 16));
+                            if (two) copy_scales<2>(sf + 12 * k + 8, ws + (2 + k) * (kTileBytes / 16));
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < steps)
+                            mma_mxf4<2>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sf + 12 * (j >> 1), sf + 12 * (j >> 1) + col0,
+                                        !first || j != 0);
+                    commit<2>(done);
+                    if (last) commit<2>(acc_full + (ac & 1));
                 }
+                __syncwarp();
+                ready = __all_sync(0xFFFFFFFFu, seen);
+                sf ^= (tmem + T::sf_col) ^ (tmem + T::sf_col + T::sf_cols);
+                if (last) ++ac;
+            };
+            bool more = ring.get(x, dead);
+            while (more && !dead) {
+                enter();
+                for (int b = 0; b + 1 < nb && !dead; ++b) stage(b, false);
+                // (before the last stage, so that there is nothing to look up between two units)
+                if (!dead) more = ring.get(x, dead);
+                if (!dead) stage(nb - 1, true);
             }
             if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
         } else if (warp == 2) {
