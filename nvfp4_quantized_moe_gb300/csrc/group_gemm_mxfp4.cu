@@ -268,11 +268,12 @@ __global__ void __launch_bounds__(kThreads4, 1)
             const bool one = elect_one();
             int s = 0, it = 0;
             uint32_t ph = 1;
+            bool ready = false;
             for (Unit4 x; !dead && ring.get(x, dead);) {
                 const int boxes = (x.cols + T::box_rows - 1) / T::box_rows;
                 const uint8_t *ws = p.ws + ((int64_t)x.e * m_tiles + x.n0 / kTileM) * kt * kTileBytes;
                 for (int b = b0; b < nb; ++b, ++it) {
-                    if (!warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
+                    if (!ready && !warp_wait(empty + s, ph, abort_flag, wl)) { dead = true; break; }
                     unsigned char *sa = smem + s * T::stage, *sb = sa + kABytes;
                     const uint32_t bar = smem_u32(full + s);
                     const uint32_t sf = min(kt - 2 * b, 2) * kTileBytes;  // (the last stage may have one word a row)
@@ -283,8 +284,8 @@ __global__ void __launch_bounds__(kThreads4, 1)
                         for (int i = 0; i < boxes; ++i)
                             load_2d<1>(sb + i * T::box_rows * kChunkBytes, &map_x, b * kChunkBytes, x.row0 + i * T::box_rows, bar);
                     }
-                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1; }
+                    ready = __all_sync(0xFFFFFFFFu, test_cluster(empty + s, ph));
                 }
             }
             if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
@@ -296,43 +297,72 @@ __global__ void __launch_bounds__(kThreads4, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
+        // (The next stage's barriers are looked at before this stage's instructions are issued, and a whole stage's have
+        // no conditions: see the wide tiles below.)
         const bool one = elect_one();
-        int s = 0, ac = 0, it = 0;
-        uint32_t ph = 0;
-        for (Unit4 x; !dead && ring.get(x, dead);) {
-            const uint32_t idesc[2] = {idesc_mxf4(kTileM, x.cols, 0), idesc_mxf4(kTileM, x.cols, 1)};
-            for (int b = b0; b < nb; ++b, ++it) {
-                const int in_part = F32 ? (b - b0) % kPart4 : b - b0;
-                const bool first = in_part == 0, last = b + 1 == nb || (F32 && in_part == kPart4 - 1);
-                if ((first && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) ||
-                    !warp_wait(full + s, ph, abort_flag, wl) || !warp_wait(sc_full + s, ph, abort_flag, wl)) {
-                    dead = true;
-                    break;
-                }
-                tc::fence_after_sync();
-                const uint32_t sa = smem_u32(smem + s * T::stage), sf = sa + kABytes + T::b_bytes;
-                const uint64_t ad = tc::sw128_desc(sa), bd = tc::sw128_desc(sa + kABytes), sd = scale_desc(sf);
-                const uint32_t d = tmem + (uint32_t)(ac & 1) * BN, sfa = tmem + T::sf_col + (it & 1) * 16, sfb = sfa + 8;
-                const int steps = min((p.K - b * kStep4 + 63) / 64, 4);  // instructions that have something to multiply
+        const uint32_t base = smem_u32(smem);
+        const uint64_t a0 = tc::sw128_desc(base), bd0 = tc::sw128_desc(base + kABytes), f0 = scale_desc(base + kABytes + T::b_bytes);
+        const int whole = p.K / kStep4;  // stages with four instructions
+        int s = 0, ac = 0;
+        uint32_t ph = 0, sfa = tmem + T::sf_col;
+        bool ready = false;
+        Unit4 x = {};
+        uint32_t idesc[2] = {};
+        auto stage = [&](int b, bool end) {
+            const int in_part = F32 ? (b - b0) % kPart4 : b - b0;
+            const bool first = in_part == 0, last = end || (F32 && in_part == kPart4 - 1);
+            if ((first && !warp_wait(acc_empty + (ac & 1), ((ac >> 1) & 1) ^ 1, abort_flag, wl)) ||
+                (!ready && (!warp_wait(full + s, ph, abort_flag, wl) || !warp_wait(sc_full + s, ph, abort_flag, wl)))) {
+                dead = true;
+                return;
+            }
+            tc::fence_after_sync();
+            const uint32_t at = (uint32_t)s * (T::stage / 16);
+            const uint64_t ad = a0 + at, bd = bd0 + at, sd = f0 + at;
+            const uint32_t d = tmem + (uint32_t)(ac & 1) * BN, sfb = sfa + 8;
+            uint64_t *done = empty + s;
+            if (++s == S) { s = 0; ph ^= 1; }
+            const bool seen = test_cluster(full + s, ph) && test_cluster(sc_full + s, ph);
+            if (b < whole) {
                 if (one) {
                     copy_scales<1>(sfa, sd);
                     copy_scales<1>(sfb, sd + T::sf_bytes / 16);
-                    if (steps > 2) {
-                        copy_scales<1>(sfa + 4, sd + kTileBytes / 16);
-                        copy_scales<1>(sfb + 4, sd + (T::sf_bytes + kTileBytes) / 16);
-                    }
+                    copy_scales<1>(sfa + 4, sd + kTileBytes / 16);
+                    copy_scales<1>(sfb + 4, sd + (T::sf_bytes + kTileBytes) / 16);
+                    mma_mxf4<1>(d, ad, bd, idesc[0], sfa, sfb, !first);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < steps)
-                            mma_mxf4<1>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sfa + 4 * (j >> 1), sfb + 4 * (j >> 1),
-                                        !first || j != 0);
-                    commit<1>(empty + s);
+                    for (int j = 1; j < 4; ++j)
+                        mma_mxf4<1>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sfa + 4 * (j >> 1), sfb + 4 * (j >> 1), 1);
+                    commit<1>(done);
                     if (last) commit<1>(acc_full + (ac & 1));
                 }
-                __syncwarp();
-                if (last) ++ac;
-                if (++s == S) { s = 0; ph ^= 1; }
+            } else if (one) {
+                const int steps = (p.K - b * kStep4 + 63) / 64;  // instructions that have something to multiply
+                copy_scales<1>(sfa, sd);
+                copy_scales<1>(sfb, sd + T::sf_bytes / 16);
+                if (steps > 2) {
+                    copy_scales<1>(sfa + 4, sd + kTileBytes / 16);
+                    copy_scales<1>(sfb + 4, sd + (T::sf_bytes + kTileBytes) / 16);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < steps)
+                        mma_mxf4<1>(d, ad + 2 * j, bd + 2 * j, idesc[j & 1], sfa + 4 * (j >> 1), sfb + 4 * (j >> 1), !first || j != 0);
+                commit<1>(done);
+                if (last) commit<1>(acc_full + (ac & 1));
             }
+            __syncwarp();
+            ready = __all_sync(0xFFFFFFFFu, seen);
+            sfa ^= (tmem + T::sf_col) ^ (tmem + T::sf_col + 16);
+            if (last) ++ac;
+        };
+        bool more = ring.get(x, dead);
+        while (more && !dead) {
+            idesc[0] = idesc_mxf4(kTileM, x.cols, 0);
+            idesc[1] = idesc_mxf4(kTileM, x.cols, 1);
+            for (int b = b0; b + 1 < nb && !dead; ++b) stage(b, false);
+            if (!dead) more = ring.get(x, dead);
+            if (!dead) stage(nb - 1, true);
         }
         if (dead && lane == 0) { raise_status(p.status, FT_ERR_TIMEOUT); *abort_flag = 1; }
     } else if (warp < 4) {
