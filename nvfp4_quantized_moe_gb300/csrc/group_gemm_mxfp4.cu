@@ -907,9 +907,16 @@ cudaError_t launch_group_gemm_mxfp4(const GroupGemm4 &g, cudaStream_t s)
     p.vec = g.N % (g.out_f32 ? 4 : 8) == 0 && g.ld_out % (g.out_f32 ? 4 : 8) == 0;
     p.status = g.status;
     injected_stall(&p.wait_ns, &p.skip_producer);
-    const int64_t per = g.P / (g.E < g.P ? g.E : g.P);
-    const int64_t pairs = (int64_t)(g.N + RingP::BN - 1) / RingP::BN * (g.P / 256 + (g.E < g.P ? g.E : g.P));
-    const int bn = per <= 24 ? 32 : per < 128 || g.N <= kTileM || 4 * pairs < sm_count() ? 128 : 256;
+    // The tile, by the rows per expert that has any. Measured on 256 experts of 1024 x 2048 (us, with 32 or 128 rows
+    // along N / 256 rows along M): 16 rows 50 / 50 / 57, 32 rows 51 / 52 / 59, 96 rows 92 / 59 / 64, 128 rows 118 / 65 /
+    // 67, 160 rows 142 / 78 / 70, 256 rows 217 / 96 / 92. The wide tiles need two and a half rounds of units to be the
+    // better ones (one expert, 4096 rows: of 1024 x 4096, 102 units, 13.9 / 15.2; 2048 rows of 4096 x 4096, 198 units,
+    // 23.5 / 20.3), and small tiles are as long as they all run at once (one expert of 2048 x 2048: 256 rows 6.4 / 9.0 /
+    // 7.7).
+    const int64_t touched = g.E < g.P ? g.E : g.P, per = g.P / touched;
+    const int64_t small = (int64_t)((g.N + kTileM - 1) / kTileM) * (g.P / 32 + touched);
+    const int64_t pairs = (int64_t)((g.N + RingP::BN - 1) / RingP::BN) * (g.P / 256 + touched);
+    const int bn = per <= 24 || small <= sm_count() ? 32 : per < 144 || 4 * pairs < 5 * sm_count() ? 128 : 256;
     if (g.plan && bn == 256) {
         write_plan(g.plan, 2, bn, 1, false);
         return cudaSuccess;

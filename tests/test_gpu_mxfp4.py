@@ -163,9 +163,10 @@ GROUPS = [
     ([1], 128, 32), ([1], 128, 256), ([3], 130, 96), ([1], 2048, 2048), ([8], 1024, 4096), ([31, 0, 2], 200, 544),
     ([0, 5, 0, 1, 17, 0], 257, 320), ([16, 24, 33], 640, 512), ([100, 0, 3, 250], 384, 672), ([129], 96, 1024),
     ([300], 256, 2048), ([1, 700, 64], 1000, 288), ([513, 511], 512, 512), ([2000, 100], 776, 256), ([1] * 40, 256, 544),
+    ([33, 70, 0, 129, 51] * 8, 300, 288), ([31, 64, 65] * 12, 257, 544), ([128, 127, 1] * 20, 136, 64),
     # by pairs of CTAs: first rows at every remainder of four, tiles that end one before, at and behind their last row
-    ([301, 0, 258, 3, 1023, 130], 1000, 544), ([255, 257, 256, 1, 511], 1213, 96), ([700, 640], 3000, 2112), ([5000], 520, 288),
-    ([129] * 20, 264, 320), ([253, 254, 255, 256, 257, 258, 259], 1984, 128), ([9000, 1], 192, 64),
+    ([301, 0, 258, 3, 1023, 130], 3100, 544), ([255, 257, 256, 1, 511], 3700, 96), ([1500, 1340], 3000, 2112), ([17000], 520, 288),
+    ([145] * 64, 264, 320), ([253, 254, 255, 256, 257, 258, 259], 2752, 128), ([60000, 1], 192, 64),
 ]
 
 

@@ -194,6 +194,52 @@ def test_no_rows(ft):
     assert (dw == 0).all()
 
 
+def test_streams_and_replays(ft):
+    """On a stream of its own, and captured into two graphs with a workspace each that are replayed at once after the inputs
+    changed: the results of calls on the new inputs."""
+    rows, H = 700, 640
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x, r, dy = _rows(gen, rows, H, 0), _rows(gen, rows, H, 0), _rows(gen, rows, H, 0)
+    w = torch.randn(H, generator=gen, device="cuda")
+
+    class Run:
+        def __init__(self):
+            self.total, self.y, self.dx = (torch.zeros((rows, H), dtype=BF, device="cuda") for _ in range(3))
+            self.rstd, self.dw = torch.zeros(rows, device="cuda"), torch.zeros(H, device="cuda")
+            self.ws = torch.zeros(ft.ft_moe_rmsnorm_workspace_size(rows, H), dtype=torch.uint8, device="cuda")
+
+        def __call__(self, stream=None):
+            ft.ft_moe_rmsnorm(x, w, EPS, y=self.y, residual=r, total=self.total, rstd=self.rstd, stream=stream)
+            ft.ft_moe_rmsnorm_backward(dy, self.total, w, self.rstd, self.dx, self.ws, dw=self.dw, stream=stream)
+
+        def same(self, other):
+            return all(torch.equal(getattr(self, n), getattr(other, n)) for n in ("total", "y", "dx", "rstd", "dw"))
+
+    plain, aside, side = Run(), Run(), torch.cuda.Stream()
+    plain()
+    torch.cuda.synchronize()
+    aside(side)
+    side.synchronize()
+    assert aside.same(plain)
+    runs, graphs = [Run(), Run()], []
+    for run in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    for t in (x, r, dy):
+        t.copy_(_rows(gen, rows, H, 0))
+    plain()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(run.same(plain) for run in runs)
+
+
 def test_more_than_2_31_elements(ft):
     """Rows behind 2^31 elements: the last rows come out as the first ones."""
     rows, H = (1 << 31) // 16384 + 8, 16384

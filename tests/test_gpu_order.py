@@ -249,6 +249,48 @@ def test_nothing_to_do(ft):
     assert (rows == 0).all()
 
 
+@pytest.mark.parametrize("T", [100, 1500])  # positions by one CTA, and cleared before the launch
+def test_streams_and_replays(ft, T):
+    """On a stream of its own, and captured and replayed after the routing changed: the results of calls on the new one."""
+    k, E, H = 4, 16, 520
+    gen = _gen(T)
+    x, dout = torch.randn((T, H), generator=gen, device="cuda").bfloat16(), torch.randn((T, H), generator=gen, device="cuda")
+    w = torch.rand((T, k), generator=gen, device="cuda")
+    slot, _ = _order(gen, T, k, E)
+
+    class Run:
+        def __init__(self):
+            self.xs, self.dy = (torch.zeros((T * k, H), dtype=BF, device="cuda") for _ in range(2))
+            self.pos, self.row_w = torch.zeros((T, k), dtype=I32, device="cuda"), torch.zeros(T * k, device="cuda")
+            self.out, self.dx = torch.zeros((T, H), device="cuda"), torch.zeros((T, H), dtype=BF, device="cuda")
+            self.dw, self.dw2 = torch.zeros((T, k), device="cuda"), torch.zeros((T, k), device="cuda")
+
+        def __call__(self, stream=None):
+            ft.ft_moe_dispatch(x, slot, k, self.xs, w=w, row_w=self.row_w, pos=self.pos, stream=stream)
+            ft.ft_moe_combine(self.xs, self.pos, w, self.out, stream=stream)
+            ft.ft_moe_combine_backward(dout, self.xs, self.pos, w, self.dy, dw=self.dw, stream=stream)
+            ft.ft_moe_dispatch_backward(self.dy, self.pos, self.dx, drow_w=self.row_w, dw=self.dw2, stream=stream)
+
+        def same(self, other):
+            return all(torch.equal(a, b) for a, b in zip(vars(self).values(), vars(other).values()))
+
+    plain, aside, side = Run(), Run(), torch.cuda.Stream()
+    plain()
+    torch.cuda.synchronize()
+    aside(side)
+    side.synchronize()
+    assert aside.same(plain)
+    run, g = Run(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    slot.copy_(_order(gen, T, k, E)[0])
+    plain()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert run.same(plain)
+
+
 def test_more_than_2_31_elements(ft):
     """The sorted rows behind 2^31 elements of a wide batch, there and back."""
     T, k, H = (1 << 20) // 8 + 16, 8, 2048
