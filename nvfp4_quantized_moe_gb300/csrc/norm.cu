@@ -206,7 +206,7 @@ __device__ __forceinline__ void open8(const Raw8<F32> &r, float (&v)[8])
 // weight's gradient adds up in registers; the CTAs' sums go to the workspace [gridDim][H] and
 // norm_weight_kernel adds them in order. The next rows' loads are in flight while these are worked on.
 template <int TPR, int NV, bool F32, bool VEC>
-__global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_backward_kernel(const __grid_constant__ NormBackParams p)
+__global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rmsnorm_backward_kernel(const __grid_constant__ NormBackParams p)
 {
     constexpr int kRows = cta_threads(TPR) / TPR;
     extern __shared__ float sh_sum[];  // [kRows - 1][H] where several rows share a CTA
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_backward_kernel(cons
     const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
     const int H = p.H;
     float acc[NV][8] = {};
+    constexpr bool kAhead = !F32;  // (an fp32 dtotal has no registers to wait in: loaded where its row's sum begins)
     Raw8<F32> total[NV] = {}, past[NV] = {};
     Raw8<false> dy[NV] = {};
     float rstd = 0.f;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_backward_kernel(cons
             if (c < H) {
                 fetch8<F32, VEC>(sr, c, H, total[i]);
                 fetch8<false, VEC>(dr, c, H, dy[i]);
-                if (p.dtotal) fetch8<F32, VEC>(pr, c, H, past[i]);
+                if (kAhead && p.dtotal) fetch8<F32, VEC>(pr, c, H, past[i]);
             }
         }
     };
@@ -241,8 +242,9 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_backward_kernel(cons
         const int64_t row = row0 + team;
         const bool live = row < p.rows;
         char *out = static_cast<char *>(p.dx) + row * p.ld_dx * (F32 ? 4 : 2);
+        const char *pr = static_cast<const char *>(p.dtotal) + row * p.ld_dtotal * (F32 ? 4 : 2);
         float n[NV][8], g[NV][8];
-        Raw8<F32> ds[NV];
+        Raw8<F32> ds[NV] = {};
         const float r = rstd;
         float dot = 0.f;
 #pragma unroll
@@ -250,7 +252,8 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_backward_kernel(cons
             const int c = 8 * (t + i * TPR);
             open8(total[i], n[i]);
             open8(dy[i], g[i]);
-            ds[i] = past[i];
+            if (kAhead) ds[i] = past[i];
+            else if (live && c < H && p.dtotal) fetch8<F32, VEC>(pr, c, H, ds[i]);
             if (live && c < H) {
                 float w[8];
                 gain8<VEC>(p.w, p.w_f32, p.offset, c, H, w);

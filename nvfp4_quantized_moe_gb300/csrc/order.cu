@@ -26,6 +26,9 @@ namespace {
 constexpr int kOrderThreads = 256;
 // Up to this many slots one CTA clears and fills pos by itself; above, a memset goes before the launch.
 constexpr int kPosByOneCta = 2048;
+// Sorted rows beyond this many bytes, which L2 cannot hold, leave as streaming stores: 65536 rows of 4 KB 52.7 us,
+// as plain ones 58.2.
+constexpr int64_t kStreamBytes = 100 << 20;
 
 __device__ __forceinline__ int rows_of(const DispatchParams &p)
 {
@@ -56,12 +59,21 @@ __global__ void __launch_bounds__(kOrderThreads) dispatch_kernel(const __grid_co
                 if (p.pos && in) atomicMax(p.pos + s, r);
                 if (p.row_w) p.row_w[r] = in ? __ldg(p.w + s) : 0.f;
             }
-        // block scales: a thread per scale, those of a block of columns side by side
-        for (int64_t i = me; i < (int64_t)p.blocks * p.P; i += threads) {
-            const int b = (int)(i / p.P), r = (int)(i - (int64_t)b * p.P);
+        // block scales: a thread takes up to eight blocks of a row, all loads in flight; neighbours take neighbouring rows
+        const int groups = (p.blocks + 7) / 8;
+        for (int64_t i = me; i < (int64_t)groups * p.P; i += threads) {
+            const int g = (int)(i / p.P), r = (int)(i - (int64_t)g * p.P);
             if (r >= n) continue;
             const int s = __ldg(p.slot + r);
-            p.out_scale[b * p.ld_os + r] = s >= 0 && s < slots ? __ldg(p.x_scale + b * p.ld_xs + s / p.k) : 0u;
+            const bool in = s >= 0 && s < slots;
+            const uint32_t *from = p.x_scale + (int64_t)8 * g * p.ld_xs + (in ? s / p.k : 0);
+            uint32_t *to = p.out_scale + (int64_t)8 * g * p.ld_os + r;
+            uint32_t v[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) v[b] = in && 8 * g + b < p.blocks ? __ldg(from + b * p.ld_xs) : 0u;
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+                if (8 * g + b < p.blocks) to[b * p.ld_os] = v[b];
         }
         return;
     }
@@ -83,77 +95,10 @@ __global__ void __launch_bounds__(kOrderThreads) dispatch_kernel(const __grid_co
         }
 #pragma unroll
         for (int i = 0; i < kUnits; ++i)
-            if (c0 + 32 * i < pieces) to[c0 + 32 * i] = v[i];
-    }
-}
-
-// Combine, and the backward of dispatch (no weights): one token per CTA and step, 8 columns per thread (or one
-// where rows are not made of 16-byte pieces), the loads of up to 8 rows in flight together.
-template <bool YF32, bool OF32, bool VEC>
-__global__ void __launch_bounds__(kOrderThreads) combine_rows_kernel(const __grid_constant__ CombineParams p)
-{
-    constexpr int W = VEC ? 8 : 1;
-    pdl_enter();
-    const int64_t t = blockIdx.x;
-    const int *pos = p.pos + t * p.k;
-    const float *w = p.w ? p.w + t * p.k : nullptr;
-    if (p.dw && blockIdx.y == 0 && (int)threadIdx.x < p.k) {
-        const int r = __ldg(pos + threadIdx.x);
-        p.dw[t * p.k + threadIdx.x] = r >= 0 && r < p.P ? __ldg(p.drow_w + r) : 0.f;
-    }
-    const int c = W * (blockIdx.y * kOrderThreads + threadIdx.x);
-    if (c >= p.H) return;
-    float acc[W] = {};
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-        float v[8][W], f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] = 0.f;
-            if (j0 + j < p.k) {
-                const int r = __ldg(pos + j0 + j);
-                if (r >= 0 && r < p.P) {
-                    f[j] = w ? __ldg(w + j0 + j) : 1.f;
-                    const char *row = static_cast<const char *>(p.y) + r * p.ld_y * (YF32 ? 4 : 2);
-                    if constexpr (VEC) load8<YF32>(row, c, v[j]);
-                    else v[j][0] = YF32 ? __ldg(reinterpret_cast<const float *>(row) + c)
-                                        : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + c) << 16);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) v[j][i] = 0.f;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < W; ++i) v[j][i] = 0.f;
+            if (c0 + 32 * i < pieces) {
+                if (p.stream) __stcs(to + c0 + 32 * i, v[i]);
+                else to[c0 + 32 * i] = v[i];
             }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] = fmaf(f[j], v[j][i], acc[i]);
-    }
-    const int size = OF32 ? 4 : 2;
-    char *out = static_cast<char *>(p.out) + t * p.ld_out * size;
-    if (p.add) {
-        const char *add = static_cast<const char *>(p.add) + t * p.ld_add * size;
-        float a[W];
-        if constexpr (VEC) load8<OF32>(add, c, a);
-        else a[0] = OF32 ? __ldg(reinterpret_cast<const float *>(add) + c)
-                         : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(add) + c) << 16);
-#pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] += a[i];
-    }
-    if constexpr (VEC) {
-        if constexpr (OF32) {
-            float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + c);
-            o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + c) = pack8(acc);
-        }
-    } else if constexpr (OF32) {
-        reinterpret_cast<float *>(out)[c] = acc[0];
-    } else {
-        reinterpret_cast<uint16_t *>(out)[c] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
     }
 }
 
@@ -190,6 +135,72 @@ struct Raw {
         }
     }
 };
+
+// Combine, and the backward of dispatch (no weights): one token per CTA, 8 columns per thread (or one where rows are not
+// made of 16-byte pieces), the loads of several rows in flight together. They stay as they lie in memory until all are
+// issued: widened to fp32 at once, eight rows took 90 registers a thread, and two CTAs an SM were too few (8192 tokens of
+// 2048 columns, top 8, bf16: 162 us).
+template <bool YF32, bool OF32, bool VEC>
+__global__ void __launch_bounds__(kOrderThreads) combine_rows_kernel(const __grid_constant__ CombineParams p)
+{
+    constexpr int W = VEC ? 8 : 1, J = YF32 ? 4 : 8;
+    pdl_enter();
+    const int64_t t = blockIdx.x;
+    const int *pos = p.pos + t * p.k;
+    const float *w = p.w ? p.w + t * p.k : nullptr;
+    if (p.dw && blockIdx.y == 0 && (int)threadIdx.x < p.k) {
+        const int r = __ldg(pos + threadIdx.x);
+        p.dw[t * p.k + threadIdx.x] = r >= 0 && r < p.P ? __ldg(p.drow_w + r) : 0.f;
+    }
+    const int c = W * (blockIdx.y * kOrderThreads + threadIdx.x);
+    if (c >= p.H) return;
+    float acc[W] = {};
+    for (int j0 = 0; j0 < p.k; j0 += J) {
+        Raw<YF32, VEC> v[J] = {};
+        float f[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            f[j] = 0.f;
+            if (j0 + j < p.k) {
+                const int r = __ldg(pos + j0 + j);
+                if (r >= 0 && r < p.P) {
+                    f[j] = w ? __ldg(w + j0 + j) : 1.f;
+                    v[j].load(static_cast<const char *>(p.y) + r * p.ld_y * (YF32 ? 4 : 2), c);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            float a[W];
+            v[j].open(a);
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] = fmaf(f[j], a[i], acc[i]);
+        }
+    }
+    const int size = OF32 ? 4 : 2;
+    char *out = static_cast<char *>(p.out) + t * p.ld_out * size;
+    if (p.add) {
+        Raw<OF32, VEC> add;
+        float a[W];
+        add.load(static_cast<const char *>(p.add) + t * p.ld_add * size, c);
+        add.open(a);
+#pragma unroll
+        for (int i = 0; i < W; ++i) acc[i] += a[i];
+    }
+    if constexpr (VEC) {
+        if constexpr (OF32) {
+            float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + c);
+            o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + c) = pack8(acc);
+        }
+    } else if constexpr (OF32) {
+        reinterpret_cast<float *>(out)[c] = acc[0];
+    } else {
+        reinterpret_cast<uint16_t *>(out)[c] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
+    }
+}
 
 // One warp per slot (neighbouring warps share a token, whose row then comes from L1).
 template <bool DF32, bool YF32, bool VEC>
@@ -259,6 +270,7 @@ cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s)
 {
     const int slots = p.T * p.k;
     p.clear = slots <= kPosByOneCta && p.P <= kPosByOneCta;
+    p.stream = (int64_t)p.P * p.row_bytes > kStreamBytes;
     if (p.pos && !p.clear) {
         const cudaError_t e = cudaMemsetAsync(p.pos, 0xFF, sizeof(int) * (size_t)slots, s);
         if (e != cudaSuccess) return e;
@@ -268,10 +280,10 @@ cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s)
     const int piece = vec ? 16 : 2, unit = vec ? 4 : 8;
     const int chunks = (p.row_bytes / piece + 32 * unit - 1) / (32 * unit);
     const int64_t want = ((int64_t)p.P * chunks + per - 1) / per, most = (int64_t)sm_count() * 32;
-    // CTAs for what is small: a thread per scale or slot, up to one CTA per SM
-    const int64_t items = (int64_t)p.P * (p.blocks > 0 ? p.blocks : 1), each = (items + kOrderThreads - 1) / kOrderThreads;
+    // CTAs for what is small: a thread per slot or eight scales, up to four CTAs per SM
+    const int64_t items = (int64_t)p.P * (p.blocks > 0 ? (p.blocks + 7) / 8 : 1), each = (items + kOrderThreads - 1) / kOrderThreads;
     p.small = 0;
-    if (p.pos || p.row_w || p.blocks) p.small = p.clear && !p.blocks ? 1 : (int)(each < sm_count() ? each : sm_count());
+    if (p.pos || p.row_w || p.blocks) p.small = p.clear && !p.blocks ? 1 : (int)(each < 4 * sm_count() ? each : 4 * sm_count());
     const unsigned grid = (unsigned)(want < most ? want : most) + p.small;
     if (vec) FT_LAUNCH(dispatch_kernel<uint4, 4>, dim3(grid), dim3(kOrderThreads), 0, s, p);
     else FT_LAUNCH(dispatch_kernel<uint16_t, 8>, dim3(grid), dim3(kOrderThreads), 0, s, p);
