@@ -301,8 +301,9 @@ struct CombineParams {
     const float *drow_w;
     float *dw;                              // may be null
     int T, k, P, H;
+    int team;                               // set by the launch
 };
-cudaError_t launch_combine_rows(const CombineParams &p, bool y_f32, bool out_f32, cudaStream_t s);
+cudaError_t launch_combine_rows(CombineParams p, bool y_f32, bool out_f32, cudaStream_t s);
 struct CombineBackParams {
     const void *dout, *y;
     void *dy;

@@ -42,25 +42,26 @@ __device__ __forceinline__ float row_sum(float v, float *red)
     return v;
 }
 
-// 8 values of a row from column c; VEC: 16-byte loads of whole vectors, else an element at a time up to H.
+// 8 values of a row: VEC: from column c on, by 16-byte loads; else an element at a time, `step` columns apart, up to H.
 template <bool F32, bool VEC>
-__device__ __forceinline__ void get8(const void *row, int c, int H, float (&v)[8])
+__device__ __forceinline__ void get8(const void *row, int c, int step, int H, float (&v)[8])
 {
     if constexpr (VEC) {
         load8<F32>(row, c, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            const int at = c + i * step;
             v[i] = 0.f;
-            if (c + i < H)
-                v[i] = F32 ? __ldg(static_cast<const float *>(row) + c + i)
-                           : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(row) + c + i) << 16);
+            if (at < H)
+                v[i] = F32 ? __ldg(static_cast<const float *>(row) + at)
+                           : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(row) + at) << 16);
         }
     }
 }
 
 template <bool F32, bool VEC>
-__device__ __forceinline__ void put8(void *row, int c, int H, const float (&v)[8])
+__device__ __forceinline__ void put8(void *row, int c, int step, int H, const float (&v)[8])
 {
     if constexpr (VEC) {
         if constexpr (F32) {
@@ -73,19 +74,19 @@ __device__ __forceinline__ void put8(void *row, int c, int H, const float (&v)[8
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < H) {
-                if (F32) static_cast<float *>(row)[c + i] = v[i];
-                else static_cast<uint16_t *>(row)[c + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+            if (c + i * step < H) {
+                if (F32) static_cast<float *>(row)[c + i * step] = v[i];
+                else static_cast<uint16_t *>(row)[c + i * step] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
             }
     }
 }
 
 // o + w for 8 columns.
 template <bool VEC>
-__device__ __forceinline__ void gain8(const void *w, bool f32, float offset, int c, int H, float (&g)[8])
+__device__ __forceinline__ void gain8(const void *w, bool f32, float offset, int c, int step, int H, float (&g)[8])
 {
-    if (f32) get8<true, VEC>(w, c, H, g);
-    else get8<false, VEC>(w, c, H, g);
+    if (f32) get8<true, VEC>(w, c, step, H, g);
+    else get8<false, VEC>(w, c, step, H, g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] += offset;
 }
@@ -105,15 +106,19 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_kernel(const __grid_
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     const bool live = row < p.rows;
     const int H = p.H;
+    // a thread's i-th eight columns: neighbouring ones, or (an element at a time) TPR apart, so that a warp's lie together
+    // (8-bit codes want neighbouring ones all the same)
+    const int step = VEC || p.codes ? 1 : TPR;
+    auto at = [&](int i) { return VEC || p.codes ? 8 * (t + i * TPR) : t + 8 * i * TPR; };
     float v[NV][8];
     float sq = 0.f;
     const uint16_t *xr = static_cast<const uint16_t *>(p.x) + row * p.ld_x;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (t + i * TPR);
+        const int c = at(i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        if (live && c < H) get8<false, VEC>(xr, c, H, v[i]);
+        if (live && c < H) get8<false, VEC>(xr, c, step, H, v[i]);
     }
     if constexpr (RES != 0) {
         constexpr bool F32 = RES == 2;
@@ -121,16 +126,16 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_kernel(const __grid_
         char *sr = static_cast<char *>(p.total) + row * p.ld_total * (F32 ? 4 : 2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (t + i * TPR);
+            const int c = at(i);
             if (live && c < H) {
                 float r[8];
-                get8<F32, VEC>(rr, c, H, r);
+                get8<F32, VEC>(rr, c, step, H, r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     v[i][j] += r[j];
                     if (!F32) v[i][j] = __bfloat162float(__float2bfloat16_rn(v[i][j]));
                 }
-                put8<F32, VEC>(sr, c, H, v[i]);
+                put8<F32, VEC>(sr, c, step, H, v[i]);
             }
         }
     }
@@ -142,15 +147,15 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_kernel(const __grid_
     if (live && t == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (t + i * TPR);
+        const int c = at(i);
         if (8 * (i * TPR) >= H) break;
         if (c < H) {
             float g[8];
-            gain8<VEC>(p.w, p.w_f32, p.offset, c, H, g);
+            gain8<VEC>(p.w, p.w_f32, p.offset, c, step, H, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * g[j];
         }
-        if (live && c < H && p.y) put8<false, VEC>(static_cast<uint16_t *>(p.y) + row * p.ld_y, c, H, v[i]);
+        if (live && c < H && p.y) put8<false, VEC>(static_cast<uint16_t *>(p.y) + row * p.ld_y, c, step, H, v[i]);
         if (p.codes) {  // 16 neighbouring threads hold a block of 128 columns (zero beyond the row)
             const float s = block_scale(v[i]);
             if (live && c < H) {
@@ -168,7 +173,7 @@ struct Raw8 {
 };
 
 template <bool F32, bool VEC>
-__device__ __forceinline__ void fetch8(const void *row, int c, int H, Raw8<F32> &r)
+__device__ __forceinline__ void fetch8(const void *row, int c, int step, int H, Raw8<F32> &r)
 {
     if constexpr (VEC) {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + c * (F32 ? 4 : 2));
@@ -176,7 +181,7 @@ __device__ __forceinline__ void fetch8(const void *row, int c, int H, Raw8<F32> 
         if constexpr (F32) r.q[1] = ldg_nc_v4(p + 1);
     } else {
         float v[8];
-        get8<F32, false>(row, c, H, v);
+        get8<F32, false>(row, c, step, H, v);
         if constexpr (F32) {
             r.q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
             r.q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
@@ -214,6 +219,8 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
     pdl_enter();
     const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
     const int H = p.H;
+    constexpr int step = VEC ? 1 : TPR;  // columns as in the forward kernel
+    auto at = [&](int i) { return VEC ? 8 * (t + i * TPR) : t + 8 * i * TPR; };
     float acc[NV][8] = {};
     constexpr bool kAhead = !F32;  // (an fp32 dtotal has no registers to wait in: loaded where its row's sum begins)
     Raw8<F32> total[NV] = {}, past[NV] = {};
@@ -227,18 +234,18 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
         rstd = __ldg(p.rstd + row);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (t + i * TPR);
+            const int c = at(i);
             if (c < H) {
-                fetch8<F32, VEC>(sr, c, H, total[i]);
-                fetch8<false, VEC>(dr, c, H, dy[i]);
-                if (kAhead && p.dtotal) fetch8<F32, VEC>(pr, c, H, past[i]);
+                fetch8<F32, VEC>(sr, c, step, H, total[i]);
+                fetch8<false, VEC>(dr, c, step, H, dy[i]);
+                if (kAhead && p.dtotal) fetch8<F32, VEC>(pr, c, step, H, past[i]);
             }
         }
     };
-    const int64_t step = (int64_t)gridDim.x * kRows;
+    const int64_t stride = (int64_t)gridDim.x * kRows;
     fetch((int64_t)blockIdx.x * kRows + team);
     int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < p.rows; row0 += step, turn ^= 1) {
+    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < p.rows; row0 += stride, turn ^= 1) {
         const int64_t row = row0 + team;
         const bool live = row < p.rows;
         char *out = static_cast<char *>(p.dx) + row * p.ld_dx * (F32 ? 4 : 2);
@@ -249,14 +256,14 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (t + i * TPR);
+            const int c = at(i);
             open8(total[i], n[i]);
             open8(dy[i], g[i]);
             if (kAhead) ds[i] = past[i];
-            else if (live && c < H && p.dtotal) fetch8<F32, VEC>(pr, c, H, ds[i]);
+            else if (live && c < H && p.dtotal) fetch8<F32, VEC>(pr, c, step, H, ds[i]);
             if (live && c < H) {
                 float w[8];
-                gain8<VEC>(p.w, p.w_f32, p.offset, c, H, w);
+                gain8<VEC>(p.w, p.w_f32, p.offset, c, step, H, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     n[i][j] *= r;
@@ -266,17 +273,17 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
                 }
             }
         }
-        fetch(row + step);
+        fetch(row + stride);
         const float mean = __fdiv_rn(row_sum<TPR>(dot, red[turn]), (float)H);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = 8 * (t + i * TPR);
+            const int c = at(i);
             if (live && c < H) {
                 float d[8];
                 open8(ds[i], d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) n[i][j] = fmaf(r, fmaf(-n[i][j], mean, g[i][j]), d[j]);
-                put8<F32, VEC>(out, c, H, n[i]);
+                put8<F32, VEC>(out, c, step, H, n[i]);
             }
         }
     }
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int c = 8 * (t + i * TPR) + j;
+                    const int c = at(i) + j * step;
                     if (c < H) sh_sum[(team - 1) * H + c] = acc[i][j];
                 }
         }
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int c = 8 * (t + i * TPR) + j;
+                const int c = at(i) + j * step;
                 for (int k = 0; c < H && k < kRows - 1; ++k) acc[i][j] += sh_sum[k * H + c];
             }
     }
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = 8 * (t + i * TPR) + j;
+            const int c = at(i) + j * step;
             if (c < H) p.part[(int64_t)blockIdx.x * H + c] = acc[i][j];
         }
 }

@@ -38,7 +38,7 @@ __device__ __forceinline__ int rows_of(const DispatchParams &p)
 }  // namespace
 
 // The first `small` CTAs carry what is small (positions, row weights, block scales), the others the rows: a warp
-// takes 32 x kUnits pieces of T (16 bytes, or 2 where rows are not made of 16-byte pieces) of one row at a time.
+// takes 32 x kUnits pieces of T (16, 4 or 2 bytes, the largest that rows are made of) of one row at a time.
 template <typename T, int kUnits>
 __global__ void __launch_bounds__(kOrderThreads) dispatch_kernel(const __grid_constant__ DispatchParams p)
 {
@@ -105,24 +105,16 @@ __global__ void __launch_bounds__(kOrderThreads) dispatch_kernel(const __grid_co
 // 8 values of a row (or one) as they lie in memory.
 template <bool F32, bool VEC>
 struct Raw {
-    uint4 q[F32 && VEC ? 2 : 1];
+    uint4 q[F32 ? 2 : 1];
     __device__ __forceinline__ void load(const char *row, int c)
     {
-        if constexpr (VEC) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(row + c * (F32 ? 4 : 2));
-            q[0] = __ldg(p);
-            if constexpr (F32) q[1] = __ldg(p + 1);
-        } else if constexpr (F32) {
-            q[0].x = __ldg(reinterpret_cast<const uint32_t *>(row) + c);
-        } else {
-            q[0].x = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + c) << 16;
-        }
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + c * (F32 ? 4 : 2));
+        q[0] = __ldg(p);
+        if constexpr (F32) q[1] = __ldg(p + 1);
     }
-    __device__ __forceinline__ void open(float (&v)[VEC ? 8 : 1]) const
+    __device__ __forceinline__ void open(float (&v)[8]) const
     {
-        if constexpr (!VEC) {
-            v[0] = __uint_as_float(q[0].x);
-        } else if constexpr (F32) {
+        if constexpr (F32) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 v[4 * i] = __uint_as_float(q[i].x);
@@ -136,27 +128,42 @@ struct Raw {
     }
 };
 
-// Combine, and the backward of dispatch (no weights): one token per CTA, 8 columns per thread (or one where rows are not
-// made of 16-byte pieces), the loads of several rows in flight together. They stay as they lie in memory until all are
-// issued: widened to fp32 at once, eight rows took 90 registers a thread, and two CTAs an SM were too few (8192 tokens of
-// 2048 columns, top 8, bf16: 162 us).
-template <bool YF32, bool OF32, bool VEC>
+template <bool F32>
+struct Raw<F32, false> {
+    uint32_t q;
+    __device__ __forceinline__ void load(const char *row, int c)
+    {
+        if constexpr (F32) q = __ldg(reinterpret_cast<const uint32_t *>(row) + c);
+        else q = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + c) << 16;
+    }
+    __device__ __forceinline__ void open(float (&v)[1]) const { v[0] = __uint_as_float(q); }
+};
+
+// Combine, and the backward of dispatch (no weights): p.team threads per token (a power of two), 8 columns each (or four,
+// apart, where rows are not made of 16-byte pieces), the loads of several rows in flight together. They stay as they lie
+// in memory until all are issued: widened to fp32 at once, eight rows took 90 registers a thread, and two CTAs an SM were
+// too few (8192 tokens of 2048 columns, top 8, bf16: 162 us, now 59). WIDE: a CTA per token, known to the compiler (67 us
+// otherwise); narrow rows share a CTA (24 columns: 3.8 us, a CTA each 23).
+template <bool YF32, bool OF32, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(kOrderThreads) combine_rows_kernel(const __grid_constant__ CombineParams p)
 {
-    constexpr int W = VEC ? 8 : 1, J = YF32 ? 4 : 8;
+    constexpr int W = VEC ? 8 : 1, J = YF32 ? 4 : 8, C = VEC ? 1 : 4;
     pdl_enter();
-    const int64_t t = blockIdx.x;
+    const int team = WIDE ? kOrderThreads : p.team, me = threadIdx.x & (team - 1);
+    const int64_t t = (int64_t)blockIdx.x * (kOrderThreads / team) + threadIdx.x / team;
+    if (t >= p.T) return;
     const int *pos = p.pos + t * p.k;
     const float *w = p.w ? p.w + t * p.k : nullptr;
-    if (p.dw && blockIdx.y == 0 && (int)threadIdx.x < p.k) {
-        const int r = __ldg(pos + threadIdx.x);
-        p.dw[t * p.k + threadIdx.x] = r >= 0 && r < p.P ? __ldg(p.drow_w + r) : 0.f;
-    }
-    const int c = W * (blockIdx.y * kOrderThreads + threadIdx.x);
-    if (c >= p.H) return;
-    float acc[W] = {};
+    if (p.dw && blockIdx.y == 0)
+        for (int j = me; j < p.k; j += team) {
+            const int r = __ldg(pos + j);
+            p.dw[t * p.k + j] = r >= 0 && r < p.P ? __ldg(p.drow_w + r) : 0.f;
+        }
+    const int c0 = W * (blockIdx.y * C * team + me);
+    if (c0 >= p.H) return;
+    float acc[C][W] = {};
     for (int j0 = 0; j0 < p.k; j0 += J) {
-        Raw<YF32, VEC> v[J] = {};
+        Raw<YF32, VEC> v[J][C] = {};
         float f[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -165,41 +172,60 @@ __global__ void __launch_bounds__(kOrderThreads) combine_rows_kernel(const __gri
                 const int r = __ldg(pos + j0 + j);
                 if (r >= 0 && r < p.P) {
                     f[j] = w ? __ldg(w + j0 + j) : 1.f;
-                    v[j].load(static_cast<const char *>(p.y) + r * p.ld_y * (YF32 ? 4 : 2), c);
+#pragma unroll
+                    for (int n = 0; n < C; ++n)
+                        if (c0 + n * team < p.H)
+                            v[j][n].load(static_cast<const char *>(p.y) + r * p.ld_y * (YF32 ? 4 : 2), c0 + n * team);
                 }
             }
         }
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            float a[W];
-            v[j].open(a);
+        for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] = fmaf(f[j], a[i], acc[i]);
-        }
+            for (int n = 0; n < C; ++n) {
+                float a[W];
+                v[j][n].open(a);
+#pragma unroll
+                for (int i = 0; i < W; ++i) acc[n][i] = fmaf(f[j], a[i], acc[n][i]);
+            }
     }
     const int size = OF32 ? 4 : 2;
     char *out = static_cast<char *>(p.out) + t * p.ld_out * size;
-    if (p.add) {
-        Raw<OF32, VEC> add;
-        float a[W];
-        add.load(static_cast<const char *>(p.add) + t * p.ld_add * size, c);
-        add.open(a);
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] += a[i];
-    }
-    if constexpr (VEC) {
-        if constexpr (OF32) {
-            float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + c);
-            o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + c) = pack8(acc);
+    for (int n = 0; n < C; ++n) {
+        const int c = c0 + n * team;
+        if (c >= p.H) break;
+        if (p.add) {
+            Raw<OF32, VEC> add;
+            float a[W];
+            add.load(static_cast<const char *>(p.add) + t * p.ld_add * size, c);
+            add.open(a);
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[n][i] += a[i];
         }
-    } else if constexpr (OF32) {
-        reinterpret_cast<float *>(out)[c] = acc[0];
-    } else {
-        reinterpret_cast<uint16_t *>(out)[c] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
+        if constexpr (VEC) {
+            if constexpr (OF32) {
+                float4 *o = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + c);
+                o[0] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                o[1] = make_float4(acc[n][4], acc[n][5], acc[n][6], acc[n][7]);
+            } else {
+                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + c) = pack8(acc[n]);
+            }
+        } else if constexpr (OF32) {
+            reinterpret_cast<float *>(out)[c] = acc[n][0];
+        } else {
+            reinterpret_cast<uint16_t *>(out)[c] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[n][0]));
+        }
     }
+}
+
+// Elements from the last 32 x T boundary of memory to `p`: a warp that stores an element a lane begins there, so that its
+// stores are whole sectors (combine's backward, 65536 rows of 2047 bf16: 235 us without this, 210 with it). Vectors are
+// aligned as they are.
+template <bool VEC, typename T>
+__device__ __forceinline__ int lead(const T *p)
+{
+    return VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T) % 32);
 }
 
 // One warp per slot (neighbouring warps share a token, whose row then comes from L1).
@@ -222,23 +248,23 @@ __global__ void __launch_bounds__(kOrderThreads) combine_backward_kernel(const _
         const char *y = static_cast<const char *>(p.y) + r * p.ld_y * (YF32 ? 4 : 2);
         uint16_t *o = static_cast<uint16_t *>(p.dy) + r * p.ld_dy;
         float sum = 0.f;
-        for (int c0 = W * lane; c0 < p.H; c0 += 32 * W * U) {
+        for (int c0 = W * lane - lead<VEC>(o); c0 < p.H; c0 += 32 * W * U) {
             Raw<DF32, VEC> a[U];
             Raw<YF32, VEC> b[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int c = c0 + 32 * W * i;
-                if (c < p.H && p.dw) b[i].load(y, c);
+                if (c >= 0 && c < p.H && p.dw) b[i].load(y, c);
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int c = c0 + 32 * W * i;
-                if (c < p.H) a[i].load(d, c);
+                if (c >= 0 && c < p.H) a[i].load(d, c);
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int c = c0 + 32 * W * i;
-                if (c >= p.H) continue;
+                if (c < 0 || c >= p.H) continue;
                 float u[W], v[W];
                 a[i].open(u);
                 if (p.dw) {
@@ -262,6 +288,18 @@ __global__ void __launch_bounds__(kOrderThreads) combine_backward_kernel(const _
 
 namespace {
 
+using CombineKernel = void (*)(CombineParams);
+template <bool... Known>
+CombineKernel combine_kernel()
+{
+    return combine_rows_kernel<Known...>;
+}
+template <bool... Known, typename... Rest>
+CombineKernel combine_kernel(bool next, Rest... rest)
+{
+    return next ? combine_kernel<Known..., true>(rest...) : combine_kernel<Known..., false>(rest...);
+}
+
 bool vec16(const void *p, int64_t row_bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0; }
 
 }  // namespace
@@ -276,8 +314,11 @@ cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s)
         if (e != cudaSuccess) return e;
     }
     const int per = kOrderThreads / 32;
-    const bool vec = vec16(p.x, p.ld_x) && vec16(p.out, p.ld_out) && p.row_bytes % 16 == 0;
-    const int piece = vec ? 16 : 2, unit = vec ? 4 : 8;
+    const auto made_of = [&](int n) {
+        return p.row_bytes % n == 0 && p.ld_x % n == 0 && p.ld_out % n == 0 && reinterpret_cast<uintptr_t>(p.x) % n == 0 &&
+               reinterpret_cast<uintptr_t>(p.out) % n == 0;
+    };
+    const int piece = made_of(16) ? 16 : made_of(4) ? 4 : 2, unit = piece == 16 ? 4 : piece == 4 ? 8 : 16;
     const int chunks = (p.row_bytes / piece + 32 * unit - 1) / (32 * unit);
     const int64_t want = ((int64_t)p.P * chunks + per - 1) / per, most = (int64_t)sm_count() * 32;
     // CTAs for what is small: a thread per slot or eight scales, up to four CTAs per SM
@@ -285,22 +326,23 @@ cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s)
     p.small = 0;
     if (p.pos || p.row_w || p.blocks) p.small = p.clear && !p.blocks ? 1 : (int)(each < 4 * sm_count() ? each : 4 * sm_count());
     const unsigned grid = (unsigned)(want < most ? want : most) + p.small;
-    if (vec) FT_LAUNCH(dispatch_kernel<uint4, 4>, dim3(grid), dim3(kOrderThreads), 0, s, p);
-    else FT_LAUNCH(dispatch_kernel<uint16_t, 8>, dim3(grid), dim3(kOrderThreads), 0, s, p);
+    auto kern = piece == 16 ? dispatch_kernel<uint4, 4> : piece == 4 ? dispatch_kernel<uint32_t, 8> : dispatch_kernel<uint16_t, 16>;
+    FT_LAUNCH(kern, dim3(grid), dim3(kOrderThreads), 0, s, p);
     count_launches(1);
     return cudaGetLastError();
 }
 
-cudaError_t launch_combine_rows(const CombineParams &p, bool y_f32, bool out_f32, cudaStream_t s)
+cudaError_t launch_combine_rows(CombineParams p, bool y_f32, bool out_f32, cudaStream_t s)
 {
     const int ys = y_f32 ? 4 : 2, os = out_f32 ? 4 : 2;
     const bool vec = p.H % 8 == 0 && vec16(p.y, p.ld_y * ys) && vec16(p.out, p.ld_out * os) && vec16(p.add, p.ld_add * os);
-    const int cols = kOrderThreads * (vec ? 8 : 1);
-    const dim3 grid(p.T, (p.H + cols - 1) / cols);
-    auto kern = y_f32 ? (out_f32 ? (vec ? combine_rows_kernel<true, true, true> : combine_rows_kernel<true, true, false>)
-                                 : (vec ? combine_rows_kernel<true, false, true> : combine_rows_kernel<true, false, false>))
-                      : (out_f32 ? (vec ? combine_rows_kernel<false, true, true> : combine_rows_kernel<false, true, false>)
-                                 : (vec ? combine_rows_kernel<false, false, true> : combine_rows_kernel<false, false, false>));
+    const int each = vec ? 8 : 4;  // columns of a thread
+    p.team = 1;
+    while (p.team < kOrderThreads && p.team * each < p.H) p.team *= 2;
+    const int tokens = kOrderThreads / p.team, cols = p.team * each;
+    const dim3 grid((p.T + tokens - 1) / tokens, (p.H + cols - 1) / cols);
+    const bool wide = p.team == kOrderThreads;
+    auto kern = combine_kernel(y_f32, out_f32, vec, wide);
     FT_LAUNCH(kern, grid, dim3(kOrderThreads), 0, s, p);
     count_launches(1);
     return cudaGetLastError();
