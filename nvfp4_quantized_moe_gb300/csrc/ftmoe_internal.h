@@ -289,7 +289,7 @@ struct DispatchParams {
     const float *w;
     float *row_w;                           // may be null
     int *pos;                               // may be null
-    int small, clear, stream;               // set by the launch
+    int small, clear, stream, team;         // set by the launch
 };
 cudaError_t launch_dispatch(DispatchParams p, cudaStream_t s);
 struct CombineParams {

@@ -52,7 +52,8 @@ def _order(gen, T, k, E):
 # rows of 16-byte pieces and not, one column, several warps a row; slots on both sides of the one-CTA limit
 @pytest.mark.parametrize("dtype", [BF, F32, U8])
 @pytest.mark.parametrize("T,k,E,H,pad", [(1, 1, 1, 16, 0), (1, 8, 16, 2048, 0), (37, 2, 8, 34, 2), (300, 8, 60, 640, 0), (700, 8, 256, 72, 8),
-                                         (513, 8, 8, 130, 0), (5, 32, 64, 5000, 0)])
+                                         (513, 8, 8, 130, 0), (5, 32, 64, 5000, 0), (900, 4, 8, 8, 0), (2000, 2, 8, 2, 0),
+                                         (33, 3, 8, 128, 0), (70, 8, 16, 30, 6)])
 def test_dispatch(ft, T, k, E, H, pad, dtype):
     gen = _gen(T + H)
     x = (torch.randn((T, H + pad), generator=gen, device="cuda") * 50).to(dtype)[:, :H]
@@ -157,7 +158,8 @@ def test_a_slot_in_two_rows_counts_for_the_last(ft):
         assert torch.equal(pos[:, 0].long(), torch.arange(T, 2 * T, device="cuda"))
 
 
-SUMS = [(1, 8, 16, 2048, 0), (1, 1, 1, 1, 0), (300, 8, 60, 640, 0), (64, 6, 8, 33, 1), (17, 32, 64, 4100, 0), (1000, 2, 8, 264, 8)]
+SUMS = [(1, 8, 16, 2048, 0), (1, 1, 1, 1, 0), (100, 32, 64, 8, 0), (777, 4, 8, 16, 0), (50, 9, 16, 2, 0), (300, 8, 60, 2056, 0),
+        (40, 8, 60, 1025, 0), (300, 8, 60, 640, 0), (64, 6, 8, 33, 1), (17, 32, 64, 4100, 0), (1000, 2, 8, 264, 8)]
 
 
 @pytest.mark.parametrize("yt", [BF, F32])
