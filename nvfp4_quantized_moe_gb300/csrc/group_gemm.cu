@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
     int *sh_unit = reinterpret_cast<int *>(unit_empty + kAhead);  // the next units
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sh_unit + kAhead);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int split = kSplit ? p.split : 1;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(Ring<CG, BN, WG>::threads, 1)
     }
     if (warp == 1) tmem_alloc<CG>(tmem_slot, 2 * BN);
     pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
-    const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles);
+    const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles, sh_flag);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
     if constexpr (CG == 2) cluster_sync();

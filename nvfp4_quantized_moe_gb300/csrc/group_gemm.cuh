@@ -308,11 +308,63 @@ struct Tile {
 
 // Offsets of the experts (clamped into [0, P], never decreasing inside an expert) and the
 // running count of their tiles, in shared memory: [E + 1] ints each. Run by all threads.
-// Returns whether the offsets were valid. ALIGN: tiles begin at multiples of it (find_aligned_tile).
-// Every warp finds what lies before its own experts by itself, so that one barrier is all it takes (the callers
-// synchronise before the table is used).
-template <int ALIGN = 1>
-__device__ __forceinline__ bool build_table(const int *offs, int E, int P, int BN, int *sh_offs, int *sh_tiles)
+// Returns whether the offsets were valid. `sh_flag` is one int of shared memory.
+__device__ __forceinline__ bool build_table(const int *offs, int E, int P, int BN, int *sh_offs, int *sh_tiles, int *sh_flag)
+{
+    if (threadIdx.x == 0) *sh_flag = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i <= E; i += blockDim.x) {
+        const int v = offs ? __ldg(offs + i) : (i ? P : 0);
+        sh_offs[i] = min(max(v, 0), P);
+        bool bad = v < 0 || v > P;
+        if (i < E && offs) bad |= __ldg(offs + i + 1) < v;
+        if (bad) *sh_flag = 1;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int base = 0;
+        for (int i0 = 0; i0 < E; i0 += 32) {
+            const int i = i0 + threadIdx.x;
+            int t = i < E ? (max(sh_offs[i + 1] - sh_offs[i], 0) + BN - 1) / BN : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, t, d);
+                if ((int)threadIdx.x >= d) t += o;
+            }
+            if (i < E) sh_tiles[i + 1] = base + t;
+            base += __shfl_sync(0xFFFFFFFFu, t, 31);
+        }
+        if (threadIdx.x == 0) sh_tiles[0] = 0;
+    }
+    __syncthreads();
+    return *sh_flag == 0;
+}
+
+__device__ __forceinline__ Tile find_tile(int t, int E, int BN, int gran, const int *sh_offs, const int *sh_tiles)
+{
+    int lo = 0, hi = E;  // sh_tiles[lo] <= t < sh_tiles[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh_tiles[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const int n = sh_offs[lo + 1] - sh_offs[lo], nt = (n + BN - 1) / BN, j = t - sh_tiles[lo];
+    const int len = ((n + nt - 1) / nt + gran - 1) / gran * gran;
+    Tile r;
+    r.e = lo;
+    r.row0 = sh_offs[lo] + j * len;
+    r.rows = max(min(len, n - j * len), 0);
+    return r;
+}
+
+// ---------------------------------------------------------------- the same table, with one barrier
+//
+// For kernels one warp of which looks tiles up: every warp finds what lies before its own experts by itself, so that one
+// barrier is all that the table takes (the caller synchronises before it is used), and a warp finds a tile's expert
+// with two ballots. Tiles begin at multiples of ALIGN rows (find_aligned_tile). Returns whether the offsets were valid.
+// (In the 8-bit product's wide kernel this costs registers that it does not have: 80 us instead of 75 for 4096^3.)
+template <int ALIGN>
+__device__ __forceinline__ bool build_tiles(const int *offs, int E, int P, int BN, int *sh_offs, int *sh_tiles)
 {
     bool bad = false;
     for (int i = threadIdx.x; i <= E; i += blockDim.x) {
@@ -343,6 +395,7 @@ __device__ __forceinline__ bool build_table(const int *offs, int E, int P, int B
     return valid;
 }
 
+// Tile t, of expert e.
 __device__ __forceinline__ Tile tile_of(int t, int e, int BN, int gran, const int *sh_offs, const int *sh_tiles)
 {
     const int n = sh_offs[e + 1] - sh_offs[e], nt = (n + BN - 1) / BN, j = t - sh_tiles[e];
@@ -352,17 +405,6 @@ __device__ __forceinline__ Tile tile_of(int t, int e, int BN, int gran, const in
     r.row0 = sh_offs[e] + j * len;
     r.rows = max(min(len, n - j * len), 0);
     return r;
-}
-
-__device__ __forceinline__ Tile find_tile(int t, int E, int BN, int gran, const int *sh_offs, const int *sh_tiles)
-{
-    int lo = 0, hi = E;  // sh_tiles[lo] <= t < sh_tiles[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh_tiles[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    return tile_of(t, lo, BN, gran, sh_offs, sh_tiles);
 }
 
 // The expert of tile t, by a whole warp: the last one whose running count is t or less.

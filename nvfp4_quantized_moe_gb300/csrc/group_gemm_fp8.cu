@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
              *sc_empty = sc_full + NS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + NS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint64_t wl = p.wait_ns ? p.wait_ns : kWaitNs;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads8, 1)
     }
     if (warp == 1) tmem_alloc<1>(tmem_slot, NA * BN);
     pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
-    const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles);
+    const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles, sh_flag);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
     __syncthreads();
@@ -388,6 +389,7 @@ __global__ void __launch_bounds__(RingW::threads, 1)
     uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 4;  // [piece][buffer]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *sh_flag = reinterpret_cast<int *>(tmem_slot + 2);
     int *sh_offs = reinterpret_cast<int *>(tmem_slot + 4), *sh_tiles = sh_offs + p.E + 1;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(RingW::threads, 1)
     }
     if (warp == 1) tmem_alloc<2>(tmem_slot, 2 * BN);
     pdl_enter();  // (only now: the set-up above overlaps the end of the kernel before)
-    const bool valid = build_table(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles);
+    const bool valid = build_table(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles, sh_flag);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
     cluster_sync();

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads4, 1)
     // its CTAs would come to SMs whose L1 is almost all shared memory here, and keep them so. A quantizer of 16384 x
     // 2048 values behind this kernel took 24 us instead of 15.)
     pdl_wait();
-    const bool valid = build_table(p.offs, p.E, p.P, BN, sh_offs, sh_tiles);
+    const bool valid = build_tiles<1>(p.offs, p.E, p.P, BN, sh_offs, sh_tiles);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
     __syncthreads();
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(RingP::threads, 1)
     // its CTAs would come to SMs whose L1 is almost all shared memory here, and keep them so. A quantizer of 65536 x
     // 2048 values behind this kernel took 85 us instead of 57.)
     pdl_wait();
-    const bool valid = build_table<4>(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles);
+    const bool valid = build_tiles<4>(p.offs, p.E, p.P, 2 * kTileM, sh_offs, sh_tiles);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = valid ? FT_OK : FT_ERR_INVALID_ROUTING;
     tc::fence_before_sync();
     cluster_sync();
