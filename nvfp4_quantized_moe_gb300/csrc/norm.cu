@@ -9,6 +9,13 @@
 // Bound by memory: every operand is read once and every result written once. A row stays in registers between
 // its sum of squares and its outputs, so that nothing is read twice; sums are fp32. The norm is that of s as it is
 // stored, so that the backward pass, which has only the stored s, is the gradient of what was computed.
+//
+// Measured on one GB300: 8192 rows of 2048 with a bf16 residual (134 MB) 25.7 us, 5.2 TB/s, where a plain copy of as
+// many bytes takes 27.7; 1999 rows of 4096 with an fp32 residual into 8 bits (90 MB) 19.5 us; backward of 8192 rows of 2048
+// (134 MB) 32.5 us, of which joining the weight's gradient is 5; one row 2.6 us. Rows that are not made of 16-byte
+// pieces go an element at a time: 8192 rows of 2047 39 us. A whole CTA per row from 257 columns on, the loads of all of
+// a thread's columns in flight: 2048 columns on 256 threads take 25.7 us, on 128 25.8, 64 31.5, 32 38.3 (one row: 2.6, 3.2,
+// 4.9, 7.5).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
