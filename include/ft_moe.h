@@ -366,7 +366,7 @@ ft_status ft_moe_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, 
  * half), with a power of two as scale for every 32 elements along K (the byte s + 127 for 2^s; 255 is NaN):
  *   y[p, n] = sum_b 2^(xs[p, b] + ws[e, n, b]) * sum_{k in block b} x[p, k] * w[e, n, k]
  * on the 4-bit tensor cores, which apply the scales themselves; sums are fp32. Rows, offs, workspace and
- * errors as ft_moe_group_gemm. Scale bytes of four neighbouring blocks (128 elements) form a word, the
+ * errors as ft_moe_group_gemm, but where offs is bad y is left as it was. Scale bytes of four neighbouring blocks (128 elements) form a word, the
  * first block's byte lowest; bytes of blocks beyond K are 0.
  *   x        device codes, rows ld_x bytes apart (a multiple of 16), 16-byte aligned
  *   x_scale  device words [ceil(K / 128)][ld_xs], one per row, ld_xs >= P and a multiple of 4, 16-byte aligned

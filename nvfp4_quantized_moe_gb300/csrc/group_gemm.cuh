@@ -361,7 +361,8 @@ __device__ __forceinline__ Tile find_tile(int t, int E, int BN, int gran, const 
 //
 // For kernels one warp of which looks tiles up: every warp finds what lies before its own experts by itself, so that one
 // barrier is all that the table takes (the caller synchronises before it is used), and a warp finds a tile's expert
-// with two ballots. Tiles begin at multiples of ALIGN rows (find_aligned_tile). Returns whether the offsets were valid.
+// with two ballots. Tiles begin at multiples of ALIGN rows (find_aligned_tile). Returns whether the offsets were valid; if
+// not, there are no tiles (ranges that overlap could be E times the work, and more units than a launch is made for).
 // (In the 8-bit product's wide kernel this costs registers that it does not have: 80 us instead of 75 for 4096^3.)
 template <int ALIGN>
 __device__ __forceinline__ bool build_tiles(const int *offs, int E, int P, int BN, int *sh_offs, int *sh_tiles)
@@ -375,7 +376,7 @@ __device__ __forceinline__ bool build_tiles(const int *offs, int E, int P, int B
     const bool valid = !__syncthreads_or(bad);
     auto tiles = [&](int i) {
         const int first = sh_offs[i], last = sh_offs[i + 1];
-        return last > first ? (last - (ALIGN > 1 ? first / ALIGN * ALIGN : first) + BN - 1) / BN : 0;
+        return valid && last > first ? (last - (ALIGN > 1 ? first / ALIGN * ALIGN : first) + BN - 1) / BN : 0;
     };
     const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
     for (int i0 = 32 * (threadIdx.x >> 5); i0 < E; i0 += 32 * warps) {

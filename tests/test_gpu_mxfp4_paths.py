@@ -139,6 +139,28 @@ def test_a_stalled_pipeline_ends_with_an_error(ft, name):
     assert torch.equal(c.run(c.empty()), want) and ft.ft_moe_read_status(c.work) == 0
 
 
+@pytest.mark.parametrize("name", list(CASES))
+def test_bad_offsets_compute_nothing(ft, name):
+    """Ranges that overlap, decrease or leave the rows: reported, y left as it was, and the next call is right."""
+    c = Case(ft, name)
+    y = torch.full_like(c.empty(), 7.0)
+    good, E, P = c.offs, c.E, c.P
+    swing = torch.tensor([0, P] * E, dtype=torch.int32, device="cuda")[:E + 1]  # 0, P, 0, P, ...
+    if E > 1:
+        bad = [swing, torch.cat([good[:-1], good[-1:] + 1]), torch.cat([good[:1] - 1, good[1:]])]
+    else:
+        bad = [torch.tensor([0, P + 1], dtype=torch.int32, device="cuda"), torch.tensor([P, 0], dtype=torch.int32, device="cuda")]
+    for offs in bad:
+        c.offs = offs
+        c.run(y)
+        assert ft.STATUS[ft.ft_moe_read_status(c.work)] == "FT_ERR_INVALID_ROUTING"
+        assert (y == 7).all()
+    c.offs = good
+    c.run(y)
+    assert ft.ft_moe_read_status(c.work) == 0
+    c.check(y)
+
+
 @pytest.mark.parametrize("name", ["pairs, bf16", "32 rows, fp32"])
 def test_first_call_of_a_thread(ft, name):
     c = Case(ft, name)
