@@ -167,6 +167,8 @@ GROUPS = [
     # by pairs of CTAs: first rows at every remainder of four, tiles that end one before, at and behind their last row
     ([301, 0, 258, 3, 1023, 130], 3100, 544), ([255, 257, 256, 1, 511], 3700, 96), ([1500, 1340], 3000, 2112), ([17000], 520, 288),
     ([145] * 64, 264, 320), ([253, 254, 255, 256, 257, 258, 259], 2752, 128), ([60000, 1], 192, 64),
+    # fewer weight rows than a piece of 16 bytes of y
+    ([3], 1, 32), ([300, 5], 7, 96), ([50000], 1, 32), ([25000, 25003], 7, 64),
 ]
 
 
