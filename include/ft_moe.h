@@ -450,8 +450,7 @@ ft_status ft_moe_combine_backward(const void *dout, int64_t ld_dout, int32_t dou
  *   total = x + residual        stored in the residual's type (total = x, not stored, without a residual)
  *   rstd  = 1 / sqrt(mean_h total^2 + eps)
  *   y     = total * rstd * (w_offset + w)
- * of the total as it is stored; fp32 inside, so that totals above 2^63 or so, whose squares' sum fp32 does not hold, give
- * rstd = 0. y goes into bf16 (y), into e4m3 codes with block scales by
+ * of the total as it is stored; fp32 inside: a row whose sum of squares fp32 does not hold (2^128) gets rstd = 0. y goes into bf16 (y), into e4m3 codes with block scales by
  * ft_moe_quantize_fp8's rule from the fp32 y (codes, scales; H a multiple of 16), or both.
  *   x         device bf16 rows
  *   residual, total  device rows of total_dtype (bf16 or fp32), both or neither; total may be residual itself
