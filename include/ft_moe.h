@@ -36,6 +36,8 @@
  *     the device and keeps no per-call state; sizes come from ft_moe_layout and
  *     ft_moe_workspace_size.
  *   - Any host thread may call; calls that may run at once need workspaces and outputs of their own.
+ *   - Calls launch on the calling thread's current device, where the stream and all operands have to lie. (The
+ *     Python binding refuses tensors and streams of another device.)
  *   - Every call that takes a stream is asynchronous on that stream (cudaStream_t,
  *     passed as void*; NULL is the legacy default stream). Argument and geometry
  *     errors are detected on the host and returned before anything is launched.

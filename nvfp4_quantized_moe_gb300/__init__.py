@@ -329,16 +329,27 @@ def _dims(name, t, n):
     return t.shape
 
 
+def _launchable(stream, dev):
+    """Refuses a call on tensors of device `dev` that would not run there: the library launches on the current device, and
+    a stream given as a number does not say whose it is (0 is the default stream of every device)."""
+    try:
+        current = torch._C._cuda_getDevice()
+    except RuntimeError:  # no driver on this machine, so that no device is current
+        current = dev
+    if dev != current:
+        raise ValueError(f"the tensors lie on cuda:{dev}, but cuda:{current} is the current device: make theirs current")
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the tensors lie on cuda:{dev}, but the stream belongs to cuda:{stream.device_index}")
+
+
 def _stream_of(stream, dev):
     """The stream to launch on, as an integer: the one given, or the device's current one."""
     if dev < 0:
         raise ValueError("expected tensors on the GPU")
-    if stream is not None:
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev != torch._C._cuda_getDevice():  # (a device's default stream is 0 on every device)
-        raise ValueError(f"the tensors lie on cuda:{dev}, which is not the current device: make it current, or pass a "
-                         "stream of it")
-    return torch._C._cuda_getCurrentRawStream(dev)
+    _launchable(stream, dev)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _offsets(offs, dev, E):
