@@ -165,13 +165,27 @@ def _check(status: int):
         raise FtMoeError(status, ft_last_error())
 
 
+def _launchable(stream, dev):
+    """Refuses a call on tensors of device `dev` that would not run there: the library launches on the current device, and
+    a stream given as a number does not say whose it is (0 is the default stream of every device)."""
+    try:
+        current = torch._C._cuda_getDevice()
+    except RuntimeError:  # no driver on this machine, so that no device is current
+        current = dev
+    if dev != current:
+        raise ValueError(f"the tensors lie on cuda:{dev}, but cuda:{current} is the current device: make theirs current")
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the tensors lie on cuda:{dev}, but the stream belongs to cuda:{stream.device_index}")
+
+
 def _stream(stream, *tensors):
+    """The stream to launch on: the one given, or the current one of the device on which the call's tensors lie."""
+    devs = {t.get_device() for t in tensors if isinstance(t, torch.Tensor)} - {-1}
+    for dev in devs:
+        _launchable(stream, dev)
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
-    return ctypes.c_void_p(0)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(devs.pop()) if devs else 0)
 
 
 def _ptr(t):
@@ -221,12 +235,12 @@ def ft_moe_pack(cfg: MoEConfig, shared: int, pieces: dict, banks, stream=None):
             raise ValueError("pieces must be contiguous")
     p = _Pieces(*[_ptr(v).value if v is not None else None for v in vals], 1 if on_dev else 0)
     _check(load().ft_moe_pack(ctypes.byref(cfg), shared, ctypes.byref(p), ctypes.byref(_banks(banks)),
-                              _stream(stream, *banks)))
+                              _stream(stream, *banks, *(vals if on_dev else ()))))
 
 
 def ft_moe_route(logits: torch.Tensor, k: int, topk_ids: torch.Tensor, topk_w: torch.Tensor, stream=None):
     T, E = logits.shape
-    _check(load().ft_moe_route(_ptr(logits), T, E, k, _ptr(topk_ids), _ptr(topk_w), _stream(stream, logits)))
+    _check(load().ft_moe_route(_ptr(logits), T, E, k, _ptr(topk_ids), _ptr(topk_w), _stream(stream, logits, topk_ids, topk_w)))
 
 
 def ft_moe_route_gemm(x: torch.Tensor, w_router: torch.Tensor, k: int, logits: torch.Tensor, topk_ids: torch.Tensor,
@@ -235,7 +249,7 @@ def ft_moe_route_gemm(x: torch.Tensor, w_router: torch.Tensor, k: int, logits: t
     T, H = x.shape
     E = w_router.shape[0]
     _check(load().ft_moe_route_gemm(_ptr(x), T, H, _ptr(w_router), E, k, _ptr(logits), _ptr(topk_ids),
-                                    _ptr(topk_w), _stream(stream, x)))
+                                    _ptr(topk_w), _stream(stream, x, w_router, logits, topk_ids, topk_w)))
 
 
 def ft_moe_workspace_size(cfg: MoEConfig, T: int) -> int:
@@ -252,7 +266,7 @@ def ft_moe_forward(cfg: MoEConfig, routed, shared, x: torch.Tensor, topk_ids: to
     _check(load().ft_moe_forward(ctypes.byref(cfg), ctypes.byref(rb), ctypes.byref(sb) if sb is not None else None,
                                  _ptr(x), x.shape[0], _ptr(topk_ids), _ptr(topk_w), _ptr(out), out_dtype,
                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 _stream(stream, x)))
+                                 _stream(stream, x, *routed, *(shared or ()), topk_ids, topk_w, out, workspace)))
 
 
 def ft_moe_workspace_size_w4a4(cfg: MoEConfig, T: int) -> int:
@@ -269,7 +283,8 @@ def ft_moe_forward_w4a4(cfg: MoEConfig, routed, shared, x: torch.Tensor, topk_id
     _check(load().ft_moe_forward_w4a4(ctypes.byref(cfg), ctypes.byref(rb),
                                       ctypes.byref(sb) if sb is not None else None, _ptr(x), x.shape[0],
                                       _ptr(topk_ids), _ptr(topk_w), _ptr(out), out_dtype, _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream, x)))
+                                      workspace.numel() * workspace.element_size(),
+                                      _stream(stream, x, *routed, *(shared or ()), topk_ids, topk_w, out, workspace)))
 
 
 def ft_moe_quantize_nvfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, glob: torch.Tensor,
@@ -278,7 +293,7 @@ def ft_moe_quantize_nvfp4(src: torch.Tensor, codes: torch.Tensor, scales: torch.
     dt = {torch.bfloat16: FT_DTYPE_BF16, torch.float32: FT_DTYPE_F32}[src.dtype]
     rows, K = src.shape
     _check(load().ft_moe_quantize_nvfp4(_ptr(src), dt, rows, K, _ptr(codes), _ptr(scales), _ptr(glob),
-                                        _stream(stream, src)))
+                                        _stream(stream, src, codes, scales, glob)))
 
 
 # A workspace belongs to one call at a time: calls on two streams need one each.
@@ -327,19 +342,6 @@ def _dims(name, t, n):
     if t.dim() != n:
         raise ValueError(f"{name}: expected {n} dimensions, got {tuple(t.shape)}")
     return t.shape
-
-
-def _launchable(stream, dev):
-    """Refuses a call on tensors of device `dev` that would not run there: the library launches on the current device, and
-    a stream given as a number does not say whose it is (0 is the default stream of every device)."""
-    try:
-        current = torch._C._cuda_getDevice()
-    except RuntimeError:  # no driver on this machine, so that no device is current
-        current = dev
-    if dev != current:
-        raise ValueError(f"the tensors lie on cuda:{dev}, but cuda:{current} is the current device: make theirs current")
-    if getattr(stream, "device_index", dev) != dev:
-        raise ValueError(f"the tensors lie on cuda:{dev}, but the stream belongs to cuda:{stream.device_index}")
 
 
 def _stream_of(stream, dev):
@@ -672,12 +674,13 @@ def ft_moe_align(topk_ids: torch.Tensor, E: int, block: int, sorted_slot, block_
     T, k = topk_ids.shape
     _check(load().ft_moe_align(_ptr(topk_ids), T, k, E, block, _ptr(sorted_slot), _ptr(block_expert),
                                _ptr(expert_off), _ptr(n_padded), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _stream(stream, topk_ids)))
+                               workspace.numel() * workspace.element_size(),
+                               _stream(stream, topk_ids, sorted_slot, block_expert, expert_off, n_padded, workspace)))
 
 
 def ft_moe_dequant(cfg: MoEConfig, shared: int, banks, which: int, expert: int, out: torch.Tensor, stream=None):
     _check(load().ft_moe_dequant(ctypes.byref(cfg), shared, ctypes.byref(_banks(banks)), which, expert, _ptr(out),
-                                 _stream(stream, out)))
+                                 _stream(stream, out, *banks)))
 
 
 def ft_moe_set_stage_events(events):
