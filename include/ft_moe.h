@@ -464,10 +464,10 @@ ft_status ft_moe_combine_backward(const void *dout, int64_t ld_dout, int32_t dou
  * n = total * rstd and g = dy * (w_offset + w):
  *   dx = dtotal + rstd * (g - n * mean_h(g * n))       (of total's type: the gradient of x and of the residual)
  *   dw = sum over the rows of dy * n                   (f32 [H], or NULL; accumulate = 1 adds to it)
- * dx may be dtotal itself. workspace (for dw): >= ft_moe_rmsnorm_workspace_size bytes, 256-byte aligned, one call
- * at a time. Results do not change from run to run. H <= 16384, rows <= 2^25. rows = 0 computes nothing (backward then
- * clears dw, or leaves it when accumulating). Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED, FT_ERR_WORKSPACE,
- * FT_ERR_CUDA. */
+ * dx may be dtotal itself. Outputs may not overlap inputs otherwise. workspace (for dw): >=
+ * ft_moe_rmsnorm_workspace_size bytes, 256-byte aligned, one call at a time. Results do not change from run to
+ * run. H <= 16384, rows <= 2^25. rows = 0 computes nothing (backward then clears dw, or leaves it when
+ * accumulating). Errors: FT_ERR_INVALID_ARG, FT_ERR_UNSUPPORTED, FT_ERR_WORKSPACE, FT_ERR_CUDA. */
 ft_status ft_moe_rmsnorm(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, void *total,
                          int64_t ld_total, int32_t total_dtype, const void *w, int32_t w_dtype, float w_offset, float eps,
                          int32_t rows, int32_t H, void *y, int64_t ld_y, uint8_t *codes, int64_t ld_codes, float *scales,

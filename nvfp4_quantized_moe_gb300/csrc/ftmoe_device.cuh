@@ -177,6 +177,18 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void *p)
     return v;
 }
 
+// The same for what the kernel's own stores may replace, an operand that an output may be: an ordinary load, since a
+// non-coherent one (and __ldg) asks for memory that nothing writes while the kernel runs. A thread that loads an element
+// stores to it only what it computed from that load, which orders the two; no other thread does.
+__device__ __forceinline__ uint4 ld_own_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ uint4 ldg_v4(const void *p)
 {
     return __ldg(reinterpret_cast<const uint4 *>(p));

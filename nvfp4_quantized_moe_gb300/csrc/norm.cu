@@ -50,19 +50,22 @@ __device__ __forceinline__ float row_sum(float v, float *red)
 }
 
 // 8 values of a row: VEC: from column c on, by 16-byte loads; else an element at a time, `step` columns apart, up to H.
-template <bool F32, bool VEC>
+// OWN: of an operand that an output of the kernel may be (ordinary loads, as ld_own_v4's).
+template <bool F32, bool VEC, bool OWN = false>
 __device__ __forceinline__ void get8(const void *row, int c, int step, int H, float (&v)[8])
 {
+    static_assert(!VEC || !OWN, "fetch8");
     if constexpr (VEC) {
         load8<F32>(row, c, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = c + i * step;
+            const float *f = static_cast<const float *>(row) + at;
+            const uint16_t *h = static_cast<const uint16_t *>(row) + at;
             v[i] = 0.f;
             if (at < H)
-                v[i] = F32 ? __ldg(static_cast<const float *>(row) + at)
-                           : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(row) + at) << 16);
+                v[i] = F32 ? (OWN ? *f : __ldg(f)) : __uint_as_float((uint32_t)(OWN ? *h : __ldg(h)) << 16);
         }
     }
 }
@@ -98,13 +101,55 @@ __device__ __forceinline__ void gain8(const void *w, bool f32, float offset, int
     for (int i = 0; i < 8; ++i) g[i] += offset;
 }
 
+// 8 values as they lie in memory. OWN: of an operand that an output of the kernel may be.
+template <bool F32>
+struct Raw8 {
+    uint4 q[F32 ? 2 : 1];
+};
+
+template <bool F32, bool VEC, bool OWN = false>
+__device__ __forceinline__ void fetch8(const void *row, int c, int step, int H, Raw8<F32> &r)
+{
+    if constexpr (VEC) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + c * (F32 ? 4 : 2));
+        r.q[0] = OWN ? ld_own_v4(p) : ldg_nc_v4(p);
+        if constexpr (F32) r.q[1] = OWN ? ld_own_v4(p + 1) : ldg_nc_v4(p + 1);
+    } else {
+        float v[8];
+        get8<F32, false, OWN>(row, c, step, H, v);
+        if constexpr (F32) {
+            r.q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            r.q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+        } else {
+            r.q[0] = pack8(v);  // (exact: the values are bf16)
+        }
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void open8(const Raw8<F32> &r, float (&v)[8])
+{
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(r.q[i].x);
+            v[4 * i + 1] = __uint_as_float(r.q[i].y);
+            v[4 * i + 2] = __uint_as_float(r.q[i].z);
+            v[4 * i + 3] = __uint_as_float(r.q[i].w);
+        }
+    } else {
+        unpack8(r.q[0], v);
+    }
+}
+
 constexpr int cta_threads(int tpr) { return tpr > 128 ? tpr : 128; }
 
 }  // namespace
 
-// TPR threads per row, NV vectors of 8 columns each; RES: 0 no residual, 1 a bf16 one, 2 an fp32 one.
+// TPR threads per row, NV vectors of 8 columns each; RES: 0 no residual, 1 a bf16 one, 2 an fp32 one. (512 threads: three
+// CTAs an SM, 40 registers a thread; with more and two CTAs, 2048 rows of 8192 columns take 31.2 us instead of 27.0.)
 template <int TPR, int NV, int RES, bool VEC>
-__global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(cta_threads(TPR), TPR == 512 ? 3 : 0) rmsnorm_kernel(const __grid_constant__ NormParams p)
 {
     constexpr int kRows = cta_threads(TPR) / TPR;
     __shared__ float red[32];
@@ -119,24 +164,37 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_kernel(const __grid_
     auto at = [&](int i) { return VEC || p.codes ? 8 * (t + i * TPR) : t + 8 * i * TPR; };
     float v[NV][8];
     float sq = 0.f;
+    constexpr bool F32 = RES == 2;
     const uint16_t *xr = static_cast<const uint16_t *>(p.x) + row * p.ld_x;
+    const char *rr = static_cast<const char *>(p.residual) + row * p.ld_residual * (F32 ? 4 : 2);
+    char *sr = static_cast<char *>(p.total) + row * p.ld_total * (F32 ? 4 : 2);
+    // (the loads of all columns stand before the first store, which may go over the residual)
+    Raw8<false> xq[NV] = {};
+    Raw8<F32> rq[NV] = {};
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (live && at(i) < H) {
+                fetch8<false, true>(xr, at(i), step, H, xq[i]);
+                if constexpr (RES != 0) fetch8<F32, true, true>(rr, at(i), step, H, rq[i]);
+            }
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = at(i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        if (live && c < H) get8<false, VEC>(xr, c, step, H, v[i]);
+        if (VEC) open8(xq[i], v[i]);
+        else if (live && c < H) get8<false, false>(xr, c, step, H, v[i]);
     }
     if constexpr (RES != 0) {
-        constexpr bool F32 = RES == 2;
-        const char *rr = static_cast<const char *>(p.residual) + row * p.ld_residual * (F32 ? 4 : 2);
-        char *sr = static_cast<char *>(p.total) + row * p.ld_total * (F32 ? 4 : 2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = at(i);
             if (live && c < H) {
                 float r[8];
-                get8<F32, VEC>(rr, c, step, H, r);
+                if constexpr (VEC) open8(rq[i], r);
+                else get8<F32, false, true>(rr, c, step, H, r);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     v[i][j] += r[j];
@@ -173,47 +231,6 @@ __global__ void __launch_bounds__(cta_threads(TPR)) rmsnorm_kernel(const __grid_
     }
 }
 
-// 8 values as they lie in memory.
-template <bool F32>
-struct Raw8 {
-    uint4 q[F32 ? 2 : 1];
-};
-
-template <bool F32, bool VEC>
-__device__ __forceinline__ void fetch8(const void *row, int c, int step, int H, Raw8<F32> &r)
-{
-    if constexpr (VEC) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + c * (F32 ? 4 : 2));
-        r.q[0] = ldg_nc_v4(p);
-        if constexpr (F32) r.q[1] = ldg_nc_v4(p + 1);
-    } else {
-        float v[8];
-        get8<F32, false>(row, c, step, H, v);
-        if constexpr (F32) {
-            r.q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-            r.q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-        } else {
-            r.q[0] = pack8(v);  // (exact: the values are bf16)
-        }
-    }
-}
-
-template <bool F32>
-__device__ __forceinline__ void open8(const Raw8<F32> &r, float (&v)[8])
-{
-    if constexpr (F32) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            v[4 * i] = __uint_as_float(r.q[i].x);
-            v[4 * i + 1] = __uint_as_float(r.q[i].y);
-            v[4 * i + 2] = __uint_as_float(r.q[i].z);
-            v[4 * i + 3] = __uint_as_float(r.q[i].w);
-        }
-    } else {
-        unpack8(r.q[0], v);
-    }
-}
-
 // Gradient. A CTA takes every gridDim-th group of rows, and its threads always the same columns, so that the
 // weight's gradient adds up in registers; the CTAs' sums go to the workspace [gridDim][H] and
 // norm_weight_kernel adds them in order. The next rows' loads are in flight while these are worked on.
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
             if (c < H) {
                 fetch8<F32, VEC>(sr, c, step, H, total[i]);
                 fetch8<false, VEC>(dr, c, step, H, dy[i]);
-                if (kAhead && p.dtotal) fetch8<F32, VEC>(pr, c, step, H, past[i]);
+                if (kAhead && p.dtotal) fetch8<F32, VEC, true>(pr, c, step, H, past[i]);
             }
         }
     };
@@ -267,7 +284,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
             open8(total[i], n[i]);
             open8(dy[i], g[i]);
             if (kAhead) ds[i] = past[i];
-            else if (live && c < H && p.dtotal) fetch8<F32, VEC>(pr, c, step, H, ds[i]);
+            else if (live && c < H && p.dtotal) fetch8<F32, VEC, true>(pr, c, step, H, ds[i]);
             if (live && c < H) {
                 float w[8];
                 gain8<VEC>(p.w, p.w_f32, p.offset, c, step, H, w);

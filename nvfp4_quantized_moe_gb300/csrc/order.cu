@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kOrderThreads) dispatch_narrow_kernel(const __
     }
 }
 
-// 8 values of a row (or one) as they lie in memory.
+// 8 values of a row (or one) as they lie in memory. load_own: of an operand that an output of the kernel may be.
 template <bool F32, bool VEC>
 struct Raw {
     uint4 q[F32 ? 2 : 1];
@@ -144,6 +144,12 @@ struct Raw {
         const uint4 *p = reinterpret_cast<const uint4 *>(row + c * (F32 ? 4 : 2));
         q[0] = __ldg(p);
         if constexpr (F32) q[1] = __ldg(p + 1);
+    }
+    __device__ __forceinline__ void load_own(const char *row, int c)
+    {
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + c * (F32 ? 4 : 2));
+        q[0] = ld_own_v4(p);
+        if constexpr (F32) q[1] = ld_own_v4(p + 1);
     }
     __device__ __forceinline__ void open(float (&v)[8]) const
     {
@@ -168,6 +174,11 @@ struct Raw<F32, false> {
     {
         if constexpr (F32) q = __ldg(reinterpret_cast<const uint32_t *>(row) + c);
         else q = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + c) << 16;
+    }
+    __device__ __forceinline__ void load_own(const char *row, int c)
+    {
+        if constexpr (F32) q = reinterpret_cast<const uint32_t *>(row)[c];
+        else q = (uint32_t)reinterpret_cast<const uint16_t *>(row)[c] << 16;
     }
     __device__ __forceinline__ void open(float (&v)[1]) const { v[0] = __uint_as_float(q); }
 };
@@ -224,15 +235,19 @@ __global__ void __launch_bounds__(kOrderThreads) combine_rows_kernel(const __gri
     }
     const int size = OF32 ? 4 : 2;
     char *out = static_cast<char *>(p.out) + t * p.ld_out * size;
+    Raw<OF32, VEC> add[C] = {};  // (all loads before the first store: add may be out)
+    if (p.add) {
+#pragma unroll
+        for (int n = 0; n < C; ++n)
+            if (c0 + n * team < p.H) add[n].load_own(static_cast<const char *>(p.add) + t * p.ld_add * size, c0 + n * team);
+    }
 #pragma unroll
     for (int n = 0; n < C; ++n) {
         const int c = c0 + n * team;
         if (c >= p.H) break;
         if (p.add) {
-            Raw<OF32, VEC> add;
             float a[W];
-            add.load(static_cast<const char *>(p.add) + t * p.ld_add * size, c);
-            add.open(a);
+            add[n].open(a);
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[n][i] += a[i];
         }
