@@ -174,7 +174,7 @@ def _launchable(stream, dev):
         current = dev
     if dev != current:
         raise ValueError(f"the tensors lie on cuda:{dev}, but cuda:{current} is the current device: make theirs current")
-    if getattr(stream, "device_index", dev) != dev:
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
         raise ValueError(f"the tensors lie on cuda:{dev}, but the stream belongs to cuda:{stream.device_index}")
 
 
