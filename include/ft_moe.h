@@ -367,9 +367,11 @@ ft_status ft_moe_swiglu_backward(const void *gu, int64_t ld_gu, const float *w, 
 /* The forward product with both operands in MXFP4: e2m1 codes, two to a byte (the even element in the low
  * half), with a power of two as scale for every 32 elements along K (the byte s + 127 for 2^s; 255 is NaN):
  *   y[p, n] = sum_b 2^(xs[p, b] + ws[e, n, b]) * sum_{k in block b} x[p, k] * w[e, n, k]
- * on the 4-bit tensor cores, which apply the scales themselves; sums are fp32. Rows, offs, workspace and
- * errors as ft_moe_group_gemm, but where offs is bad y is left as it was. Scale bytes of four neighbouring blocks (128 elements) form a word, the
- * first block's byte lowest; bytes of blocks beyond K are 0.
+ * on the 4-bit tensor cores, which apply the scales themselves; sums are fp32. Both operands are 4-bit: for models
+ * whose activations are meant to be (random ones lose some 15% of a layer's result in norm); weights made for 8-bit
+ * or bf16 activations want the other products. Rows, offs, workspace and errors as ft_moe_group_gemm, but where offs
+ * is bad y is left as it was. Scale bytes of four neighbouring blocks (128 elements) form a word, the first block's
+ * byte lowest; bytes of blocks beyond K are 0.
  *   x        device codes, rows ld_x bytes apart (a multiple of 16), 16-byte aligned
  *   x_scale  device words [ceil(K / 128)][ld_xs], one per row, ld_xs >= P and a multiple of 4, 16-byte aligned
  *   w        device codes [E, N, K / 2], contiguous, 16-byte aligned
@@ -452,8 +454,9 @@ ft_status ft_moe_combine_backward(const void *dout, int64_t ld_dout, int32_t dou
  *   total = x + residual        stored in the residual's type (total = x, not stored, without a residual)
  *   rstd  = 1 / sqrt(mean_h total^2 + eps)
  *   y     = total * rstd * (w_offset + w)
- * of the total as it is stored; fp32 inside: a row whose sum of squares fp32 does not hold (2^128) gets rstd = 0. y goes into bf16 (y), into e4m3 codes with block scales by
- * ft_moe_quantize_fp8's rule from the fp32 y (codes, scales; H a multiple of 16), or both.
+ * of the total as it is stored; fp32 inside: a row whose sum of squares fp32 does not hold (2^128) gets rstd = 0, and
+ * squares below 2^-126 lose their last bits (eps covers them where it is not 0). y goes into bf16 (y), into e4m3 codes
+ * with block scales by ft_moe_quantize_fp8's rule from the fp32 y (codes, scales; H a multiple of 16), or both.
  *   x         device bf16 rows
  *   residual, total  device rows of total_dtype (bf16 or fp32), both or neither; total may be residual itself
  *   w         device [H], bf16 or fp32 (w_dtype)

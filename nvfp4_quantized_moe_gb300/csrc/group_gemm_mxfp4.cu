@@ -12,9 +12,11 @@
 // order with the MMAs that follow it.
 //
 // What bounds it, measured on one GB300 (copy bandwidth 6.7 TB/s, cuBLAS bf16 1919 TFLOP/s):
-//   - many rows: shared memory. A stage of a wide tile (256 x 192 x 256 by a pair of CTAs) writes 31 KB to each SM's and
-//     its MMAs read 28 KB back, 470 cycles at 128 bytes each; the MMAs alone take 384 and the six copies of scales 120.
-//     8192 x 8192 x 8192 takes 150 us, 7300 TFLOP/s; 4096 x 4096 x 4096 (352 units on 76 pairs, five rounds) 28.7 us, 4800.
+//   - many rows: shared memory, by this count: a stage of a wide tile (256 x 192 x 256 by a pair of CTAs) writes 31 KB to
+//     each SM's and its MMAs read 28 KB back, 470 cycles at 128 bytes each; the MMAs alone take 384 and the six copies of
+//     scales 120. (What L2 delivers, 42 bytes a cycle and SM, may count as well: the two were not told apart.)
+//     8192 x 8192 x 8192 takes 150 us, 7300 TFLOP/s; 4096 x 4096 x 4096 (352 units on 76 pairs, five rounds) 28.7 us, 4800:
+//     18 us of it are five rounds of 16 stages, the rest was not taken apart.
 //   - skewed routing: 8192 tokens to 8 of 256 experts of 1024 x 2048 (65536 rows, 0.41 GB) 90 us, 4.6 TB/s: a round of
 //     units takes 470 cycles a stage, and 1100 more where the unit before goes through shared memory on its way out;
 //     experts' last tiles fill 256 rows by two thirds.
@@ -134,8 +136,8 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, int pair)
 }
 
 // Where a unit's tile lies: found by one warp of the CTA ahead of the others, which take it from a ring in shared memory.
-// (Finding it, a binary search over the experts and a division, takes a warp 800 cycles with one expert and up to 2000
-// with 256: done by the issuing warps themselves, the tensor cores stood still that long between two units.)
+// (The issuing warps found it themselves at first, by a binary search over the experts and a division: 800 cycles with one
+// expert and up to 2000 with 256, during which the tensor cores stood still between two units.)
 struct Unit4 {
     int e;           // expert, or -1 after the last unit
     int row0;        // first row of the tile

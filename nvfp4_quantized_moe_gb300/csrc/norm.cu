@@ -10,12 +10,13 @@
 // its sum of squares and its outputs, so that nothing is read twice; sums are fp32. The norm is that of s as it is
 // stored, so that the backward pass, which has only the stored s, is the gradient of what was computed.
 //
-// Measured on one GB300: 8192 rows of 2048 with a bf16 residual (134 MB) 25.7 us, 5.2 TB/s, where a plain copy of as
-// many bytes takes 27.7; 1999 rows of 4096 with an fp32 residual into 8 bits (90 MB) 19.5 us; backward of 8192 rows of 2048
-// (134 MB) 32.5 us, of which joining the weight's gradient is 5; one row 2.6 us. Rows that are not made of 16-byte
-// pieces go an element at a time: 8192 rows of 2047 39 us. A whole CTA per row from 257 columns on, the loads of all of
-// a thread's columns in flight: 2048 columns on 256 threads take 25.7 us, on 128 25.8, 64 31.5, 32 38.3 (one row: 2.6, 3.2,
-// 4.9, 7.5).
+// Measured on one GB300, in a captured graph over inputs larger than L2: 8192 rows of 2048 with a bf16 residual (134 MB)
+// 24.0 us, 5.6 TB/s, where a plain copy of as many bytes takes 27.7; 1999 rows of 4096 with an fp32 residual into 8 bits
+// (90 MB) 18.5 us; one row 2.4 us. Backward of 8192 rows of 2048 (134 MB) 26.1 us, 5.2 TB/s, and 32.9 with the weight's
+// gradient, whose 608 partial sums are written, read and added by a second launch; 64 rows 2.0 and 5.7. Rows that are not
+// made of 16-byte pieces go an element at a time: 8192 rows of 2047 40.7 us, backward 56. A whole CTA per row from 257
+// columns on, the loads of all of a thread's columns in flight (compared when 2048 columns on 256 threads took 25.7 us: on
+// 128 25.8, 64 31.5, 32 38.3; one row 2.6, 3.2, 4.9, 7.5).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(cta_threads(TPR), 1024 / cta_threads(TPR)) rms
 
 // dw[c] = (dw[c] +) the sum of part[i][c] over i: 32 columns per CTA, each of its 32 warps a share of the parts (all
 // loads in flight), the shares joined in order. Bound by the latency of two rounds of loads: 608 parts of 2048 columns
-// take 3 us; with eight warps a CTA they took 9.
+// take 6.7 us by themselves under a profiler, nothing in L1; with eight warps a CTA they took three times as long.
 constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps)
     norm_weight_kernel(const float *__restrict__ part, int parts, int H, float *__restrict__ dw, int accumulate)

@@ -12,8 +12,9 @@
 // row holds, a padding row) is skipped or read as zero: no value of slot or pos makes a kernel leave its arrays.
 //
 // Measured on one GB300, 8192 tokens of 2048 bf16 columns to 8 experts each (Zipf): dispatch with positions and weights
-// (302 MB, most of it written) 52.7 us, 5.7 TB/s; in 8 bits with block scales 27.8 us; combine 58 us and dispatch's
-// backward 51 us (5.8 TB/s, read); combine's backward with the weights' gradients (570 MB) 85 us, 6.7 TB/s. 64 tokens: 3 us.
+// (302 MB, most of it written) 52.7 us, 5.7 TB/s; in 8 bits with block scales 27.8 us; combine with added rows 58 us (50
+// without) and dispatch's backward 51 us (5.8 TB/s, read); combine's backward with the weights' gradients (570 MB) 85 us,
+// 6.7 TB/s. 64 tokens: 3 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -1,5 +1,5 @@
-// Building blocks of the row kernels: 16-byte loads and stores of bf16 and fp32 rows, e4m3 and e2m1 codes with
-// their block scales, the sigmoid.
+// Building blocks of the row kernels: 16-byte loads and stores of bf16 and fp32 rows, e4m3 codes with their block
+// scales, the sigmoid.
 #pragma once
 
 #include <cuda_bf16.h>
